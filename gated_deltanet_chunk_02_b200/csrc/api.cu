@@ -5,12 +5,15 @@
 // a message for gdn_last_error().  Kernels report device-side failures by
 // OR-ing bits into a per-device status word (never by trapping).
 #include <cstdio>
+#include <cmath>
 #include <cstdarg>
+#include <cstring>
 #include <string>
 
 #include "../../include/gdn.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "linear.h"
 #include "tc.h"
 
 namespace gdn {
@@ -82,10 +85,81 @@ int check_NS(int N, int mask, int S, int k) {
     return GDN_OK;
 }
 
-int launched(cudaError_t e, const char* what) {
+int launched(cudaError_t e, const char* what, int kernels = 1) {
     if (e != cudaSuccess) return cuda_fail(e, what);
-    ++t_launches;
+    t_launches += kernels;
     return GDN_OK;
+}
+
+// Small vectors (positions, lengths, slots, per-head scalars): element alignment.
+int check_vec(const void* p, size_t size, const char* name, bool optional = false) {
+    if (!p) return optional ? GDN_OK : fail(GDN_ERR_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(p) % size)
+        return fail(GDN_ERR_ALIGN, "%s is not aligned to its %d-byte elements", name, (int)size);
+    return GDN_OK;
+}
+
+// Strides of rows that are read and written 16 bytes at a time.
+int check_strides(const gdn_strides& s, gdn_dtype dt, const char* name) {
+    const int64_t vec = dt == GDN_BF16 ? 8 : 4;
+    if (s.b < 0 || s.h < 0 || s.t < 0) return fail(GDN_ERR_ARG, "%s has a negative stride", name);
+    if (s.b % vec || s.h % vec || s.t % vec)
+        return fail(GDN_ERR_ALIGN, "%s: strides are not multiples of 16 bytes", name);
+    return GDN_OK;
+}
+
+// Rows of an output may not share memory: every stride that is walked is at
+// least the extent of the dimensions inside it, in some order of the three.
+int check_out_strides(const gdn_strides& s, int64_t B, int64_t H, int64_t T, int64_t d,
+                      const char* name) {
+    int64_t st[3] = {s.b, s.h, s.t}, n[3] = {B, H, T};
+    int64_t extent = d;
+    bool used[3] = {n[0] <= 1, n[1] <= 1, n[2] <= 1};
+    for (int pass = 0; pass < 3; ++pass) {
+        int best = -1;
+        for (int i = 0; i < 3; ++i)
+            if (!used[i] && (best < 0 || st[i] < st[best])) best = i;
+        if (best < 0) break;
+        if (st[best] < extent) return fail(GDN_ERR_ARG, "%s: rows overlap", name);
+        used[best] = true;
+        extent += (n[best] - 1) * st[best];
+    }
+    return GDN_OK;
+}
+
+constexpr int64_t kMaxRows = 0x7fffffffLL;             // tokens or rows of a call
+
+int check_linear(const gdn_linear_shape& s, const int32_t* cu, gdn_dtype dtype) {
+    if (int rc = check_dtype(dtype)) return rc;
+    if (s.B < 0 || s.Hk < 0 || s.Hv < 0 || s.T < 0 || s.nseq < 0)
+        return fail(GDN_ERR_ARG, "negative B, Hk, Hv, T or nseq");
+    if (s.d != 128) return fail(GDN_ERR_UNSUPPORTED, "head dim d=%d (only 128 is built)", s.d);
+    if (s.B == 0 || s.Hv == 0) return GDN_OK;
+    if (s.Hk == 0 || s.Hv % s.Hk)
+        return fail(GDN_ERR_ARG, "Hv=%lld is not a multiple of Hk=%lld", (long long)s.Hv,
+                    (long long)s.Hk);
+    if (s.Hv > 8192) return fail(GDN_ERR_ARG, "Hv=%lld above 8192", (long long)s.Hv);
+    if (s.nseq > 0 && s.B != 1) return fail(GDN_ERR_ARG, "packed sequences need B=1");
+    if (s.T > kMaxRows || s.B > kMaxRows || s.nseq > kMaxRows ||
+        s.B * s.Hv > kMaxRows || s.nseq * s.Hv > kMaxRows || s.T * 32 > kMaxRows * 8 / s.Hv / s.B)
+        return fail(GDN_ERR_ARG, "too many rows (B=%lld, Hv=%lld, T=%lld, nseq=%lld)",
+                    (long long)s.B, (long long)s.Hv, (long long)s.T, (long long)s.nseq);
+    if (s.nseq > 0) return check_vec(cu, 4, "cu_seqlens");
+    if (cu) return fail(GDN_ERR_ARG, "cu_seqlens without nseq");
+    return GDN_OK;
+}
+
+// the packed or padded sequences of a call
+gdn::LinArgs linear_args(const gdn_linear_shape& s, const float* loggate, const int32_t* cu) {
+    gdn::LinArgs a;
+    memset(&a, 0, sizeof a);
+    a.loggate = loggate;
+    a.cu = s.nseq > 0 ? cu : nullptr;
+    a.nseq = s.nseq > 0 ? s.nseq : s.B;
+    a.B = s.B;
+    a.Hv = s.Hv;
+    a.T = s.T;
+    return a;
 }
 
 }  // namespace
@@ -414,6 +488,278 @@ int gdn_decode(const void* Q, const void* K, const void* V, const float* beta,
                     "decode");
 }
 
+int gdn_rotary_frequencies(float* inv_freq, float* mscale, int rot, double base, int scaling,
+                           double factor, int64_t original_length) {
+    if (!inv_freq || !mscale) return fail(GDN_ERR_ARG, "inv_freq or mscale is NULL");
+    if (rot < 2 || rot > 128 || rot % 2)
+        return fail(GDN_ERR_ARG, "rot=%d is not an even number in [2, 128]", rot);
+    if (!(base > 1.0) || !std::isfinite(base)) return fail(GDN_ERR_ARG, "base must be above 1");
+    if (scaling < GDN_ROTARY_PLAIN || scaling > GDN_ROTARY_YARN)
+        return fail(GDN_ERR_ARG, "unknown scaling %d", scaling);
+    if (scaling != GDN_ROTARY_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return fail(GDN_ERR_ARG, "factor must be at least 1");
+    if (scaling == GDN_ROTARY_YARN && original_length < 1)
+        return fail(GDN_ERR_ARG, "original_length must be positive");
+    if (scaling == GDN_ROTARY_NTK && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot);
+        if (scaling == GDN_ROTARY_LINEAR) f /= factor;
+        if (scaling == GDN_ROTARY_YARN) {
+            const double turns = (double)original_length * f / 6.283185307179586;
+            double keep = (turns - 1.0) / 31.0;
+            keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+            f *= keep + (1.0 - keep) / factor;
+        }
+        inv_freq[i] = (float)f;
+    }
+    *mscale = scaling == GDN_ROTARY_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return GDN_OK;
+}
+
+int gdn_rotary(const void* Q, gdn_strides qs, void* Q_out, gdn_strides qos, const void* K,
+               gdn_strides ks, void* K_out, gdn_strides kos, const int64_t* positions,
+               const float* inv_freq, float mscale, int rot, int interleaved, int inverse,
+               int64_t B, int64_t Hq, int64_t Hk, int64_t T, int32_t d, gdn_dtype dtype,
+               void* stream) {
+    GDN_TRY(check_dtype(dtype));
+    if (B < 0 || Hq < 0 || Hk < 0 || T < 0) return fail(GDN_ERR_ARG, "negative B, Hq, Hk or T");
+    if (d != 128) return fail(GDN_ERR_UNSUPPORTED, "head dim d=%d (only 128 is built)", d);
+    if (rot < 2 || rot > d || rot % 2)
+        return fail(GDN_ERR_ARG, "rot=%d is not an even number in [2, %d]", rot, d);
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+        return fail(GDN_ERR_ARG, "interleaved and inverse must be 0 or 1");
+    if (B == 0 || T == 0 || Hq + Hk == 0) return GDN_OK;
+    if (B > kMaxRows || T > kMaxRows || B * T > kMaxRows || Hq > 65536 || Hk > 65536)
+        return fail(GDN_ERR_ARG, "too many tokens or heads");
+    GDN_TRY(check_vec(positions, 8, "positions"));
+    GDN_TRY(check_vec(inv_freq, 4, "inv_freq"));
+    if (Hq > 0) {
+        GDN_TRY(check_ptrs({{Q, "Q"}, {Q_out, "Q_out"}}));
+        GDN_TRY(check_strides(qs, dtype, "Q"));
+        GDN_TRY(check_strides(qos, dtype, "Q_out"));
+        GDN_TRY(check_out_strides(qos, B, Hq, T, d, "Q_out"));
+    }
+    if (Hk > 0) {
+        GDN_TRY(check_ptrs({{K, "K"}, {K_out, "K_out"}}));
+        GDN_TRY(check_strides(ks, dtype, "K"));
+        GDN_TRY(check_strides(kos, dtype, "K_out"));
+        GDN_TRY(check_out_strides(kos, B, Hk, T, d, "K_out"));
+    }
+    gdn::RotaryArgs a;
+    memset(&a, 0, sizeof a);
+    a.Q = Q; a.qs = qs; a.Qo = Q_out; a.qos = qos;
+    a.K = K; a.ks = ks; a.Ko = K_out; a.kos = kos;
+    a.positions = positions; a.inv_freq = inv_freq; a.mscale = mscale;
+    a.rot = rot; a.interleaved = interleaved; a.inverse = inverse;
+    a.B = B; a.Hq = Hq; a.Hk = Hk; a.T = T;
+    return launched(gdn::launch_rotary(a, dtype == GDN_BF16, (cudaStream_t)stream), "rotary");
+}
+
+int64_t gdn_linear_forward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype) {
+    static const int32_t some = 0;
+    if (check_linear(s, s.nseq > 0 ? &some : nullptr, dtype) != GDN_OK) return -1;
+    if (s.B == 0 || s.Hv == 0) return 0;
+    return gdn::linear_plan(s, 1, dtype == GDN_BF16).state_bytes;
+}
+
+int gdn_linear_forward(const void* Q, const void* K, const void* V, const float* loggate,
+                       const float* S0, const int32_t* cu_seqlens, float scale, void* O,
+                       float* S_final, void* workspace, int64_t workspace_bytes,
+                       gdn_linear_shape s, gdn_dtype dtype, void* stream) {
+    GDN_TRY(check_linear(s, cu_seqlens, dtype));
+    if (s.B == 0 || s.Hv == 0) return GDN_OK;
+    if (s.T > 0) GDN_TRY(check_ptrs({{Q, "Q"}, {K, "K"}, {V, "V"}, {O, "O"}}));
+    GDN_TRY(check_vec(loggate, 4, "loggate"));
+    GDN_TRY(check_opt_ptr(S0, "S0"));
+    GDN_TRY(check_opt_ptr(S_final, "S_final"));
+    const gdn::LinPlan pl = gdn::linear_plan(s, 1, dtype == GDN_BF16);
+    if (workspace_bytes < pl.state_bytes)
+        return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
+                    (long long)workspace_bytes, (long long)pl.state_bytes);
+    if (pl.state_bytes > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
+    const int group = (int)(s.Hv / s.Hk);
+    gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
+    a.pr[0] = {Q, K, V, O, group, group, 1, 0, 0, S0, 0, S_final, scale, scale, 1.f, nullptr};
+    int kernels = 0;
+    return launched(gdn::launch_linear(a, 1, pl, dtype == GDN_BF16, workspace, &kernels,
+                                       (cudaStream_t)stream),
+                    "linear forward", kernels);
+}
+
+int64_t gdn_linear_backward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype) {
+    static const int32_t some = 0;
+    if (check_linear(s, s.nseq > 0 ? &some : nullptr, dtype) != GDN_OK) return -1;
+    if (s.B == 0 || s.Hv == 0) return 0;
+    const int64_t part = s.Hv == s.Hk ? 0 : s.B * s.Hv * s.T * (int64_t)s.d * 4;
+    return 3 * gdn::linear_plan(s, 3, dtype == GDN_BF16).state_bytes + 2 * part;
+}
+
+int gdn_linear_backward(const void* Q, const void* K, const void* V, const float* loggate,
+                        const float* S0, const void* dO, const float* dS_final,
+                        const int32_t* cu_seqlens, float scale, void* dQ, void* dK, void* dV,
+                        float* dS0, void* workspace, int64_t workspace_bytes, gdn_linear_shape s,
+                        gdn_dtype dtype, void* stream) {
+    GDN_TRY(check_linear(s, cu_seqlens, dtype));
+    if (s.B == 0 || s.Hv == 0) return GDN_OK;
+    if (s.T > 0)
+        GDN_TRY(check_ptrs({{Q, "Q"}, {K, "K"}, {V, "V"}, {dO, "dO"}, {dQ, "dQ"}, {dK, "dK"},
+                            {dV, "dV"}}));
+    GDN_TRY(check_vec(loggate, 4, "loggate"));
+    GDN_TRY(check_opt_ptr(S0, "S0"));
+    GDN_TRY(check_opt_ptr(dS_final, "dS_final"));
+    GDN_TRY(check_opt_ptr(dS0, "dS0"));
+    const int64_t need = gdn_linear_backward_workspace_bytes(s, dtype);
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
+                    (long long)workspace_bytes, (long long)need);
+    if (need > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
+    const bool bf16 = dtype == GDN_BF16;
+    const gdn::LinPlan pl = gdn::linear_plan(s, 3, bf16);
+    const int group = (int)(s.Hv / s.Hk);
+    const int64_t part = group == 1 ? 0 : s.B * s.Hv * s.T * (int64_t)s.d;
+    float* pq = (float*)((uint8_t*)workspace + 3 * pl.state_bytes);
+    float* pk = pq + part;
+    const int f32 = group > 1;
+    gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
+    a.pr[0] = {dO, V, K, f32 ? (void*)pq : dQ, 1, 1, group, 0, f32, S0, 1, nullptr,
+               scale, scale, 1.f, nullptr};
+    a.pr[1] = {V, dO, Q, f32 ? (void*)pk : dK, 1, 1, group, 1, f32, dS_final, 1, nullptr,
+               scale, 1.f, scale, nullptr};
+    a.pr[2] = {K, Q, dO, dV, group, group, 1, 1, 0, dS_final, 0, dS0, scale, 1.f, scale, nullptr};
+    cudaStream_t st = (cudaStream_t)stream;
+    int kernels = 0;
+    GDN_TRY(launched(gdn::launch_linear(a, 3, pl, bf16, workspace, &kernels, st),
+                     "linear backward", kernels));
+    if (group > 1 && s.T > 0) {
+        GDN_TRY(launched(gdn::launch_linear_group_sum(a, pq, dQ, group, bf16, st), "dQ of a group"));
+        GDN_TRY(launched(gdn::launch_linear_group_sum(a, pk, dK, group, bf16, st), "dK of a group"));
+    }
+    return GDN_OK;
+}
+
+int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* loggate, float* S,
+                      const int32_t* slots, int64_t nslots, float scale, void* O, int64_t B,
+                      int64_t Hk, int64_t Hv, int64_t n, int32_t d, gdn_dtype dtype,
+                      void* stream) {
+    GDN_TRY(check_dtype(dtype));
+    if (B < 0 || Hk < 0 || Hv < 0 || n < 0) return fail(GDN_ERR_ARG, "negative B, Hk, Hv or n");
+    if (d != 128) return fail(GDN_ERR_UNSUPPORTED, "head dim d=%d (only 128 is built)", d);
+    if (B == 0 || Hv == 0 || n == 0) return GDN_OK;
+    if (Hk == 0 || Hv % Hk)
+        return fail(GDN_ERR_ARG, "Hv=%lld is not a multiple of Hk=%lld", (long long)Hv,
+                    (long long)Hk);
+    if (B > 65535 || Hv > (1LL << 28) || n > 0x7fffffffLL)
+        return fail(GDN_ERR_ARG, "B, Hv or n too large");
+    if (nslots < (slots ? 0 : B))
+        return fail(GDN_ERR_ARG, "nslots=%lld is below %lld", (long long)nslots,
+                    (long long)(slots ? 0 : B));
+    GDN_TRY(check_ptrs({{Q, "Q"}, {K, "K"}, {V, "V"}, {S, "S"}, {O, "O"}}));
+    GDN_TRY(check_vec(loggate, 4, "loggate"));
+    GDN_TRY(check_vec(slots, 4, "slots", true));
+    return launched(gdn::launch_linear_decode(Q, K, V, loggate, S, slots, nslots, scale, O, B, Hk,
+                                              Hv, n, dtype == GDN_BF16, (cudaStream_t)stream),
+                    "linear decode");
+}
+
+static int check_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
+                      const void* R, const float* w_pre, float eps, int act, int64_t B, int64_t T,
+                      int64_t H, int64_t d, gdn_dtype dtype) {
+    GDN_TRY(check_dtype(dtype));
+    if (B < 0 || T < 0 || H < 0 || d < 0) return fail(GDN_ERR_ARG, "negative B, T, H or d");
+    if (H > 1 && d != 128)
+        return fail(GDN_ERR_UNSUPPORTED, "head dim d=%lld (only 128 is built for H > 1)",
+                    (long long)d);
+    if (d % 8) return fail(GDN_ERR_UNSUPPORTED, "width d=%lld is not a multiple of 8", (long long)d);
+    if (H > 128 || d > 16384 || H * d > 16384)
+        return fail(GDN_ERR_UNSUPPORTED, "rows of %lld x %lld channels (at most 16384)",
+                    (long long)H, (long long)d);
+    if (act != GDN_ACT_SIGMOID && act != GDN_ACT_SILU) return fail(GDN_ERR_ARG, "unknown act %d", act);
+    if (!(eps > 0.f)) return fail(GDN_ERR_ARG, "eps must be positive");
+    if (B > kMaxRows || T > kMaxRows || B * T > kMaxRows) return fail(GDN_ERR_ARG, "too many rows");
+    if (B == 0 || T == 0 || H == 0 || d == 0) return GDN_OK;
+    GDN_TRY(check_ptrs({{Y, "Y"}}));
+    GDN_TRY(check_strides(ys, dtype, "Y"));
+    GDN_TRY(check_opt_ptr(Z, "Z"));
+    GDN_TRY(check_opt_ptr(w_post, "w_post"));
+    GDN_TRY(check_opt_ptr(R, "R"));
+    return check_opt_ptr(w_pre, "w_pre");
+}
+
+int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
+                   const void* R, const float* w_pre, float scale, float eps, int act, void* X,
+                   void* N, int64_t B, int64_t T, int64_t H, int64_t d, gdn_dtype dtype,
+                   void* stream) {
+    GDN_TRY(check_norm(Y, ys, Z, w_post, R, w_pre, eps, act, B, T, H, d, dtype));
+    if (B == 0 || T == 0 || H == 0 || d == 0) return GDN_OK;
+    if (!X && !N) return fail(GDN_ERR_ARG, "X and N are both NULL");
+    if (!w_pre != !N) return fail(GDN_ERR_ARG, "w_pre and N go together");
+    GDN_TRY(check_opt_ptr(X, "X"));
+    GDN_TRY(check_opt_ptr(N, "N"));
+    gdn::NormArgs a;
+    memset(&a, 0, sizeof a);
+    a.Y = Y; a.ys = ys; a.Z = Z; a.w_post = w_post; a.R = R; a.w_pre = w_pre;
+    a.scale = scale; a.eps = eps; a.act = act; a.X = X; a.N = N;
+    a.B = B; a.T = T; a.H = H; a.d = d;
+    return launched(gdn::launch_block_norm(a, dtype == GDN_BF16, (cudaStream_t)stream),
+                    "block norm");
+}
+
+int64_t gdn_block_norm_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d) {
+    if (B < 0 || T < 0 || H < 0 || d < 0 || d % 8 || H > 128 || d > 16384 || H * d > 16384 ||
+        B > kMaxRows || T > kMaxRows || B * T > kMaxRows)
+        return -1;
+    if (B * T == 0 || H * d == 0) return 0;
+    return gdn::block_norm_ws_bytes(B * T, H * d);
+}
+
+int gdn_block_norm_backward(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
+                            const void* R, const float* w_pre, const void* dX, const void* dN,
+                            float scale, float eps, int act, void* dY, gdn_strides dys, void* dZ,
+                            void* dR, float* dw_post, float* dw_pre, void* workspace,
+                            int64_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t d,
+                            gdn_dtype dtype, void* stream) {
+    GDN_TRY(check_norm(Y, ys, Z, w_post, R, w_pre, eps, act, B, T, H, d, dtype));
+    if (!Z != !dZ) return fail(GDN_ERR_ARG, "Z and dZ go together");
+    if (!w_post != !dw_post) return fail(GDN_ERR_ARG, "w_post and dw_post go together");
+    if (!w_pre != !dw_pre || !w_pre != !dN)
+        return fail(GDN_ERR_ARG, "w_pre, dN and dw_pre go together");
+    if (!R && dR) return fail(GDN_ERR_ARG, "dR without R");
+    GDN_TRY(check_opt_ptr(dw_post, "dw_post"));
+    GDN_TRY(check_opt_ptr(dw_pre, "dw_pre"));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (B == 0 || T == 0 || H == 0 || d == 0) {        // no rows: the weights' gradients are zero
+        const size_t bytes = (size_t)(H * d) * 4;
+        for (float* w : {dw_post, dw_pre})
+            if (w && bytes) {
+                const cudaError_t e = cudaMemsetAsync(w, 0, bytes, st);
+                if (e != cudaSuccess) return cuda_fail(e, "zero weight gradients");
+            }
+        return GDN_OK;
+    }
+    if (!dX && !dN) return fail(GDN_ERR_ARG, "dX and dN are both NULL");
+    GDN_TRY(check_ptrs({{dY, "dY"}}));
+    GDN_TRY(check_strides(dys, dtype, "dY"));
+    GDN_TRY(check_out_strides(dys, B, H, T, d, "dY"));
+    GDN_TRY(check_opt_ptr(dX, "dX"));
+    GDN_TRY(check_opt_ptr(dN, "dN"));
+    GDN_TRY(check_opt_ptr(dZ, "dZ"));
+    GDN_TRY(check_opt_ptr(dR, "dR"));
+    const int64_t need = w_post || w_pre ? gdn::block_norm_ws_bytes(B * T, H * d) : 0;
+    if (workspace_bytes < need)
+        return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
+                    (long long)workspace_bytes, (long long)need);
+    if (need > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
+    gdn::NormArgs a;
+    memset(&a, 0, sizeof a);
+    a.Y = Y; a.ys = ys; a.Z = Z; a.w_post = w_post; a.R = R; a.w_pre = w_pre;
+    a.scale = scale; a.eps = eps; a.act = act; a.dX = dX; a.dN = dN;
+    a.dY = dY; a.dys = dys; a.dZ = dZ; a.dR = dR; a.dw_post = dw_post; a.dw_pre = dw_pre;
+    a.ws = (float*)workspace;
+    a.B = B; a.T = T; a.H = H; a.d = d;
+    return launched(gdn::launch_block_norm_backward(a, dtype == GDN_BF16, st),
+                    "block norm backward", w_post || w_pre ? 2 : 1);
+}
+
 int gdn_get_status(void* stream) {
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaStreamSynchronize(st);
@@ -425,6 +771,8 @@ int gdn_get_status(void* stream) {
     e = cudaMemcpyToSymbol(gdn::g_status, &z, sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e, "clear status");
     if (v & gdn::kStatusTimeout) return fail(GDN_ERR_TIMEOUT, "a bounded device wait ran out");
+    if (v & gdn::kStatusIndex)
+        return fail(GDN_ERR_ARG, "a slot or a sequence bound in device memory is out of range");
     if (v) return fail(GDN_ERR_CUDA, "device status bits 0x%x", v);
     return GDN_OK;
 }
@@ -450,6 +798,21 @@ namespace gdn {
 void record_error(int code, const char* msg) {
     (void)code;
     t_last_error = msg;
+}
+
+int sm_count() {
+    static int sms_of[64] = {0};                       // per device, looked up once
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+        (void)cudaGetLastError();
+        return 148;
+    }
+    if (sms_of[dev]) return sms_of[dev];
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 148;
+    }
+    return sms_of[dev] = n;
 }
 
 int* status_ptr() {

@@ -11,7 +11,10 @@ namespace gdn {
 // Status bits that kernels OR into the per-device status word (a device
 // pointer handed to them as an argument) instead of trapping.  Host side:
 // gdn_get_status() reads and clears the word.
-enum : int { kStatusTimeout = 1 };
+enum : int {
+    kStatusTimeout = 1,
+    kStatusIndex = 4       // a slot or a sequence bound in device memory is out of range
+};
 
 __device__ __forceinline__ void raise_status(int* status, int bits) {
     if (status) atomicOr(status, bits);

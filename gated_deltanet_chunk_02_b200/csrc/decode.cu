@@ -1,4 +1,5 @@
-// decode.cu — decode steps of the gated delta rule (gdn_decode).
+// decode.cu — decode steps of the gated delta rule (gdn_decode) and of linear
+// attention with one decay per head (gdn_linear_decode, at the end).
 //
 // "A Persistent-State Dataflow Accelerator for Memory-Bound Linear Attention
 // Decode on FPGA" (technical summary, §1-§2): generating one token touches the
@@ -152,24 +153,148 @@ void run_decode(const void* Q, const void* K, const void* V, const float* beta,
         loggate, S, static_cast<T*>(O), (int)Hk, (int)Hv, (int)n);
 }
 
+// ---- linear attention with one decay per head ----
+// S <- a S + v k^T, o = scale S q, a = exp(loggate[h]); with p = S q of the old
+// state, o = scale (a p + v (k . q)).  The mapping is k_decode's: the state is
+// moved once each way per call and nothing else counts.  Row b's state is
+// S[slots[b]]; a row with a negative slot is left alone, and so is one whose
+// slot is outside the pool or named by an earlier row, with the status word
+// set, so that no two CTAs ever write one state.
+template <typename T, int R>
+__global__ void __launch_bounds__(kDecWarps * 32)
+k_linear_decode(const T* __restrict__ Q, const T* __restrict__ K, const T* __restrict__ V,
+                const float* __restrict__ loggate, float* S, const int32_t* __restrict__ slots,
+                int64_t nslots, float scale, T* O, int Hk, int Hv, int n, int* status) {
+    constexpr int kCtaRows = kDecWarps * 4 * R;
+    constexpr int kGroups = kDh / kCtaRows;
+    const int b = blockIdx.y;
+    const int hv = blockIdx.x / kGroups;
+    const int hk = hv / (Hv / Hk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = lane & 7;
+    const int row0 = (blockIdx.x % kGroups) * kCtaRows + warp * 4 * R + (lane >> 3) * R;
+    const int64_t bh = (int64_t)b * Hv + hv;
+    const int64_t bk = (int64_t)b * Hk + hk;
+    const int64_t slot = slots ? slots[b] : b;
+    if (slot < 0) return;
+    if (slot >= nslots) {
+        if (threadIdx.x == 0) raise_status(status, kStatusIndex);
+        return;
+    }
+
+    float* Sh = S + (slot * Hv + hv) * kDh * kDh + (int64_t)row0 * kDh + 4 * sub;
+    float s[R][kSeg];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 f = *reinterpret_cast<const float4*>(Sh + r * kDh + 32 * c);
+            s[r][4 * c] = f.x; s[r][4 * c + 1] = f.y; s[r][4 * c + 2] = f.z; s[r][4 * c + 3] = f.w;
+        }
+    if (slots) {                                       // while the state is on its way
+        bool again = false;
+        for (int j = threadIdx.x; j < b; j += kDecWarps * 32) again |= slots[j] == slot;
+        if (__syncthreads_or(again)) {
+            if (threadIdx.x == 0) raise_status(status, kStatusIndex);
+            return;
+        }
+    }
+
+    const T* qp = Q + bk * n * kDh + 4 * sub;
+    const T* kp = K + bk * n * kDh + 4 * sub;
+    const T* vp = V + bh * n * kDh + row0;
+    T* op = O + bh * n * kDh + row0;
+    const float a = expf(loggate[hv]);
+
+    float kn[kSeg], qn[kSeg], vn[R];
+    ld16(kp, kn);
+    ld16(qp, qn);
+#pragma unroll
+    for (int r = 0; r < R; ++r) vn[r] = ld_elem(vp, r);
+    for (int t = 0; t < n; ++t) {
+        float k[kSeg], q[kSeg], v[R];
+#pragma unroll
+        for (int c = 0; c < kSeg; ++c) { k[c] = kn[c]; q[c] = qn[c]; }
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] = vn[r];
+        if (t + 1 < n) {                               // next token's inputs
+            const int64_t o1 = (int64_t)(t + 1) * kDh;
+            ld16(kp + o1, kn);
+            ld16(qp + o1, qn);
+#pragma unroll
+            for (int r = 0; r < R; ++r) vn[r] = ld_elem(vp, o1 + r);
+        }
+        float kq = 0.f, p[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) p[r] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kSeg; ++c) {
+            kq += k[c] * q[c];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                p[r] += s[r][c] * q[c];
+                s[r][c] = a * s[r][c] + v[r] * k[c];
+            }
+        }
+        kq = row_sum(kq);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            p[r] = row_sum(p[r]);
+            if (sub == r) st_elem(op, (int64_t)t * kDh + r, scale * (a * p[r] + v[r] * kq));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<float4*>(Sh + r * kDh + 32 * c) =
+                make_float4(s[r][4 * c], s[r][4 * c + 1], s[r][4 * c + 2], s[r][4 * c + 3]);
+}
+
+template <typename T, int R>
+void run_linear_decode(const void* Q, const void* K, const void* V, const float* loggate,
+                       float* S, const int32_t* slots, int64_t nslots, float scale, void* O,
+                       int64_t B, int64_t Hk, int64_t Hv, int64_t n, cudaStream_t st) {
+    constexpr int kGroups = kDh / (kDecWarps * 4 * R);
+    const dim3 grid((unsigned)(Hv * kGroups), (unsigned)B);
+    k_linear_decode<T, R><<<grid, kDecWarps * 32, 0, st>>>(
+        static_cast<const T*>(Q), static_cast<const T*>(K), static_cast<const T*>(V), loggate, S,
+        slots, nslots, scale, static_cast<T*>(O), (int)Hk, (int)Hv, (int)n, status_ptr());
+}
+
+// 4 CTAs per head (two state rows per lane group) once they fill the GPU twice
+bool decode_wide(int64_t B, int64_t Hv) { return B * Hv * 4 >= 2LL * sm_count(); }
+
 }  // namespace
 
 cudaError_t launch_decode(const void* Q, const void* K, const void* V, const float* beta,
                           const float* loggate, float* S, void* O, int64_t B, int64_t Hk,
                           int64_t Hv, int64_t n, bool bf16, cudaStream_t st) {
-    static int sms_of[64] = {0};                       // SM count per device, looked up once
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64) {
-        if (!sms_of[dev]) cudaDeviceGetAttribute(&sms_of[dev], cudaDevAttrMultiProcessorCount, dev);
-        if (sms_of[dev] > 0) sms = sms_of[dev];
-    }
-    const bool wide = B * Hv * 4 >= 2LL * sms;        // 4 CTAs per head fill the GPU
+    const bool wide = decode_wide(B, Hv);
     if (bf16) {
         if (wide) run_decode<__nv_bfloat16, 2>(Q, K, V, beta, loggate, S, O, B, Hk, Hv, n, st);
         else run_decode<__nv_bfloat16, 1>(Q, K, V, beta, loggate, S, O, B, Hk, Hv, n, st);
     } else {
         if (wide) run_decode<float, 2>(Q, K, V, beta, loggate, S, O, B, Hk, Hv, n, st);
         else run_decode<float, 1>(Q, K, V, beta, loggate, S, O, B, Hk, Hv, n, st);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_decode(const void* Q, const void* K, const void* V,
+                                 const float* loggate, float* S, const int32_t* slots,
+                                 int64_t nslots, float scale, void* O, int64_t B, int64_t Hk,
+                                 int64_t Hv, int64_t n, bool bf16, cudaStream_t st) {
+    const bool wide = decode_wide(B, Hv);
+    auto run = [&](auto f) {
+        f(Q, K, V, loggate, S, slots, nslots, scale, O, B, Hk, Hv, n, st);
+    };
+    if (bf16) {
+        if (wide) run(run_linear_decode<__nv_bfloat16, 2>);
+        else run(run_linear_decode<__nv_bfloat16, 1>);
+    } else {
+        if (wide) run(run_linear_decode<float, 2>);
+        else run(run_linear_decode<float, 1>);
     }
     return cudaGetLastError();
 }

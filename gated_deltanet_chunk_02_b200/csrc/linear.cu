@@ -1,0 +1,427 @@
+// linear.cu — linear attention with one decay per head: host side, the states
+// at segment boundaries, shared-head gradients, and the float32 kernel
+// (gdn_linear_forward, gdn_linear_backward).
+//
+// S_t = lambda_h S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.  Within a chunk the
+// products are dense (queries with keys, weights with values); between chunks
+// only the 128 x 128 state is carried, so the work is linear in the length.
+// A sequence's recurrence is cut into segments that run in parallel:
+//   1. the states that segments add, each from zero (k_state kernels);
+//   2. k_lin_combine: the states at the boundaries, in order;
+//   3. every segment's outputs from its incoming state.
+// One segment per sequence needs step 3 alone.  Step 1 reads keys and values
+// once more, so the cut is made only where sequences times heads leave SMs
+// idle (pick_segment).  The gradients are three recurrences of the same form
+// (linear.h) and go through the same kernels, three problems to a launch.
+#include "linear.h"
+
+namespace gdn {
+namespace {
+
+// ---- step 2: boundary states ----
+// Slot k of a sequence holds what segment k (k + 1 if reverse) adds from zero;
+// it is replaced by the state that crosses that boundary.
+__global__ void __launch_bounds__(256) k_lin_combine(const LinArgs p) {
+    const LinProblem& q = p.pr[blockIdx.z];
+    const int64_t seq = blockIdx.x / p.Hv;
+    const int hv = (int)(blockIdx.x - seq * p.Hv);
+    LinSeg g;
+    if (p.cu) {
+        // the sequence's first slot: boundaries of the sequences before it
+        const int lane = threadIdx.x & 31;
+        int64_t slots = 0, t0, n;
+        for (int64_t s = lane; s < seq; s += 32) {
+            lin_bounds(p, s, t0, n);
+            slots += lin_segments(n, p.seg_len) - 1;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) slots += __shfl_xor_sync(0xffffffffu, slots, o);
+        lin_bounds(p, seq, t0, n);
+        g.slot0 = slots;
+        g.seq_n = n;
+        g.m = (int)lin_segments(n, p.seg_len);
+    } else {
+        g.seq_n = p.T;
+        g.m = (int)lin_segments(p.T, p.seg_len);
+        g.slot0 = seq * (g.m - 1);
+    }
+    if (g.m < 2 || g.slot0 + g.m - 1 > p.bounds) return;
+    const double lg = lin_log2(p.loggate, hv);
+    const float a_full = lin_pow(lg, p.seg_len);
+    const float a_last = lin_pow(lg, g.seq_n - (g.m - 1) * p.seg_len);
+    const int e = 4 * (blockIdx.y * 256 + threadIdx.x);
+    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q.m0) {
+        const float* s = q.m0 + (seq * p.Hv + hv) * kLinState;
+        if (!q.m0_t) {
+            m = *reinterpret_cast<const float4*>(s + e);
+        } else {
+            const int r = e / kLinD, c = e % kLinD;
+            m = make_float4(s[c * kLinD + r], s[(c + 1) * kLinD + r], s[(c + 2) * kLinD + r],
+                            s[(c + 3) * kLinD + r]);
+        }
+    }
+    for (int i = 0; i < g.m - 1; ++i) {
+        const int k = q.reverse ? g.m - 2 - i : i;
+        const float a = q.reverse && i == 0 ? a_last : a_full;
+        float4* at = reinterpret_cast<float4*>(q.ws + ((g.slot0 + k) * p.Hv + hv) * kLinState + e);
+        const float4 u = *at;
+        m = make_float4(fmaf(a, m.x, u.x), fmaf(a, m.y, u.y), fmaf(a, m.z, u.z), fmaf(a, m.w, u.w));
+        *at = m;
+    }
+}
+
+// ---- gradients of shared heads: the sum over the value heads of a group ----
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_lin_group_sum(const LinArgs p, const float* part, T* out, int group) {
+    const int64_t Hk = p.Hv / group;
+    int64_t lo = 0, hi = p.T;
+    if (p.cu) {                                        // rows of no sequence stay as they were
+        lo = p.cu[0];
+        hi = p.cu[p.nseq];
+        if (lo < 0 || hi > p.T || hi < lo) return;
+    }
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, row = v >> 5;
+    const int64_t bh = row / p.T, t = row - bh * p.T, b = bh / Hk, h = bh - b * Hk;
+    const int c = 4 * (int)(v & 31);
+    if (bh >= p.B * Hk || t < lo || t >= hi) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < group; ++g) {
+        const float4 f = *reinterpret_cast<const float4*>(
+            part + ((b * p.Hv + h * group + g) * p.T + t) * kLinD + c);
+        s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
+    }
+    T* o = out + (bh * p.T + t) * kLinD + c;
+    st_elem(o, 0, s.x); st_elem(o, 1, s.y); st_elem(o, 2, s.z); st_elem(o, 3, s.w);
+}
+
+// ---- steps 1 and 3 on CUDA cores ----
+constexpr int kSimtThreads = 256;
+constexpr int kSimtC = 64;                             // rows of a chunk
+constexpr int kSimtDV = 32;                            // state rows (columns of c) per CTA
+constexpr int kPitchD = kLinD + 4;                     // an odd number of 16-byte groups
+constexpr int kPitchC = kSimtC + 4;
+
+struct SimtSmem {
+    float a[kSimtC][kPitchD];
+    float b[kSimtC][kPitchD];
+    float ct[kSimtDV][kPitchC];                        // values, transposed
+    float m[kSimtDV][kPitchD];                         // the state slice
+    float pm[kSimtC][kPitchC];                         // weights of the chunk
+    float dec[kSimtC + 1];                             // lambda^0 .. lambda^64
+};
+
+// The rows of a chunk split over 16 x 16 threads (scores) and 32 x 8 (outputs);
+// each CTA carries 32 rows of the state, so four share a head and form the
+// chunk's scores again, which costs less than passing them on: the float32
+// peak of the CUDA cores is the bound either way.
+template <typename T, bool STATE_ONLY, bool REV>
+__device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
+                             int v0, SimtSmem& s) {
+    const int tid = threadIdx.x;
+    const double lg = lin_log2(p.loggate, hv);
+    if (tid <= kSimtC) s.dec[tid] = lin_pow(lg, tid);
+    // incoming state
+    for (int e = tid; e < kSimtDV * kLinD; e += kSimtThreads) {
+        const int r = e / kLinD, c = e % kLinD;
+        float m = 0.f;
+        if (!STATE_ONLY) {
+            const bool first = REV ? g.k == g.m - 1 : g.k == 0;
+            if (!first) {
+                const int64_t slot = g.slot0 + (REV ? g.k : g.k - 1);
+                m = q.ws[(slot * p.Hv + hv) * kLinState + (v0 + r) * kLinD + c];
+            } else if (q.m0) {
+                const float* src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
+                m = q.m0_t ? src[c * kLinD + v0 + r] : src[(v0 + r) * kLinD + c];
+            }
+        }
+        s.m[r][c] = m;
+    }
+    auto base = [&](int group) {
+        const int64_t H = p.Hv / group;
+        return ((g.b * H + hv / group) * p.T + g.t0) * kLinD;
+    };
+    const T* ga = (const T*)q.a + base(q.ga);
+    const T* gb = (const T*)q.b + base(q.gb);
+    const T* gc = (const T*)q.c + base(q.gc) + v0;
+    const int64_t ob = ((g.b * p.Hv + hv) * p.T + g.t0) * kLinD + v0;
+    const int64_t nch = (g.n + kSimtC - 1) / kSimtC;
+    for (int64_t ci = 0; ci < nch; ++ci) {
+        const int64_t r0 = (REV ? nch - 1 - ci : ci) * kSimtC;
+        const int n = (int)(g.n - r0 < kSimtC ? g.n - r0 : kSimtC);
+        __syncthreads();
+        for (int e = tid; e < kSimtC * (kLinD / 4); e += kSimtThreads) {
+            const int r = e / (kLinD / 4), c = 4 * (e % (kLinD / 4));
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (r < n) {
+                const int64_t o = (r0 + r) * kLinD + c;
+                if (!STATE_ONLY)
+                    x = make_float4(ld_elem(ga, o), ld_elem(ga, o + 1), ld_elem(ga, o + 2),
+                                    ld_elem(ga, o + 3));
+                y = make_float4(ld_elem(gb, o), ld_elem(gb, o + 1), ld_elem(gb, o + 2),
+                                ld_elem(gb, o + 3));
+            }
+            if (!STATE_ONLY) *reinterpret_cast<float4*>(&s.a[r][c]) = x;
+            *reinterpret_cast<float4*>(&s.b[r][c]) = y;
+        }
+        for (int e = tid; e < kSimtC * kSimtDV; e += kSimtThreads) {
+            const int r = e / kSimtDV, c = e % kSimtDV;
+            s.ct[c][r] = r < n ? ld_elem(gc, (r0 + r) * kLinD + c) : 0.f;
+        }
+        __syncthreads();
+        if (!STATE_ONLY) {
+            {   // weights: rows ti + 16 u, columns tj + 16 w; blocks off the causal side are zero
+                const int ti = tid >> 4, tj = tid & 15;
+                float acc[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) acc[u][w] = 0.f;
+#pragma unroll 2
+                for (int k = 0; k < kLinD; k += 4) {
+                    float4 x[4], y[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        x[u] = *reinterpret_cast<const float4*>(&s.a[ti + 16 * u][k]);
+                        y[u] = *reinterpret_cast<const float4*>(&s.b[tj + 16 * u][k]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            if (REV ? w >= u : w <= u) {
+                                acc[u][w] = fmaf(x[u].x, y[w].x, acc[u][w]);
+                                acc[u][w] = fmaf(x[u].y, y[w].y, acc[u][w]);
+                                acc[u][w] = fmaf(x[u].z, y[w].z, acc[u][w]);
+                                acc[u][w] = fmaf(x[u].w, y[w].w, acc[u][w]);
+                            }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int i = ti + 16 * u, j = tj + 16 * w, dist = REV ? j - i : i - j;
+                        s.pm[i][j] = dist >= 0 ? q.s_intra * s.dec[dist] * acc[u][w] : 0.f;
+                    }
+            }
+            __syncthreads();
+            {   // outputs: rows ri, ri + 32, columns cj + 8 w
+                const int ri = tid >> 3, cj = tid & 7;
+                float in[2][4], st[2][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) in[u][w] = st[u][w] = 0.f;
+#pragma unroll 2
+                for (int k = 0; k < kLinD; k += 4) {
+                    float4 x[2], y[4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        x[u] = *reinterpret_cast<const float4*>(&s.a[ri + 32 * u][k]);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        y[w] = *reinterpret_cast<const float4*>(&s.m[cj + 8 * w][k]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            st[u][w] = fmaf(x[u].x, y[w].x, st[u][w]);
+                            st[u][w] = fmaf(x[u].y, y[w].y, st[u][w]);
+                            st[u][w] = fmaf(x[u].z, y[w].z, st[u][w]);
+                            st[u][w] = fmaf(x[u].w, y[w].w, st[u][w]);
+                        }
+                }
+#pragma unroll 2
+                for (int k = 0; k < kSimtC; k += 4) {
+                    float4 x[2], y[4];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        x[u] = *reinterpret_cast<const float4*>(&s.pm[ri + 32 * u][k]);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        y[w] = *reinterpret_cast<const float4*>(&s.ct[cj + 8 * w][k]);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            in[u][w] = fmaf(x[u].x, y[w].x, in[u][w]);
+                            in[u][w] = fmaf(x[u].y, y[w].y, in[u][w]);
+                            in[u][w] = fmaf(x[u].z, y[w].z, in[u][w]);
+                            in[u][w] = fmaf(x[u].w, y[w].w, in[u][w]);
+                        }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int i = ri + 32 * u;
+                    if (i >= n) continue;
+                    const float d = q.s_inter * (REV ? s.dec[n - 1 - i] : s.dec[i + 1]);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float o = fmaf(d, st[u][w], in[u][w]);
+                        const int64_t at = ob + (r0 + i) * kLinD + cj + 8 * w;
+                        if (q.out_f32) static_cast<float*>(q.out)[at] = o;
+                        else st_elem(static_cast<T*>(q.out), at, o);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        {   // state: rows cr + 8 u (values), columns 4 kc .. 4 kc + 3 (keys)
+            const int cr = tid >> 5, kc = 4 * (tid & 31);
+            float4 acc[4];
+            const float an = s.dec[n];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int j = 0; j < kSimtC; j += 4) {
+                float4 x[4], y[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    x[u] = *reinterpret_cast<const float4*>(&s.ct[cr + 8 * u][j]);
+                    y[u] = *reinterpret_cast<const float4*>(&s.b[j + u][kc]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int jj = j + e;
+                    const float w = jj < n ? q.s_state * (REV ? s.dec[jj + 1] : s.dec[n - 1 - jj])
+                                           : 0.f;
+                    y[e].x *= w; y[e].y *= w; y[e].z *= w; y[e].w *= w;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float xe[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        acc[u].x = fmaf(xe[e], y[e].x, acc[u].x);
+                        acc[u].y = fmaf(xe[e], y[e].y, acc[u].y);
+                        acc[u].z = fmaf(xe[e], y[e].z, acc[u].z);
+                        acc[u].w = fmaf(xe[e], y[e].w, acc[u].w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float4* m = reinterpret_cast<float4*>(&s.m[cr + 8 * u][kc]);
+                const float4 o = *m;
+                *m = make_float4(fmaf(an, o.x, acc[u].x), fmaf(an, o.y, acc[u].y),
+                                 fmaf(an, o.z, acc[u].z), fmaf(an, o.w, acc[u].w));
+            }
+        }
+    }
+    __syncthreads();
+    float* dst = nullptr;
+    if (STATE_ONLY)
+        dst = q.ws + ((g.slot0 + (REV ? g.k - 1 : g.k)) * p.Hv + hv) * kLinState;
+    else if (q.mout && (REV ? g.k == 0 : g.k == g.m - 1))
+        dst = q.mout + (g.seq * p.Hv + hv) * kLinState;
+    if (dst)
+        for (int e = tid; e < kSimtDV * kLinD; e += kSimtThreads)
+            dst[v0 * kLinD + e] = s.m[e / kLinD][e % kLinD];
+}
+
+// grid: (segments or boundaries, 4 Hv, problems)
+template <typename T, bool STATE_ONLY>
+__global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    SimtSmem& s = *reinterpret_cast<SimtSmem*>(raw);
+    const LinProblem& q = p.pr[blockIdx.z];
+    LinSeg g = lin_find(p, blockIdx.x, STATE_ONLY ? 1 : 0);
+    if (!g.ok) return;
+    const int hv = blockIdx.y >> 2, v0 = (blockIdx.y & 3) * kSimtDV;
+    if (STATE_ONLY && q.reverse) {                     // boundary k: what segment k + 1 adds
+        g.k += 1;
+        g.t0 = g.seq_t0 + g.k * p.seg_len;
+        g.n = g.seq_n - g.k * p.seg_len < p.seg_len ? g.seq_n - g.k * p.seg_len : p.seg_len;
+    }
+    if (q.reverse) simt_segment<T, STATE_ONLY, true>(p, q, g, hv, v0, s);
+    else simt_segment<T, STATE_ONLY, false>(p, q, g, hv, v0, s);
+}
+
+template <typename T>
+cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t bounds, bool states,
+                     cudaStream_t st) {
+    const int smem = (int)sizeof(SimtSmem);
+    if (states) {
+        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<T, true>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        k_linear_simt<T, true><<<dim3((unsigned)bounds, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
+                                 smem, st>>>(a);
+    } else {
+        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<T, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        k_linear_simt<T, false><<<dim3((unsigned)segs, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
+                                  smem, st>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+// Segment length (a multiple of 128): one segment per sequence when that fills
+// the GPU, else as many as bring the two passes' steps down.  A step is a
+// chunk of 128 rows on one SM (CTA); the state pass costs about half of an
+// output step, and cutting at all costs two launches and the states' traffic,
+// about four steps.
+int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int ctas_per_head) {
+    const int64_t chunks = (rows + 127) / 128, sms = sm_count();
+    const int64_t lines = nprob * nseq * Hv * ctas_per_head;
+    int64_t best = chunks, cost = INT64_MAX;
+    for (int64_t m = 1; m <= chunks && m <= 64; ++m) {
+        const int64_t len = (chunks + m - 1) / m;
+        const int64_t waves = (lines * m + sms - 1) / sms, waves1 = (lines * (m - 1) + sms - 1) / sms;
+        const int64_t c = 2 * waves * len + (m > 1 ? waves1 * len + 8 : 0);
+        if (c < cost) { cost = c; best = len; }
+    }
+    return best < 1 ? 128 : 128 * best;
+}
+
+}  // namespace
+
+LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16) {
+    LinPlan pl;
+    const bool packed = s.nseq > 0;
+    (void)bf16;
+    pl.seg_len = pick_segment(nprob, packed ? 1 : s.B, s.Hv, s.T, 4);
+    // boundaries: a sequence of n rows has at most n / seg_len
+    const int64_t m = s.T <= pl.seg_len ? 1 : (s.T + pl.seg_len - 1) / pl.seg_len;
+    pl.bounds = packed ? (s.T <= pl.seg_len ? 0 : s.T / pl.seg_len) : s.B * (m - 1);
+    pl.segs = packed ? s.nseq + pl.bounds : s.B * m;
+    pl.state_bytes = pl.bounds * s.Hv * kLinState * 4;
+    return pl;
+}
+
+cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool bf16, void* ws,
+                          int* launches, cudaStream_t st) {
+    LinArgs a = a0;
+    a.seg_len = pl.seg_len;
+    a.bounds = pl.bounds;
+    a.status = status_ptr();
+    for (int i = 0; i < nprob; ++i) a.pr[i].ws = (float*)((uint8_t*)ws + i * pl.state_bytes);
+    cudaError_t e;
+    if (pl.bounds > 0) {
+        e = bf16 ? run_simt<__nv_bfloat16>(a, nprob, pl.segs, pl.bounds, true, st)
+                 : run_simt<float>(a, nprob, pl.segs, pl.bounds, true, st);
+        if (e != cudaSuccess) return e;
+        k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), kLinState / 1024, nprob), 256, 0, st>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        *launches += 2;
+    }
+    e = bf16 ? run_simt<__nv_bfloat16>(a, nprob, pl.segs, pl.bounds, false, st)
+             : run_simt<float>(a, nprob, pl.segs, pl.bounds, false, st);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+cudaError_t launch_linear_group_sum(const LinArgs& a, const float* part, void* out, int group,
+                                    bool bf16, cudaStream_t st) {
+    const unsigned grid = (unsigned)((a.B * (a.Hv / group) * a.T * (kLinD / 4) + 255) / 256);
+    if (bf16)
+        k_lin_group_sum<<<grid, 256, 0, st>>>(a, part, (__nv_bfloat16*)out, group);
+    else
+        k_lin_group_sum<<<grid, 256, 0, st>>>(a, part, (float*)out, group);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

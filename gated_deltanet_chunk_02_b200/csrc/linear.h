@@ -1,0 +1,160 @@
+// linear.h — internal structures of linear attention with a decay per head
+// (linear.cu: host side and CUDA-core kernels; linear_tc.cu: tcgen05 kernels).
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gdn {
+
+constexpr int kLinD = 128;                             // head dim
+constexpr int kLinState = kLinD * kLinD;               // floats of one state
+
+// One decayed linear attention.  With queries a, keys b, values c of one head
+// and lambda = exp(loggate):
+//   forward:  out_i = s_intra sum_{j<=i} lambda^(i-j) (a_i.b_j) c_j + s_inter lambda^(i+1) M a_i
+//             M'    = lambda^n M + s_state sum_j lambda^(n-1-j) c_j b_j^T
+//   reverse:  out_i = s_intra sum_{j>=i} lambda^(j-i) (a_i.b_j) c_j + s_inter lambda^(n-1-i) M a_i
+//             M'    = lambda^n M + s_state sum_j lambda^(j+1) c_j b_j^T
+// over n rows whose incoming state is M (entering at the first row, or at the
+// last one if reverse).  The forward pass is (a, b, c) = (q, k, v); the
+// gradients are three more: dq from (do, v, k), and in reverse dk from
+// (v, do, q) and dv from (k, q, do).
+struct LinProblem {
+    const void* a; const void* b; const void* c;
+    void* out;
+    int ga, gb, gc;            // value heads per head of a, b, c
+    int reverse;
+    int out_f32;               // out is float32 whatever the data type
+    const float* m0; int m0_t; // incoming state of each sequence (or null); transposed
+    float* mout;               // outgoing state of each sequence (or null)
+    float s_intra, s_inter, s_state;
+    float* ws;                 // states at the segment boundaries [boundary][Hv][128][128]
+};
+constexpr int kLinProblems = 3;
+
+// Sequences are cut into segments of seg_len rows that run in parallel, each
+// from the state at its boundary.
+struct LinArgs {
+    LinProblem pr[kLinProblems];
+    const float* loggate;      // [Hv]
+    const int32_t* cu;         // packed: [nseq + 1], else null
+    int64_t nseq;              // sequences
+    int64_t B, Hv, T;
+    int64_t seg_len;           // a multiple of 128
+    int64_t bounds;            // boundary slots in a problem's ws
+    int* status;
+};
+
+// rows [t0, t0 + n) of batch row b: one segment, number k of m of its sequence
+struct LinSeg {
+    int64_t seq, b, t0, n;
+    int k, m;
+    int64_t slot0;             // boundary slot between segments 0 and 1 of the sequence
+    int64_t seq_t0, seq_n;
+    bool ok;
+};
+
+__device__ __forceinline__ int64_t lin_segments(int64_t n, int64_t seg_len) {
+    return n <= seg_len ? 1 : (n + seg_len - 1) / seg_len;
+}
+__device__ __forceinline__ void lin_bounds(const LinArgs& p, int64_t s, int64_t& t0, int64_t& n) {
+    const int64_t lo = p.cu[s], hi = p.cu[s + 1];
+    if (lo < 0 || hi < lo || hi > p.T) {               // bad bounds: no rows, and the status word
+        raise_status(p.status, kStatusIndex);
+        t0 = 0;
+        n = 0;
+    } else {
+        t0 = lo;
+        n = hi - lo;
+    }
+}
+// The idx-th segment (sub = 0), or the idx-th boundary (sub = 1: boundary k of
+// a sequence lies between its segments k and k + 1).  Called by whole warps;
+// packed sequences are counted 32 at a time.
+__device__ __forceinline__ LinSeg lin_find(const LinArgs& p, int64_t idx, int sub) {
+    LinSeg g;
+    g.ok = false;
+    if (!p.cu) {
+        const int64_t m = lin_segments(p.T, p.seg_len), per = m - sub;
+        if (per <= 0 || idx >= per * p.nseq) return g;
+        g.seq = idx / per;
+        g.k = (int)(idx - g.seq * per);
+        g.m = (int)m;
+        g.b = g.seq;
+        g.seq_t0 = 0;
+        g.seq_n = p.T;
+        g.slot0 = g.seq * (m - 1);
+    } else {
+        const int lane = threadIdx.x & 31;
+        int64_t before = 0, slots = 0;
+        bool found = false;
+        for (int64_t s0 = 0; s0 < p.nseq && !found; s0 += 32) {
+            int64_t t0 = 0, n = 0, m = 0;
+            if (s0 + lane < p.nseq) {
+                lin_bounds(p, s0 + lane, t0, n);
+                m = lin_segments(n, p.seg_len);
+            }
+            const int64_t mine = m ? m - sub : 0;
+            int64_t inc = mine, sinc = m ? m - 1 : 0;  // inclusive sums over the lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t a = __shfl_up_sync(0xffffffffu, inc, o);
+                const int64_t b = __shfl_up_sync(0xffffffffu, sinc, o);
+                if (lane >= o) { inc += a; sinc += b; }
+            }
+            const unsigned hit = __ballot_sync(
+                0xffffffffu, mine > 0 && idx < before + inc && idx >= before + inc - mine);
+            if (hit) {
+                const int w = __ffs(hit) - 1;
+                g.seq = s0 + w;
+                g.k = (int)(idx - before - __shfl_sync(0xffffffffu, inc - mine, w));
+                g.m = (int)__shfl_sync(0xffffffffu, m, w);
+                g.seq_t0 = __shfl_sync(0xffffffffu, t0, w);
+                g.seq_n = __shfl_sync(0xffffffffu, n, w);
+                g.slot0 = slots + __shfl_sync(0xffffffffu, sinc - (m ? m - 1 : 0), w);
+                found = true;
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
+            slots += __shfl_sync(0xffffffffu, sinc, 31);
+        }
+        if (!found) return g;
+        g.b = 0;
+    }
+    g.t0 = g.seq_t0 + g.k * p.seg_len;
+    g.n = g.seq_n - g.k * p.seg_len;
+    if (g.n > p.seg_len) g.n = p.seg_len;
+    if (g.slot0 + g.m - 1 > p.bounds) {                // only sequences that overlap need more
+        raise_status(p.status, kStatusIndex);
+        return g;
+    }
+    g.ok = true;
+    return g;
+}
+
+// How a call is cut: the same for its workspace size and its launches.
+struct LinPlan {
+    int64_t seg_len, segs, bounds;                     // upper bounds of the counts if packed
+    int64_t state_bytes;                               // boundary states of one problem
+};
+LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16);
+// ws: nprob * state_bytes; *launches counts the kernels
+cudaError_t launch_linear(const LinArgs& a, int nprob, const LinPlan& pl, bool bf16, void* ws,
+                          int* launches, cudaStream_t st);
+// out[b, h] = sum of part[b, h * group + g] over g, float32 -> the data type
+cudaError_t launch_linear_group_sum(const LinArgs& a, const float* part, void* out, int group,
+                                    bool bf16, cudaStream_t st);
+
+// log2 of the decay; -inf (no memory at all) becomes a finite number whose
+// product with a distance of zero is zero
+__device__ __forceinline__ double lin_log2(const float* loggate, int hv) {
+    return fmax((double)loggate[hv] * 1.4426950408889634, -1e30);
+}
+// lambda^n: the exponent in binary64 and its fraction alone to exp2f, so that
+// the error stays at exp2f's two units however far n reaches
+__device__ __forceinline__ float lin_pow(double lg, int64_t n) {
+    const double x = lg * (double)n, i = rint(x);
+    return ldexpf(exp2f((float)(x - i)), (int)fmin(fmax(i, -1000.0), 1000.0));
+}
+
+}  // namespace gdn

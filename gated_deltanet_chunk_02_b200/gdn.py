@@ -31,12 +31,27 @@ EXPORTS = [
     "gdn_forward_workspace_bytes", "gdn_forward_static", "gdn_decode", "gdn_get_status",
     "gdn_last_error", "gdn_launch_count", "gdn_debug_arm_wait_expiry", "gdn_forward_raw",
     "gdn_forward_raw_workspace_bytes",
+    "gdn_rotary_frequencies", "gdn_rotary", "gdn_linear_forward",
+    "gdn_linear_forward_workspace_bytes", "gdn_linear_backward",
+    "gdn_linear_backward_workspace_bytes", "gdn_linear_decode", "gdn_block_norm",
+    "gdn_block_norm_backward", "gdn_block_norm_backward_workspace_bytes",
 ]
+GDN_ACT = {"sigmoid": 0, "silu": 1}
+GDN_ROTARY = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
 class GdnShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("T", ctypes.c_int64),
                 ("k", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class GdnStrides(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class GdnLinearShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
+                ("T", ctypes.c_int64), ("nseq", ctypes.c_int64), ("d", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -62,6 +77,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                        "`python -m gated_deltanet_chunk_02_b200.build`")
     lib = ctypes.CDLL(path)
     S = GdnShape
+    X, L = GdnStrides, GdnLinearShape
+    F = ctypes.c_float
     sig = {
         "gdn_build_A": [_P, _P, _P, _P, S, _I, _P],
         "gdn_invert_neumann": [_P, _P, S, _I, _I, _I, _I, _P],
@@ -83,6 +100,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gdn_forward_static": [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, S, _I, _P],
         "gdn_decode": [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, ctypes.c_int32, _I,
                        _P],
+        "gdn_rotary_frequencies": [_P, _P, _I, ctypes.c_double, _I, ctypes.c_double, _I64],
+        "gdn_rotary": [_P, X, _P, X, _P, X, _P, X, _P, _P, F, _I, _I, _I, _I64, _I64, _I64, _I64,
+                       ctypes.c_int32, _I, _P],
+        "gdn_linear_forward": [_P, _P, _P, _P, _P, _P, F, _P, _P, _P, _I64, L, _I, _P],
+        "gdn_linear_forward_workspace_bytes": [L, _I],
+        "gdn_linear_backward": [_P, _P, _P, _P, _P, _P, _P, _P, F, _P, _P, _P, _P, _P, _I64, L, _I,
+                                _P],
+        "gdn_linear_backward_workspace_bytes": [L, _I],
+        "gdn_linear_decode": [_P, _P, _P, _P, _P, _P, _I64, F, _P, _I64, _I64, _I64, _I64,
+                              ctypes.c_int32, _I, _P],
+        "gdn_block_norm": [_P, X, _P, _P, _P, _P, F, F, _I, _P, _P, _I64, _I64, _I64, _I64, _I,
+                           _P],
+        "gdn_block_norm_backward": [_P, X, _P, _P, _P, _P, _P, _P, F, F, _I, _P, X, _P, _P, _P, _P,
+                                    _P, _I64, _I64, _I64, _I64, _I64, _I, _P],
+        "gdn_block_norm_backward_workspace_bytes": [_I64, _I64, _I64, _I64],
         "gdn_get_status": [_P],
         "gdn_debug_arm_wait_expiry": [_I, _I, ctypes.c_double],
         "gdn_last_error": [],
@@ -94,6 +126,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         f.restype = _I
     lib.gdn_forward_workspace_bytes.restype = _I64
     lib.gdn_forward_raw_workspace_bytes.restype = _I64
+    for name in ("gdn_linear_forward_workspace_bytes", "gdn_linear_backward_workspace_bytes",
+                 "gdn_block_norm_backward_workspace_bytes"):
+        getattr(lib, name).restype = _I64
     lib.gdn_launch_count.restype = _I64
     lib.gdn_last_error.restype = ctypes.c_char_p
     _lib = lib
@@ -278,6 +313,241 @@ def gdn_decode(Q, K, V, beta, loggate, S, O, stream=None):
     Hv = V.shape[1]
     _check(load().gdn_decode(_ptr(Q), _ptr(K), _ptr(V), _ptr(beta), _ptr(loggate), _ptr(S),
                              _ptr(O), B, Hk, Hv, n, d, _dtype(K), _stream(stream)))
+
+
+class _Call:
+    """Checks of one call's tensors: shapes, types, one CUDA device (made
+    current for the launch) and the stream on it."""
+
+    def __init__(self, stream, first):
+        if not isinstance(first, torch.Tensor):
+            raise TypeError("expected a torch tensor")
+        self.device, self.stream = first.device, stream
+
+    def check(self, t, name, shape=None, dtype=None, strided=False):
+        """The data pointer of ``t`` (None passes as NULL)."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: libgdn takes CUDA tensors")
+        if strided:
+            if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+                raise ValueError(f"{name}: the last dimension is not contiguous")
+        elif not t.is_contiguous():
+            raise ValueError(f"{name}: libgdn takes contiguous tensors")
+        return ctypes.c_void_p(t.data_ptr())
+
+    def run(self, name, *args):
+        """The C call on the tensors' device and its current (or the given) stream."""
+        if self.stream is not None and self.stream.device != self.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+        with torch.cuda.device(self.device):
+            _check(getattr(load(), name)(*args, _stream(self.stream)))
+
+
+def _strides(t, b, h, tok):
+    """Element strides of the named dimensions (0 where nothing is walked)."""
+    at = [t.stride(i) if t.shape[i] > 1 else 0 for i in (b, h, tok)]
+    return GdnStrides(*at)
+
+
+def _apart(outs, ins):
+    """Outputs share no memory with inputs or one another (contiguous tensors)."""
+    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+    outs = [(n, t) for n, t in outs if t is not None and t.numel()]
+    rest = [(n, t) for n, t in ins if t is not None and t.numel()]
+    for i, (n, t) in enumerate(outs):
+        a0, a1 = span(t)
+        for m, u in outs[i + 1:] + rest:
+            b0, b1 = span(u)
+            if a0 < b1 and b0 < a1:
+                raise ValueError(f"{n} shares memory with {m}")
+
+
+def gdn_rotary_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, original_length=0):
+    """Frequencies of ``rot / 2`` rotated pairs (CPU float32 tensor) and the
+    factor on sines and cosines; ``scaling``: plain, linear, ntk or yarn."""
+    inv = torch.empty(max(0, rot // 2), dtype=torch.float32)
+    m = ctypes.c_float()
+    _check(load().gdn_rotary_frequencies(ctypes.c_void_p(inv.data_ptr()), ctypes.byref(m), rot,
+                                         float(base), GDN_ROTARY[scaling], float(factor),
+                                         int(original_length)))
+    return inv, m.value
+
+
+def gdn_rotary(Q, K, positions, inv_freq, Q_out, K_out, mscale=1.0, interleaved=False,
+               inverse=False, stream=None):
+    """Rotary positions on the first ``2 * len(inv_freq)`` columns of Q
+    ``[B, Hq, T, d]`` and K ``[B, Hk, T, d]`` (either may be None; views of any
+    strides with contiguous rows) at ``positions`` int64 ``[B, T]``; outputs may
+    be the inputs.  ``inverse`` turns back: the gradient."""
+    given = Q if Q is not None else K
+    c = _Call(stream, given)
+    B, _, T, d = given.shape
+    ptr, strides, heads = [], [], []
+    for x, y, name in ((Q, Q_out, "Q"), (K, K_out, "K")):
+        if x is None:
+            ptr += [None, None]
+            strides += [GdnStrides(), GdnStrides()]
+            heads.append(0)
+            continue
+        if y is None:
+            raise TypeError(f"{name}_out: expected a torch tensor")
+        H = x.shape[1]
+        ptr += [c.check(x, name, (B, H, T, d), given.dtype, strided=True),
+                c.check(y, name + "_out", (B, H, T, d), given.dtype, strided=True)]
+        strides += [_strides(x, 0, 1, 2), _strides(y, 0, 1, 2)]
+        heads.append(H)
+    c.run("gdn_rotary", ptr[0], strides[0], ptr[1], strides[1], ptr[2], strides[2], ptr[3],
+          strides[3], c.check(positions, "positions", (B, T), torch.int64),
+          c.check(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32), mscale,
+          2 * inv_freq.numel(), int(interleaved), int(inverse), B, heads[0], heads[1], T, d,
+          _dtype(given))
+
+
+def _linear_shape(K, V, cu_seqlens):
+    B, Hk, T, d = K.shape
+    return GdnLinearShape(B, Hk, V.shape[1], T,
+                          0 if cu_seqlens is None else cu_seqlens.numel() - 1, d)
+
+
+def _workspace(fn, *args):
+    n = int(fn(*args))
+    if n < 0:
+        raise GdnError(GDN_ERR_ARG, gdn_last_error())
+    return n
+
+
+def gdn_linear_forward_workspace_bytes(K, V, cu_seqlens=None):
+    """Scratch bytes ``gdn_linear_forward`` needs for these shapes and dtype."""
+    with torch.cuda.device(K.device):
+        return _workspace(load().gdn_linear_forward_workspace_bytes,
+                          _linear_shape(K, V, cu_seqlens), _dtype(K))
+
+
+def gdn_linear_backward_workspace_bytes(K, V, cu_seqlens=None):
+    """Scratch bytes ``gdn_linear_backward`` needs for these shapes and dtype."""
+    with torch.cuda.device(K.device):
+        return _workspace(load().gdn_linear_backward_workspace_bytes,
+                          _linear_shape(K, V, cu_seqlens), _dtype(K))
+
+
+def _linear_inputs(c, Q, K, V, loggate, cu_seqlens):
+    """Checked pointers of Q, K, V, loggate, cu_seqlens and the shapes of a
+    tensor over value heads and of the states."""
+    B, Hk, T, d = K.shape
+    Hv = V.shape[1]
+    n = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens: expected [nseq + 1] bounds")
+        n = cu_seqlens.numel() - 1
+    rows, states = (B, Hv, T, d), (n, Hv, d, d)
+    return ([c.check(Q, "Q", K.shape, K.dtype), c.check(K, "K"), c.check(V, "V", rows, K.dtype),
+             c.check(loggate, "loggate", (Hv,), torch.float32),
+             c.check(cu_seqlens, "cu_seqlens", None, torch.int32)], rows, states)
+
+
+def gdn_linear_forward(Q, K, V, loggate, S0, O, S_final, workspace, scale=1.0, cu_seqlens=None,
+                       stream=None):
+    """Linear attention with a decay per head, o_t = scale S_t q_t with S_t =
+    e^loggate S_{t-1} + v_t k_t^T: Q, K ``[B, Hk, T, d]``, V, O ``[B, Hv, T, d]``,
+    loggate float32 ``[Hv]``, S0 (or None) and S_final (or None) float32
+    ``[n, Hv, d, d]``; n = B, or with ``cu_seqlens`` (int32 ``[n + 1]``, B = 1)
+    the number of packed sequences."""
+    _apart([("O", O), ("S_final", S_final), ("workspace", workspace)],
+           [("Q", Q), ("K", K), ("V", V), ("S0", S0), ("loggate", loggate),
+            ("cu_seqlens", cu_seqlens)])
+    c = _Call(stream, K)
+    (q, k, v, lg, cu), rows, states = _linear_inputs(c, Q, K, V, loggate, cu_seqlens)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    c.run("gdn_linear_forward", q, k, v, lg, c.check(S0, "S0", states, torch.float32), cu, scale,
+          c.check(O, "O", rows, K.dtype), c.check(S_final, "S_final", states, torch.float32),
+          c.check(workspace, "workspace"), ws, _linear_shape(K, V, cu_seqlens), _dtype(K))
+
+
+def gdn_linear_backward(Q, K, V, loggate, S0, dO, dS_final, dQ, dK, dV, dS0, workspace, scale=1.0,
+                        cu_seqlens=None, stream=None):
+    """Gradients of ``gdn_linear_forward`` for dO and dS_final (or None): dQ, dK
+    (summed over the value heads that share them), dV, and dS0 (or None)."""
+    _apart([("dQ", dQ), ("dK", dK), ("dV", dV), ("dS0", dS0), ("workspace", workspace)],
+           [("Q", Q), ("K", K), ("V", V), ("S0", S0), ("dO", dO), ("dS_final", dS_final),
+            ("loggate", loggate), ("cu_seqlens", cu_seqlens)])
+    c = _Call(stream, K)
+    (q, k, v, lg, cu), rows, states = _linear_inputs(c, Q, K, V, loggate, cu_seqlens)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lambda t, name: c.check(t, name, states, torch.float32)
+    c.run("gdn_linear_backward", q, k, v, lg, st(S0, "S0"), c.check(dO, "dO", rows, K.dtype),
+          st(dS_final, "dS_final"), cu, scale, c.check(dQ, "dQ", K.shape, K.dtype),
+          c.check(dK, "dK", K.shape, K.dtype), c.check(dV, "dV", rows, K.dtype), st(dS0, "dS0"),
+          c.check(workspace, "workspace"), ws, _linear_shape(K, V, cu_seqlens), _dtype(K))
+
+
+def gdn_linear_decode(Q, K, V, loggate, S, O, slots=None, scale=1.0, stream=None):
+    """n tokens of the same recurrence: Q, K ``[B, Hk, n, d]``, V, O
+    ``[B, Hv, n, d]``, loggate float32 ``[Hv]``; states S float32 ``[slots, Hv, d, d]``
+    in place, row b using ``S[slots[b]]`` (int32 ``[B]``; negative: the row is left
+    out), or ``S[b]`` without slots."""
+    c = _Call(stream, K)
+    B, Hk, n, d = K.shape
+    Hv = V.shape[1]
+    _apart([("O", O), ("S", S)], [("Q", Q), ("K", K), ("V", V), ("loggate", loggate),
+                                  ("slots", slots)])
+    c.run("gdn_linear_decode", c.check(Q, "Q", K.shape, K.dtype), c.check(K, "K"),
+          c.check(V, "V", (B, Hv, n, d), K.dtype),
+          c.check(loggate, "loggate", (Hv,), torch.float32),
+          c.check(S, "S", (S.shape[0], Hv, d, d), torch.float32),
+          c.check(slots, "slots", (B,), torch.int32), S.shape[0], scale,
+          c.check(O, "O", (B, Hv, n, d), K.dtype), B, Hk, Hv, n, d, _dtype(K))
+
+
+def gdn_block_norm(Y, Z, w_post, R, w_pre, X, N, scale=1.0, eps=1e-6, act="silu", stream=None):
+    """x = R + scale act(Z) w_post norm(Y) and N = w_pre norm(x): Y ``[B, T, H, d]``
+    (a view of any strides with contiguous channels, normalised over d), the
+    others ``[B, T, H * d]``, weights float32 ``[H * d]``.  w_post, Z, R, and
+    w_pre with N may be None (left out); X may be R, or None."""
+    c = _Call(stream, Y)
+    B, T, H, d = Y.shape
+    wide = lambda t, name: c.check(t, name, (B, T, H * d), Y.dtype)
+    weight = lambda t, name: c.check(t, name, (H * d,), torch.float32)
+    c.run("gdn_block_norm", c.check(Y, "Y", strided=True), _strides(Y, 0, 2, 1), wide(Z, "Z"),
+          weight(w_post, "w_post"), wide(R, "R"), weight(w_pre, "w_pre"), scale, eps, GDN_ACT[act],
+          wide(X, "X"), wide(N, "N"), B, T, H, d, _dtype(Y))
+
+
+def gdn_block_norm_backward_workspace_bytes(Y):
+    """Scratch bytes ``gdn_block_norm_backward`` needs for Y ``[B, T, H, d]``."""
+    B, T, H, d = Y.shape
+    with torch.cuda.device(Y.device):
+        n = int(load().gdn_block_norm_backward_workspace_bytes(B, T, H, d))
+    if n < 0:
+        raise GdnError(GDN_ERR_UNSUPPORTED, f"rows of {H} x {d} channels are not served")
+    return n
+
+
+def gdn_block_norm_backward(Y, Z, w_post, R, w_pre, dX, dN, dY, dZ, dR, dw_post, dw_pre, workspace,
+                            scale=1.0, eps=1e-6, act="silu", stream=None):
+    """Gradients of ``gdn_block_norm`` for dX and dN; each of Z, w_post and
+    w_pre (with dN) goes together with its gradient; dR may be None or dX."""
+    c = _Call(stream, Y)
+    B, T, H, d = Y.shape
+    wide = lambda t, name: c.check(t, name, (B, T, H * d), Y.dtype)
+    weight = lambda t, name: c.check(t, name, (H * d,), torch.float32)
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    c.run("gdn_block_norm_backward", c.check(Y, "Y", strided=True), _strides(Y, 0, 2, 1),
+          wide(Z, "Z"), weight(w_post, "w_post"), wide(R, "R"), weight(w_pre, "w_pre"),
+          wide(dX, "dX"), wide(dN, "dN"), scale, eps, GDN_ACT[act],
+          c.check(dY, "dY", (B, T, H, d), Y.dtype, strided=True), _strides(dY, 0, 2, 1),
+          wide(dZ, "dZ"), wide(dR, "dR"), weight(dw_post, "dw_post"), weight(dw_pre, "dw_pre"),
+          c.check(workspace, "workspace"), ws, B, T, H, d, _dtype(Y))
 
 
 def gdn_get_status(stream=None) -> int:

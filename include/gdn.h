@@ -54,6 +54,26 @@ typedef struct gdn_shape {
 
 typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 
+/* Element strides of batch, head and token of a strided tensor whose last
+ * dimension (the channels of a head) is contiguous; non-negative multiples of
+ * 16 bytes.  Inputs may be broadcast with strides of zero. */
+typedef struct gdn_strides {
+    int64_t b, h, t;
+} gdn_strides;
+
+/* Linear attention: B batch rows of T tokens, Hk query/key heads, Hv value
+ * heads (a multiple of Hk), d = 128.  nseq > 0: B = 1 and the T rows hold nseq
+ * packed sequences; nseq = 0: B sequences of T tokens. */
+typedef struct gdn_linear_shape {
+    int64_t B, Hk, Hv, T;
+    int64_t nseq;
+    int32_t d;
+} gdn_linear_shape;
+
+/* Gate of gdn_block_norm; scaling of gdn_rotary_frequencies. */
+enum { GDN_ACT_SIGMOID = 0, GDN_ACT_SILU = 1 };
+enum { GDN_ROTARY_PLAIN = 0, GDN_ROTARY_LINEAR = 1, GDN_ROTARY_NTK = 2, GDN_ROTARY_YARN = 3 };
+
 /* Arithmetic of the k x k product chain in gdn_invert_neumann. */
 typedef enum gdn_prec {
     GDN_PREC_F32 = 0,  /* float32 FMA on CUDA cores (k <= 128)               */
@@ -318,6 +338,140 @@ int gdn_decode(const void* Q, const void* K, const void* V, const float* beta,
                int64_t n, int32_t d, gdn_dtype dtype, void* stream);
 
 /*
+ * The operators of a linear-attention layer around its recurrence: rotary
+ * positions on queries and keys, linear attention with one decay per head
+ * (prompts, gradients, single tokens), and the norms around a block.  They
+ * take the layouts of the calls above; small vectors (positions, frequencies,
+ * log-decays, sequence bounds, slots) need the alignment of their elements
+ * only.  Outputs may not share memory with inputs except where stated.
+ */
+
+/*
+ * Frequencies of the rotated pairs, on the HOST: inv_freq[i] = base^(-2i/rot),
+ * i < rot/2, and the factor *mscale on sines and cosines (1 unless stated).
+ * For contexts longer than the trained one, `scaling` changes them:
+ *   GDN_ROTARY_LINEAR  every frequency divided by `factor`;
+ *   GDN_ROTARY_NTK     base raised to base * factor^(rot/(rot-2)), so that the
+ *                      slowest pair is divided by `factor` and the fastest kept;
+ *   GDN_ROTARY_YARN    pairs that turn more than 32 times over
+ *                      `original_length` tokens kept, those below 1 turn divided
+ *                      by `factor`, linear in the turns between;
+ *                      *mscale = 0.1 ln(factor) + 1.
+ * Both outputs are host pointers.  rot is even, 2 <= rot <= 128; factor >= 1.
+ */
+int gdn_rotary_frequencies(float* inv_freq, float* mscale, int rot, double base, int scaling,
+                           double factor, int64_t original_length);
+
+/*
+ * Rotary positions: the first `rot` columns of every query and key row turn in
+ * pairs (a, b) by the angle positions[b, t] * inv_freq[i],
+ *   a' = mscale (a cos - b sin),  b' = mscale (a sin + b cos),
+ * pair i being columns (i, i + rot/2), or (2i, 2i + 1) if interleaved; columns
+ * from rot on are copied.  inverse = 1 turns back by the same angle (times
+ * mscale again): the gradient of the forward call.  Angles are formed in
+ * binary64, so positions may be any that it holds.  In: Q [B,Hq,T,d], K
+ * [B,Hk,T,d] (dtype, strided: a projection's [B,T,H,d] output serves as it is),
+ * positions [B,T] int64, inv_freq [rot/2] f32.  Out: Q_out, K_out (dtype,
+ * strided); each may be its input (same pointer and strides), else they share
+ * no memory.  Hq or Hk = 0: that tensor is not touched.  d = 128.
+ */
+int gdn_rotary(const void* Q, gdn_strides qs, void* Q_out, gdn_strides qos, const void* K,
+               gdn_strides ks, void* K_out, gdn_strides kos, const int64_t* positions,
+               const float* inv_freq, float mscale, int rot, int interleaved, int inverse,
+               int64_t B, int64_t Hq, int64_t Hk, int64_t T, int32_t d, gdn_dtype dtype,
+               void* stream);
+
+/*
+ * Linear attention with one decay per head, over whole sequences:
+ *   S_t = a_h S_{t-1} + v_t k_t^T,  o_t = scale S_t q_t,  a_h = exp(loggate[h]),
+ * value head h reading query/key head h / (Hv / Hk) as in gdn_decode.  loggate
+ * is a constant of the head (usually <= 0; -inf keeps no state) and has no
+ * gradient.  In: Q, K [B,Hk,T,d], V [B,Hv,T,d] (dtype), loggate [Hv] f32, S0
+ * [n,Hv,d,d] f32 (d_v x d_k, NULL = zero), n = nseq if packed, else B;
+ * cu_seqlens [nseq+1] int32 on the device (non-decreasing, within [0, T]; NULL
+ * unless packed): sequence i owns rows [cu[i], cu[i+1]), which may be none.
+ * Out: O [B,Hv,T,d] (dtype; rows of no sequence stay as they were), S_final
+ * [n,Hv,d,d] f32 (NULL to skip; S0 for a sequence of no rows).  T need not be a multiple of
+ * anything.  `workspace` holds gdn_linear_forward_workspace_bytes(s, dtype)
+ * bytes (it may be 0; of the current device, fixed by shape and dtype); calls
+ * that may overlap need one each.  A bound outside the rule sets the status
+ * word (gdn_get_status returns GDN_ERR_ARG) and that sequence is left out.
+ * bf16 data: products of bf16 on the tensor cores with fp32 accumulation, the
+ * state fp32 with its updates split into two bf16 parts (2^-17); weights and the
+ * state as an operand of o are rounded to bf16.  f32 data: fp32 on CUDA cores.
+ */
+int gdn_linear_forward(const void* Q, const void* K, const void* V, const float* loggate,
+                       const float* S0, const int32_t* cu_seqlens, float scale, void* O,
+                       float* S_final, void* workspace, int64_t workspace_bytes,
+                       gdn_linear_shape s, gdn_dtype dtype, void* stream);
+int64_t gdn_linear_forward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype);
+
+/*
+ * Gradients of gdn_linear_forward for dO [B,Hv,T,d] (dtype) and dS_final
+ * [n,Hv,d,d] f32 (NULL = zero):
+ *   dQ, dK [B,Hk,T,d] (summed over the value heads that share them), dV
+ *   [B,Hv,T,d] (dtype), dS0 [n,Hv,d,d] f32 (NULL to skip).
+ * Nothing is saved by the forward call: the states are formed again.  Other
+ * arguments as there; rows of no sequence stay as they were.
+ */
+int gdn_linear_backward(const void* Q, const void* K, const void* V, const float* loggate,
+                        const float* S0, const void* dO, const float* dS_final,
+                        const int32_t* cu_seqlens, float scale, void* dQ, void* dK, void* dV,
+                        float* dS0, void* workspace, int64_t workspace_bytes, gdn_linear_shape s,
+                        gdn_dtype dtype, void* stream);
+int64_t gdn_linear_backward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype);
+
+/*
+ * The same recurrence token by token from carried states (gdn_decode without
+ * the delta term): n tokens per call, the state read and written once.  In:
+ * Q, K [B,Hk,n,d], V [B,Hv,n,d] (dtype), loggate [Hv] f32.  In/out: S
+ * [nslots,Hv,d,d] f32, a pool of states; row b uses S[slots[b]] (slots [B]
+ * int32 on the device; NULL: S[b]).  Out: O [B,Hv,n,d] (dtype).  A row with a
+ * negative slot is left out (its O stays as it was).  So is one whose slot is
+ * nslots or more, or the slot of an earlier row, and the status word is set
+ * (gdn_get_status returns GDN_ERR_ARG).  d = 128, B <= 65535.
+ */
+int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* loggate, float* S,
+                      const int32_t* slots, int64_t nslots, float scale, void* O, int64_t B,
+                      int64_t Hk, int64_t Hv, int64_t n, int32_t d, gdn_dtype dtype,
+                      void* stream);
+
+/*
+ * The norms after a block and before the next, with the block's gate and the
+ * residual scale, for rows of W = H d channels:
+ *   yh = y / sqrt(mean_d(y^2) + eps),  n = w_post yh   (mean over each head's d)
+ *   x  = r + scale act(z) n,                           (act: GDN_ACT_*)
+ *   N  = w_pre x / sqrt(mean_W(x^2) + eps).
+ * Parts that are NULL are left out: w_post (n = y), Z (act = 1), R (x = scale
+ * act(z) n), w_pre with N.  In: Y [B,H,T,d] (dtype, strided: the head-major
+ * output of the attention calls, or H = 1 and [B,T,d]), Z, R [B,T,W] (dtype),
+ * w_post, w_pre [W] f32.  Out: X [B,T,W] (dtype; NULL to skip if N is given; may
+ * be R), N [B,T,W] (dtype).  N is the norm of x before X's rounding.  d = 128,
+ * or H = 1 and d a multiple of 8; W <= 16384; eps > 0.
+ */
+int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
+                   const void* R, const float* w_pre, float scale, float eps, int act, void* X,
+                   void* N, int64_t B, int64_t T, int64_t H, int64_t d, gdn_dtype dtype,
+                   void* stream);
+
+/*
+ * Gradients of gdn_block_norm for dX and dN [B,T,W] (dtype; dX may be NULL if
+ * dN is given): dY (strided like Y), dZ, dR (dtype; dR may be NULL, or dX),
+ * dw_post, dw_pre [W] f32, summed over the rows in an order fixed by shape and
+ * device.  Inputs are those of the forward call; each weight, Z and their
+ * gradients are given or left out together.  `workspace` holds
+ * gdn_block_norm_backward_workspace_bytes(B, T, H, d) bytes (unused without
+ * weights).  Without rows the weights' gradients are set to zero.
+ */
+int gdn_block_norm_backward(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
+                            const void* R, const float* w_pre, const void* dX, const void* dN,
+                            float scale, float eps, int act, void* dY, gdn_strides dys, void* dZ,
+                            void* dR, float* dw_post, float* dw_pre, void* workspace,
+                            int64_t workspace_bytes, int64_t B, int64_t T, int64_t H, int64_t d,
+                            gdn_dtype dtype, void* stream);
+int64_t gdn_block_norm_backward_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t d);
+
+/*
  * Streams: every entry point enqueues its kernels on `stream` (NULL = the
  * legacy default stream) and returns without synchronising; none allocates
  * device memory (gdn_forward takes a caller workspace).  The first call in a
@@ -328,8 +482,9 @@ int gdn_decode(const void* Q, const void* K, const void* V, const float* beta,
  * kept; a device reset (cudaDeviceReset) invalidates it, as it does the
  * static scratch of gdn_forward_static: reload the library after one. */
 /* Synchronises `stream`, returns the device status word of the current
- * device (GDN_OK, GDN_ERR_TIMEOUT, or GDN_ERR_CUDA when a kernel found its
- * shared memory misaligned) and clears it. */
+ * device (GDN_OK, GDN_ERR_TIMEOUT, GDN_ERR_ARG when a kernel found a slot or a
+ * sequence bound out of range, or GDN_ERR_CUDA when one found its shared memory
+ * misaligned) and clears it. */
 int gdn_get_status(void* stream);
 
 /*

@@ -1,0 +1,203 @@
+"""Host-side checks of the layer operators (no GPU is touched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from gated_deltanet_chunk_02_b200 import build as B
+from gated_deltanet_chunk_02_b200 import gdn
+from oracle import layer_oracle as L
+
+FAKE, ODD = 0x10000, 0x10008       # never dereferenced: every call fails its checks first
+BF16, F32 = gdn.GDN_BF16, gdn.GDN_F32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return gdn.load()
+
+
+def P(x):
+    return ctypes.c_void_p(x)
+
+
+def last(lib):
+    return lib.gdn_last_error().decode()
+
+
+def st(b, h, t):
+    return gdn.GdnStrides(b, h, t)
+
+
+# ---- rotary ----
+@pytest.mark.parametrize("rot", [2, 64, 128])
+@pytest.mark.parametrize("scaling,factor", [("plain", 1.0), ("linear", 4.0), ("ntk", 8.0),
+                                            ("yarn", 8.0)])
+def test_frequencies(lib, rot, scaling, factor):
+    f, m = gdn.gdn_rotary_frequencies(rot, 10000.0, scaling, factor, 8192)
+    g, n = L.rotary_frequencies(rot, 10000.0, scaling, factor, 8192)
+    # one rounding to float32 and the powers' own errors in float64
+    assert np.allclose(f.numpy(), g, rtol=2.0 ** -23, atol=0)
+    assert abs(m - n) <= 2.0 ** -23 * n
+
+
+@pytest.mark.parametrize("rot,base,scaling,factor,length", [
+    (0, 1e4, 0, 1.0, 0), (7, 1e4, 0, 1.0, 0), (130, 1e4, 0, 1.0, 0), (64, 1.0, 0, 1.0, 0),
+    (64, float("nan"), 0, 1.0, 0), (64, 1e4, 4, 1.0, 0), (64, 1e4, 1, 0.5, 0),
+    (64, 1e4, 3, 2.0, 0)])
+def test_frequency_refusals(lib, rot, base, scaling, factor, length):
+    out = (ctypes.c_float * 64)()
+    m = ctypes.c_float()
+    assert lib.gdn_rotary_frequencies(out, ctypes.byref(m), rot, base, scaling, factor,
+                                      length) == gdn.GDN_ERR_ARG
+    assert lib.gdn_rotary_frequencies(None, ctypes.byref(m), 64, 1e4, 0, 1.0, 0) == gdn.GDN_ERR_ARG
+
+
+def rotary(lib, q=FAKE, qo=FAKE, qs=None, qos=None, pos=FAKE, inv=FAKE, rot=64, inter=0, back=0,
+           B=2, Hq=4, Hk=0, T=8, d=128, dtype=BF16, k=None):
+    s = st(4 * 8 * 128, 8 * 128, 128)
+    return lib.gdn_rotary(P(q), qs or s, P(qo), qos or s, P(k), s, P(k), s, P(pos), P(inv), 1.0,
+                          rot, inter, back, B, Hq, Hk, T, d, dtype, None)
+
+
+def test_rotary_refusals(lib):
+    bad = [dict(rot=0), dict(rot=63), dict(rot=130), dict(inter=2), dict(back=-1), dict(B=-1),
+           dict(dtype=7), dict(q=None), dict(qo=None), dict(pos=None), dict(inv=None),
+           dict(qs=st(-8, 128, 128)), dict(Hk=1), dict(B=1 << 20, T=1 << 20)]
+    for kw in bad:
+        assert rotary(lib, **kw) == gdn.GDN_ERR_ARG, kw
+    assert rotary(lib, d=64) == gdn.GDN_ERR_UNSUPPORTED
+    for kw in [dict(q=ODD), dict(qo=ODD), dict(pos=FAKE + 4), dict(inv=FAKE + 2),
+               dict(qs=st(4, 128, 128)), dict(dtype=F32, qs=st(2, 128, 128))]:
+        assert rotary(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
+    # output rows on one another: broadcast, and a token stride below a row
+    assert rotary(lib, qos=st(0, 1024, 128)) == gdn.GDN_ERR_ARG and "overlap" in last(lib)
+    assert rotary(lib, qos=st(4096, 1024, 64)) == gdn.GDN_ERR_ARG
+    # nothing to do
+    for kw in [dict(B=0), dict(T=0), dict(Hq=0)]:
+        assert rotary(lib, q=None, qo=None, pos=None, inv=None, **kw) == gdn.GDN_OK
+
+
+# ---- linear attention ----
+def shape(B=1, Hk=2, Hv=4, T=100, nseq=0, d=128):
+    return gdn.GdnLinearShape(B, Hk, Hv, T, nseq, d)
+
+
+def forward(lib, q=FAKE, lg=FAKE, s0=None, cu=None, sf=FAKE, ws=None, wsb=1 << 40, s=None,
+            dtype=BF16):
+    return lib.gdn_linear_forward(P(q), P(FAKE), P(FAKE), P(lg), P(s0), P(cu), 1.0, P(FAKE), P(sf),
+                                  P(ws), wsb, s or shape(), dtype, None)
+
+
+def backward(lib, dq=FAKE, cu=None, ws=None, wsb=1 << 40, s=None, ds0=None, dtype=BF16):
+    return lib.gdn_linear_backward(P(FAKE), P(FAKE), P(FAKE), P(FAKE), None, P(FAKE), None, P(cu),
+                                   1.0, P(dq), P(FAKE), P(FAKE), P(ds0), P(ws), wsb, s or shape(),
+                                   dtype, None)
+
+
+def test_linear_refusals(lib):
+    long = shape(T=65536, Hk=4)
+    for f in (forward, backward):
+        for kw in [dict(dtype=2), dict(s=shape(B=-1)), dict(s=shape(nseq=-1)),
+                   dict(s=shape(Hk=3)), dict(s=shape(Hk=0)), dict(s=shape(Hk=9000, Hv=9000)),
+                   dict(s=shape(nseq=2)), dict(s=shape(B=2, nseq=2), cu=FAKE), dict(cu=FAKE),
+                   dict(s=shape(B=1 << 20, T=1 << 20)), dict(s=long, wsb=0),
+                   dict(s=long, ws=None)]:
+            assert f(lib, **kw) == gdn.GDN_ERR_ARG, (f, kw)
+        assert f(lib, s=shape(d=64)) == gdn.GDN_ERR_UNSUPPORTED
+        assert f(lib, s=shape(nseq=2), cu=FAKE + 2) == gdn.GDN_ERR_ALIGN
+        assert f(lib, s=shape(B=0)) == gdn.GDN_OK and f(lib, s=shape(Hk=0, Hv=0)) == gdn.GDN_OK
+    for kw in [dict(q=None), dict(lg=None)]:
+        assert forward(lib, **kw) == gdn.GDN_ERR_ARG
+    for kw in [dict(q=ODD), dict(lg=FAKE + 2), dict(s0=ODD), dict(sf=ODD), dict(s=long, ws=ODD)]:
+        assert forward(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
+    assert backward(lib, dq=None) == gdn.GDN_ERR_ARG
+    assert backward(lib, ds0=ODD) == gdn.GDN_ERR_ALIGN
+
+
+def test_linear_workspace_sizes(lib):
+    f, b = lib.gdn_linear_forward_workspace_bytes, lib.gdn_linear_backward_workspace_bytes
+    for dtype in (BF16, F32):
+        assert f(shape(T=1, Hk=4), dtype) == 0 == b(shape(T=128, Hk=4), dtype)
+        assert f(shape(T=65536), dtype) % (4 * 65536) == 0 < f(shape(T=65536), dtype)
+        # shared heads: float32 dQ and dK of every value head
+        assert b(shape(T=128), dtype) >= 2 * 4 * 128 * 128 * 4
+        assert f(shape(Hk=3), dtype) == -1 == b(shape(B=2, nseq=1), dtype)
+
+
+def test_linear_decode_refusals(lib):
+    def call(q=FAKE, lg=FAKE, S=FAKE, slots=None, nslots=8, B=2, Hk=2, Hv=4, n=1, d=128,
+             dtype=BF16):
+        return lib.gdn_linear_decode(P(q), P(FAKE), P(FAKE), P(lg), P(S), P(slots), nslots, 1.0,
+                                     P(FAKE), B, Hk, Hv, n, d, dtype, None)
+    for kw in [dict(q=None), dict(lg=None), dict(S=None), dict(nslots=1), dict(Hk=3), dict(Hk=0),
+               dict(n=-1), dict(B=65536), dict(dtype=9), dict(slots=FAKE, nslots=-1)]:
+        assert call(**kw) == gdn.GDN_ERR_ARG, kw
+    for kw in [dict(q=ODD), dict(S=ODD), dict(slots=FAKE + 2), dict(lg=FAKE + 2)]:
+        assert call(**kw) == gdn.GDN_ERR_ALIGN, kw
+    assert call(d=64) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(q=None, B=0) == gdn.GDN_OK == call(q=None, n=0)
+
+
+# ---- block norm ----
+def norm(lib, y=FAKE, ys=None, z=None, wo=FAKE, r=None, wi=None, eps=1e-6, act=1, X=FAKE, N=None,
+         B=2, T=4, H=3, d=128, dtype=BF16):
+    return lib.gdn_block_norm(P(y), ys or st(4096, 512, 128), P(z), P(wo), P(r), P(wi), 1.0, eps,
+                              act, P(X), P(N), B, T, H, d, dtype, None)
+
+
+def norm_back(lib, z=None, dz=None, wo=FAKE, dwo=FAKE, wi=None, dwi=None, dX=FAKE, dN=None, r=None,
+              dr=None, dy=FAKE, dys=None, ws=FAKE, wsb=1 << 40, B=2, T=4, H=3, d=128):
+    s = st(4096, 512, 128)
+    return lib.gdn_block_norm_backward(P(FAKE), s, P(z), P(wo), P(r), P(wi), P(dX), P(dN), 1.0,
+                                       1e-6, 0, P(dy), dys or s, P(dz), P(dr), P(dwo), P(dwi),
+                                       P(ws), wsb, B, T, H, d, BF16, None)
+
+
+def test_norm_refusals(lib):
+    for kw in [dict(y=None), dict(eps=0.0), dict(eps=float("nan")), dict(act=2), dict(X=None),
+               dict(wi=FAKE), dict(N=FAKE), dict(dtype=3), dict(T=-1), dict(ys=st(-8, 8, 8))]:
+        assert norm(lib, **kw) == gdn.GDN_ERR_ARG, kw
+    for kw in [dict(d=64), dict(H=1, d=12), dict(H=129), dict(H=1, d=16392)]:
+        assert norm(lib, **kw) == gdn.GDN_ERR_UNSUPPORTED, kw
+    for kw in [dict(y=ODD), dict(z=ODD), dict(wo=ODD), dict(r=ODD), dict(X=ODD),
+               dict(ys=st(4096, 512, 4))]:
+        assert norm(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
+    for kw in [dict(B=0), dict(T=0), dict(H=0)]:
+        assert norm(lib, y=None, **kw) == gdn.GDN_OK
+
+
+def test_norm_backward_refusals(lib):
+    for kw in [dict(z=FAKE), dict(dz=FAKE), dict(dwo=None), dict(wi=FAKE), dict(dN=FAKE),
+               dict(dr=FAKE), dict(dX=None), dict(dy=None), dict(wsb=0), dict(ws=None),
+               dict(dys=st(0, 512, 128))]:
+        assert norm_back(lib, **kw) == gdn.GDN_ERR_ARG, kw
+    for kw in [dict(dy=ODD), dict(dwo=ODD), dict(ws=ODD), dict(dX=ODD), dict(dys=st(4096, 512, 4))]:
+        assert norm_back(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
+    assert norm_back(lib, wo=None, dwo=None, B=0) == gdn.GDN_OK
+    f = lib.gdn_block_norm_backward_workspace_bytes
+    assert f(2, 4, 3, 128) > 0 and f(0, 4, 3, 128) == 0 and f(1, 1, 1, 12) == -1
+
+
+# ---- the binding ----
+def test_binding_refuses_what_the_library_cannot_see(lib):
+    x = torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16)
+    lg = torch.zeros(2)
+    S = torch.zeros(1, 2, 128, 128)
+    with pytest.raises(ValueError, match="CUDA"):
+        gdn.gdn_linear_decode(x, x, x, lg, S, x.clone())
+    with pytest.raises(ValueError, match="shares memory"):
+        gdn.gdn_linear_decode(x, x, x, lg, S, x)
+    with pytest.raises(ValueError, match="shares memory"):
+        gdn.gdn_linear_forward(x, x, x, lg, S, x.clone(), S, None)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        gdn.gdn_linear_forward(x, x, x, lg, None, x.clone(), None, None,
+                               cu_seqlens=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        gdn.gdn_rotary(x, None, None, torch.ones(4), None, None)
+    with pytest.raises(KeyError):
+        gdn.gdn_rotary_frequencies(64, scaling="other")
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_rotary_frequencies(63)

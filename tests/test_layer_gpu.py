@@ -1,0 +1,678 @@
+"""GPU parity of the layer operators against the float64 oracle, entry by entry.
+
+Tolerances count roundings (half a step: bf16 2^-8, fp32 2^-24 of the value):
+* rotary: two products and a sum in fp32 on sines and cosines good to 2^-22,
+  then the output's rounding;
+* linear attention: with A the same sums over absolute values, every term of an
+  output passes at most one rounding to bf16 (its weight, or its state) besides
+  the output's own, and fp32 sums of at most 256 terms a chunk; state updates
+  carry two bf16 parts (2^-17) on the tensor cores, and one more fp32 rounding
+  per chunk;
+* norms: sums over a row in fp32 (a tree, counted as 64 roundings with the
+  exponential and divisions), weight gradients over the rows in fp32.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gated_deltanet_chunk_02_b200 import gdn
+from oracle import layer_oracle as L
+
+pytestmark = pytest.mark.gpu
+U32, UBF, USTATE = 2.0 ** -24, 2.0 ** -8, 2.0 ** -17
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+half_step = lambda dtype: UBF if dtype == "bf16" else U32
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def near(got, want, tol, name):
+    got = f64(got)
+    assert got.shape == want.shape, name
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (name, int(bad.sum()), float(np.abs(got - want)[bad].max()),
+                           tuple(int(i[0]) for i in np.nonzero(bad)))
+
+
+def rand(gen, *shape, dtype="f32", scale=1.0):
+    return (torch.randn(*shape, generator=gen) * scale).to(DT[dtype]).cuda()
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    torch.cuda.synchronize()
+    assert gdn.gdn_get_status() == gdn.GDN_OK
+
+
+# --------------------------------------------------------------------------- #
+# rotary
+# --------------------------------------------------------------------------- #
+def rotary_tol(x, inv, m, inter, dtype):
+    """Sum of the magnitudes of a pair's two terms, at most m (|a| + |b|)."""
+    half = len(inv)
+    mag = np.abs(x).copy()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+        s = m * (np.abs(x[..., a]) + np.abs(x[..., b]))
+        mag[..., a] = mag[..., b] = s
+    return mag * (half_step(dtype) + 8 * 2.0 ** -23) * 1.01
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [128, 64, 16, 2, 10, 126])
+def test_rotary(lib, dtype, inter, rot):
+    B, Hq, Hk, T = 2, 5, 2, 19
+    g = gen(rot)
+    q, k = rand(g, B, Hq, T, 128, dtype=dtype), rand(g, B, Hk, T, 128, dtype=dtype)
+    inv, m = gdn.gdn_rotary_frequencies(rot, scaling="yarn", factor=4.0, original_length=4096)
+    pos = torch.randint(0, 1 << 20, (B, T), generator=g).cuda()
+    for back in (False, True):
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        gdn.gdn_rotary(q, k, pos, inv.cuda(), qo, ko, mscale=m, interleaved=inter, inverse=back)
+        for x, y, name in ((q, qo, "q"), (k, ko, "k")):
+            want = L.rotary(f64(x), f64(pos), f64(inv), m, inter, back)
+            near(y, want, rotary_tol(f64(x), inv, m, inter, dtype), name)
+        # in place, and the copied columns bit for bit
+        qi, ki = q.clone(), k.clone()
+        gdn.gdn_rotary(qi, ki, pos, inv.cuda(), qi, ki, mscale=m, interleaved=inter, inverse=back)
+        assert torch.equal(qi, qo) and torch.equal(ki, ko)
+        assert torch.equal(qo[..., rot:], q[..., rot:])
+
+
+@pytest.mark.parametrize("B,T,Hq,Hk", [(1, 1, 1, 0), (1, 1, 0, 3), (64, 1, 32, 16), (3, 17, 4, 4),
+                                       (1, 4097, 9, 1)])
+def test_rotary_strided_views_and_sizes(lib, B, T, Hq, Hk):
+    """A fused projection's [B, T, heads, d] slices in, head-major out; far positions."""
+    g = gen(T)
+    fused = rand(g, B, T, Hq + Hk + 1, 128, dtype="bf16")
+    keep = fused.clone()
+    q = fused[:, :, :Hq].transpose(1, 2) if Hq else None
+    k = fused[:, :, Hq:Hq + Hk].transpose(1, 2) if Hk else None
+    inv, m = gdn.gdn_rotary_frequencies(128)
+    pos = (torch.arange(T)[None] + torch.randint(0, 1 << 40, (B, 1), generator=g)).cuda()
+    new = lambda x: None if x is None else torch.empty(x.shape, dtype=x.dtype, device="cuda")
+    qo, ko = new(q), new(k)
+    gdn.gdn_rotary(q, k, pos, inv.cuda(), qo, ko, mscale=m)
+    # positions near 2^40: the angle's binary64 error is 2^-53 * 2^40 turns on top
+    for x, y in ((q, qo), (k, ko)):
+        if x is not None:
+            want = L.rotary(f64(x), pos.cpu().numpy(), f64(inv), m)
+            tol = rotary_tol(f64(x), inv, m, False, "bf16") + 2.0 ** -9 * np.abs(f64(x)).max()
+            near(y, want, tol, "far")
+    assert torch.equal(fused, keep)
+    # the same in place on the fused buffer: nothing else moves
+    gdn.gdn_rotary(q, k, pos, inv.cuda(), q, k, mscale=m)
+    assert torch.equal(fused[:, :, Hq + Hk:], keep[:, :, Hq + Hk:])
+    if q is not None:
+        assert torch.equal(q, qo)
+
+
+def test_rotary_copies_odd_values(lib):
+    """Infinities and NaN outside the rotated columns stay where they are."""
+    x = torch.zeros(1, 1, 3, 128, device="cuda")
+    x[..., 64:] = float("inf")
+    x[0, 0, 1, 100] = float("nan")
+    inv, _ = gdn.gdn_rotary_frequencies(64)
+    y = torch.empty_like(x)
+    gdn.gdn_rotary(x, None, torch.arange(3, device="cuda")[None], inv.cuda(), y, None)
+    assert torch.equal(y[..., 64:].nan_to_num(7.0), x[..., 64:].nan_to_num(7.0))
+    assert (y[..., :64] == 0).all()
+
+
+# --------------------------------------------------------------------------- #
+# linear attention
+# --------------------------------------------------------------------------- #
+DECAYS = [-0.9, -0.05, -0.001, 0.0, -3.0, -0.3, -1e-5, -0.01]
+
+
+def linear_case(seed, dtype, B, Hk, Hv, T, lens, carried):
+    g = gen(seed)
+    n = len(lens) if lens is not None else B
+    c = dict(Q=rand(g, B, Hk, T, 128, dtype=dtype, scale=128 ** -0.5),
+             K=rand(g, B, Hk, T, 128, dtype=dtype, scale=128 ** -0.5),
+             V=rand(g, B, Hv, T, 128, dtype=dtype), dO=rand(g, B, Hv, T, 128, dtype=dtype),
+             lg=torch.tensor((DECAYS * Hv)[:Hv]).cuda(), S0=None, dS=None, cu=None)
+    if carried:
+        c["S0"] = rand(g, n, Hv, 128, 128)
+        c["dS"] = rand(g, n, Hv, 128, 128)
+    if lens is not None:
+        c["cu"] = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+    if lens is None:
+        c["rows"] = [(b, 0, T) for b in range(B)]
+    else:
+        at = np.concatenate([[0], np.cumsum(lens)])
+        c["rows"] = [(0, int(at[i]), lens[i]) for i in range(n)]
+    return c
+
+
+def oracle_linear(c, scale, absolute=False):
+    """o, S over all sequences; of the absolute values if asked."""
+    f = (lambda t: None if t is None else np.abs(f64(t))) if absolute else f64
+    Q, K, V, S0 = (f(c[x]) for x in ("Q", "K", "V", "S0"))
+    o, S = np.zeros(V.shape), np.zeros((len(c["rows"]), V.shape[1], 128, 128))
+    for i, (b, a, n) in enumerate(c["rows"]):
+        part = [x[b, :, a:a + n] for x in (Q, K, V)]
+        o[b, :, a:a + n], S[i] = L.linear_forward(*part, f64(c["lg"]),
+                                                  None if S0 is None else S0[i], scale)
+    return o, S
+
+
+def oracle_linear_grad(c, scale, absolute=False):
+    f = (lambda t: None if t is None else np.abs(f64(t))) if absolute else f64
+    Q, K, V, S0, dO, dS = (f(c[x]) for x in ("Q", "K", "V", "S0", "dO", "dS"))
+    out = [np.zeros(Q.shape), np.zeros(K.shape), np.zeros(V.shape),
+           np.zeros((len(c["rows"]), V.shape[1], 128, 128))]
+    for i, (b, a, n) in enumerate(c["rows"]):
+        q, k, v, do = (x[b, :, a:a + n] for x in (Q, K, V, dO))
+        *g, e = L.linear_backward(q, k, v, f64(c["lg"]), None if S0 is None else S0[i], do,
+                                  None if dS is None else dS[i], scale)
+        for x, y in zip(out, g):
+            x[b, :, a:a + n] = y
+        out[3][i] = e
+    return out
+
+
+def out_tol(ref, mag, dtype, T):
+    u = half_step(dtype)
+    sums = (512 + T / 16) * U32
+    return (u * np.abs(ref) + ((UBF + USTATE if dtype == "bf16" else 0.0) + sums) * mag) * 1.02 + 1e-30
+
+
+def state_tol(mag, dtype, T):
+    return ((USTATE if dtype == "bf16" else 0.0) + (512 + T / 16) * U32) * mag + 1e-30
+
+
+def run_forward(c, scale, want_state=True):
+    O = torch.full_like(c["V"], 77.0)
+    S = torch.full((len(c["rows"]), c["V"].shape[1], 128, 128), 77.0, device="cuda") \
+        if want_state else None
+    n = gdn.gdn_linear_forward_workspace_bytes(c["K"], c["V"], c["cu"])
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")        # NaN everywhere
+    gdn.gdn_linear_forward(c["Q"], c["K"], c["V"], c["lg"], c["S0"], O, S, ws, scale=scale,
+                           cu_seqlens=c["cu"])
+    return O, S
+
+
+def run_backward(c, scale):
+    outs = [torch.full_like(c[x], 77.0) for x in ("Q", "K", "V")]
+    dS0 = torch.full((len(c["rows"]), c["V"].shape[1], 128, 128), 77.0, device="cuda")
+    n = gdn.gdn_linear_backward_workspace_bytes(c["K"], c["V"], c["cu"])
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    gdn.gdn_linear_backward(c["Q"], c["K"], c["V"], c["lg"], c["S0"], c["dO"], c["dS"], *outs, dS0,
+                            ws, scale=scale, cu_seqlens=c["cu"])
+    return (*outs, dS0)
+
+
+SHAPES = [                         # B, Hk, Hv, T, lens
+    (1, 1, 1, 1, None), (2, 2, 2, 2, None), (1, 2, 4, 63, None), (1, 1, 2, 64, None),
+    (1, 3, 3, 127, None), (2, 1, 1, 128, None), (1, 2, 2, 129, None), (1, 1, 3, 300, None),
+    (1, 1, 8, 1025, None), (1, 1, 1, 1, [1]), (1, 1, 2, 40, [0, 1, 0, 33]),
+    (1, 2, 4, 700, [128, 0, 129, 1, 127, 256]), (1, 1, 1, 1500, [5, 1400]),
+    (1, 2, 2, 500, [0, 0, 0]), (1, 1, 2, 300, [1] * 70 + [3] * 20),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("carried", [False, True])
+@pytest.mark.parametrize("B,Hk,Hv,T,lens", SHAPES)
+def test_linear_forward(lib, dtype, carried, B, Hk, Hv, T, lens):
+    c = linear_case(T, dtype, B, Hk, Hv, T, lens, carried)
+    O, S = run_forward(c, 0.7)
+    o, s = oracle_linear(c, 0.7)
+    om, sm = oracle_linear(c, 0.7, absolute=True)
+    used = T if lens is None else sum(lens)
+    near(S, s, state_tol(sm, dtype, T), "S")
+    near(O[:, :, :used], o[:, :, :used], out_tol(o, om, dtype, T)[:, :, :used], "O")
+    assert (O[:, :, used:] == 77.0).all()              # rows of no sequence
+    if not carried:
+        O2, _ = run_forward(c, 0.7, want_state=False)
+        assert torch.equal(O, O2)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("carried", [False, True])
+@pytest.mark.parametrize("B,Hk,Hv,T,lens", SHAPES)
+def test_linear_backward(lib, dtype, carried, B, Hk, Hv, T, lens):
+    c = linear_case(T + 1, dtype, B, Hk, Hv, T, lens, carried)
+    got = run_backward(c, 0.7)
+    want = oracle_linear_grad(c, 0.7)
+    mag = oracle_linear_grad(c, 0.7, absolute=True)
+    used = T if lens is None else sum(lens)
+    near(got[3], want[3], state_tol(mag[3], dtype, T), "dS0")
+    for x, y, m, name in zip(got, want[:3], mag, ("dQ", "dK", "dV")):
+        near(x[:, :, :used], y[:, :, :used], out_tol(y, m, dtype, T)[:, :, :used], name)
+        assert (x[:, :, used:] == 77.0).all(), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_long_is_cut_into_segments(lib, dtype):
+    """Few heads over many rows: the call is cut, and its pieces fit together:
+    the same rows as two calls with the state handed over."""
+    T, cut = 6400, 3100
+    c = linear_case(5, dtype, 1, 1, 2, T, None, True)
+    assert gdn.gdn_linear_forward_workspace_bytes(c["K"], c["V"]) > 0
+    O, S = run_forward(c, 1.0)
+    o, s = oracle_linear(c, 1.0)
+    om, sm = oracle_linear(c, 1.0, absolute=True)
+    near(S, s, state_tol(sm, dtype, T), "S")
+    near(O, o, out_tol(o, om, dtype, T), "O")
+    got = run_backward(c, 1.0)
+    want, mag = oracle_linear_grad(c, 1.0), oracle_linear_grad(c, 1.0, absolute=True)
+    near(got[3], want[3], state_tol(mag[3], dtype, T), "dS0")
+    for x, y, m, name in zip(got, want, mag, ("dQ", "dK", "dV")):
+        near(x, y, out_tol(y, m, dtype, T), name)
+    state = c["S0"]
+    for a, b in ((0, cut), (cut, T)):
+        part = {x: c[x][:, :, a:b].contiguous() for x in ("Q", "K", "V")}
+        O1, state = run_forward(dict(c, **part, S0=state, rows=[(0, 0, b - a)]), 1.0)
+        near(O1, o[:, :, a:b], out_tol(o, om, dtype, T)[:, :, a:b], "part")
+    near(state, s, state_tol(sm, dtype, T), "state handed over")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_no_rows_and_no_memory(lib, dtype):
+    c = linear_case(6, dtype, 2, 1, 2, 0, None, True)
+    _, S = run_forward(c, 1.0)
+    assert torch.equal(S, c["S0"])
+    assert torch.equal(run_backward(c, 1.0)[3], c["dS"])
+    c = linear_case(7, dtype, 1, 1, 2, 200, None, False)
+    c["lg"] = torch.tensor([float("-inf"), -200.0]).cuda()
+    O, S = run_forward(c, 1.0)                          # o_t = v_t (k_t . q_t)
+    o, s = oracle_linear(c, 1.0)
+    om, sm = oracle_linear(c, 1.0, absolute=True)
+    near(O, o, out_tol(o, om, dtype, 200), "O")
+    near(S, s, state_tol(sm, dtype, 200), "S")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_rows_behind_and_between_do_not_leak(lib, dtype):
+    """NaN and infinity in one packed sequence and behind the last leave the
+    other sequences' results as they are."""
+    lens = [70, 200, 130]
+    c = linear_case(8, dtype, 1, 2, 2, 500, lens, True)
+    good, goodS = run_forward(c, 1.0)
+    grads = run_backward(c, 1.0)
+    for x in ("Q", "K", "V", "dO"):
+        c[x][:, :, 70:270:7] = float("nan")
+        c[x][:, :, 75:270:7] = float("inf")
+        c[x][:, :, 400:] = float("nan")
+    O, S = run_forward(c, 1.0)
+    for rows in (slice(0, 70), slice(270, 400)):
+        assert torch.equal(O[:, :, rows], good[:, :, rows])
+        for a, b in zip(run_backward(c, 1.0)[:3], grads):
+            assert torch.equal(a[:, :, rows], b[:, :, rows])
+    assert torch.equal(S[[0, 2]], goodS[[0, 2]])
+
+
+@pytest.mark.parametrize("cu", [[0, 50, 40, 200], [0, 100, 300, 400], [-5, 20, 60, 100]])
+def test_linear_bad_bounds_are_reported(lib, cu):
+    c = linear_case(9, "bf16", 1, 1, 2, 300, [100, 100, 100], False)
+    c["cu"] = torch.tensor(cu, dtype=torch.int32).cuda()
+    run_forward(c, 1.0)
+    assert gdn.gdn_get_status() == gdn.GDN_ERR_ARG
+    run_backward(c, 1.0)
+    assert gdn.gdn_get_status() == gdn.GDN_ERR_ARG
+
+
+# --------------------------------------------------------------------------- #
+# single tokens
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,Hv,n", [(1, 1, 1, 1), (3, 2, 4, 5), (1, 8, 16, 4), (40, 2, 8, 1)])
+def test_linear_decode(lib, dtype, B, Hk, Hv, n):
+    g = gen(B + n)
+    q = rand(g, B, Hk, n, 128, dtype=dtype, scale=128 ** -0.5)
+    k = rand(g, B, Hk, n, 128, dtype=dtype, scale=128 ** -0.5)
+    v = rand(g, B, Hv, n, 128, dtype=dtype)
+    lg = torch.tensor((DECAYS * Hv)[:Hv]).cuda()
+    pool = rand(g, B + 3, Hv, 128, 128)
+    slots = torch.randperm(B + 3, generator=g)[:B].to(torch.int32)
+    for at in (slots, None):
+        S = pool.clone()
+        O = torch.full_like(v, 77.0)
+        gdn.gdn_linear_decode(q, k, v, lg, S, O, None if at is None else at.cuda(), scale=0.7)
+        rows = range(B) if at is None else at.tolist()
+        for b, s in enumerate(rows):
+            args = (f64(q[b]), f64(k[b]), f64(v[b]), f64(lg))
+            o, e = L.linear_forward(*args, f64(pool[s]), 0.7)
+            om, em = L.linear_forward(*(np.abs(x) for x in args[:3]), args[3],
+                                      np.abs(f64(pool[s])), 0.7)
+            near(O[b], o, half_step(dtype) * np.abs(o) + 160 * U32 * om, "O")
+            near(S[s], e, (4 * n + 4) * U32 * em, "S")
+        rest = [i for i in range(B + 3) if i not in rows]
+        assert torch.equal(S[rest], pool[rest])
+
+
+def test_linear_decode_continues_a_prompt(lib):
+    """A prompt's state, then its next tokens: as the longer prompt."""
+    c = linear_case(11, "f32", 2, 1, 2, 140, None, False)
+    o, s = oracle_linear(c, 1.0)
+    om, sm = oracle_linear(c, 1.0, absolute=True)
+    head = {x: c[x][:, :, :137].contiguous() for x in ("Q", "K", "V")}
+    _, S = run_forward(dict(c, **head, rows=[(0, 0, 137), (1, 0, 137)]), 1.0)
+    q, k, v = (c[x][:, :, 137:].contiguous() for x in ("Q", "K", "V"))
+    O = torch.empty_like(v)
+    gdn.gdn_linear_decode(q, k, v, c["lg"], S, O)
+    near(O, o[:, :, 137:], out_tol(o, om, "f32", 140)[:, :, 137:], "O")
+    near(S, s, state_tol(sm, "f32", 140), "S")
+
+
+def test_linear_decode_slots_left_out_and_refused(lib):
+    g = gen(12)
+    x = rand(g, 6, 2, 1, 128)
+    lg = torch.zeros(2).cuda()
+    pool = rand(g, 4, 2, 128, 128)
+    S, O = pool.clone(), torch.full_like(x, 77.0)
+    gdn.gdn_linear_decode(x, x, x, lg, S, O, torch.tensor([2, -1, 0, -7, 1, -1],
+                                                          dtype=torch.int32).cuda())
+    assert gdn.gdn_get_status() == gdn.GDN_OK
+    assert (O[[1, 3, 5]] == 77.0).all() and (O[[0, 2, 4]] != 77.0).any()
+    assert torch.equal(S[3], pool[3])
+    want, out = S.clone(), O.clone()
+    # slot 4 is not there, slot 2 is named twice: those rows are left out and reported
+    S, O = pool.clone(), torch.full_like(x, 77.0)
+    gdn.gdn_linear_decode(x, x, x, lg, S, O, torch.tensor([2, 4, 0, 2, 1, 2 ** 31 - 1],
+                                                          dtype=torch.int32).cuda())
+    assert gdn.gdn_get_status() == gdn.GDN_ERR_ARG
+    assert torch.equal(S, want) and torch.equal(O, out)
+
+
+# --------------------------------------------------------------------------- #
+# norms
+# --------------------------------------------------------------------------- #
+def norm_case(seed, dtype, B, T, H, d, parts, head_major=True):
+    g = gen(seed)
+    W = H * d
+    y = rand(g, B, H, T, d, dtype=dtype).transpose(1, 2) if head_major \
+        else rand(g, B, T, H, d, dtype=dtype)
+    return dict(Y=y, Z=rand(g, B, T, W, dtype=dtype, scale=2.0) if "z" in parts else None,
+                wo=rand(g, W) if "p" in parts else None,
+                R=rand(g, B, T, W, dtype=dtype) if "r" in parts else None,
+                wi=rand(g, W) if "n" in parts else None,
+                dX=rand(g, B, T, W, dtype=dtype) if "x" in parts else None,
+                dN=rand(g, B, T, W, dtype=dtype) if "n" in parts else None)
+
+
+def flat(c):
+    Y = c["Y"]
+    B, T, H, d = Y.shape
+    row = lambda t: None if t is None else f64(t).reshape(B * T, H * d)
+    return (f64(Y).reshape(B * T, H, d), row(c["Z"]), f64(c["wo"]), row(c["R"]), f64(c["wi"]))
+
+
+PARTS = ["zprnx", "zpx", "px", "zx", "pn", "rnx", "zprn", "nx"]
+NORM_SHAPES = [(1, 1, 1, 8, True), (2, 3, 1, 128, True), (1, 5, 3, 128, True),
+               (3, 2, 32, 128, False), (1, 67, 1, 264, True), (2, 9, 1, 2048, True),
+               (1, 2, 1, 5000, True), (1, 2, 1, 16384, True), (1, 700, 16, 128, True)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("parts", PARTS)
+@pytest.mark.parametrize("B,T,H,d,hm", NORM_SHAPES)
+def test_block_norm(lib, dtype, act, parts, B, T, H, d, hm):
+    c = norm_case(d + T, dtype, B, T, H, d, parts, hm)
+    W = H * d
+    empty = lambda: torch.empty(B, T, W, dtype=DT[dtype], device="cuda")
+    X, N = empty(), empty() if "n" in parts else None
+    gdn.gdn_block_norm(c["Y"], c["Z"], c["wo"], c["R"], c["wi"], X, N, scale=0.5, eps=1e-5,
+                       act=act)
+    y, z, wo, r, wi = flat(c)
+    x, n = L.block_norm(y, z, wo, r, wi, 0.5, 1e-5, act)
+    mag = np.abs(x) if r is None else np.abs(r) + np.abs(x - r)
+    u = half_step(dtype)
+    near(X.view(B * T, W), x, u * np.abs(x) + 64 * U32 * mag, "X")
+    if n is not None:
+        rms = np.sqrt((x * x).mean(-1, keepdims=True) + 1e-5)
+        near(N.view(B * T, W), n, u * np.abs(n) + 128 * U32 * np.abs(wi) * (mag / rms + np.abs(x) / rms),
+             "N")
+        if r is not None:                              # the residual stream in place; X left out
+            X2, N2 = c["R"].clone(), empty()
+            gdn.gdn_block_norm(c["Y"], c["Z"], c["wo"], X2, c["wi"], X2, N2, scale=0.5, eps=1e-5,
+                               act=act)
+            assert torch.equal(X2, X) and torch.equal(N2, N)
+        N2 = empty()
+        gdn.gdn_block_norm(c["Y"], c["Z"], c["wo"], c["R"], c["wi"], None, N2, scale=0.5, eps=1e-5,
+                           act=act)
+        assert torch.equal(N2, N)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("parts", PARTS)
+@pytest.mark.parametrize("B,T,H,d,hm", NORM_SHAPES)
+def test_block_norm_backward(lib, dtype, act, parts, B, T, H, d, hm):
+    c = norm_case(d + T + 1, dtype, B, T, H, d, parts, hm)
+    W = H * d
+    new = lambda t: None if t is None else torch.full_like(t, 77.0)
+    dY = new(c["Y"])
+    dZ, dR, dwo, dwi = new(c["Z"]), new(c["R"]), new(c["wo"]), new(c["wi"])
+    n = gdn.gdn_block_norm_backward_workspace_bytes(c["Y"])
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    call = lambda *out: gdn.gdn_block_norm_backward(
+        c["Y"], c["Z"], c["wo"], c["R"], c["wi"], c["dX"], c["dN"], *out, ws, scale=0.5, eps=1e-5,
+        act=act)
+    call(dY, dZ, dR, dwo, dwi)
+    y, z, wo, r, wi = flat(c)
+    row = lambda t: None if t is None else f64(t).reshape(B * T, W)
+    gx, gn = row(c["dX"]), row(c["dN"])
+    dy, dz, dr, gwo, gwi = L.block_norm_backward(y, z, wo, r, wi, gx, gn, 0.5, 1e-5, act)
+    # magnitudes of the terms that the gradients are sums of
+    x, _ = L.block_norm(y, z, wo, r, wi, 0.5, 1e-5, act)
+    rx = np.sqrt((x * x).mean(-1, keepdims=True) + 1e-5)
+    mx = np.abs(x) if r is None else np.abs(r) + np.abs(x - r)
+    mdx = np.zeros_like(x) if gx is None else np.abs(gx)
+    if wi is not None:
+        g = np.abs(gn * wi)
+        mdx = mdx + g / rx + mx / rx * (g * mx).mean(-1, keepdims=True) / rx ** 2
+    ry = np.sqrt((y * y).mean(-1, keepdims=True) + 1e-5) if wo is not None else np.ones(())
+    yh = (np.abs(y) / ry).reshape(B * T, W)
+    nn = yh * (1.0 if wo is None else np.abs(wo))
+    a, da = (1.0, 0.0)
+    if z is not None:
+        s = 1.0 / (1.0 + np.exp(-z))
+        a = np.abs(z * s) if act == "silu" else s
+        da = s * (1.0 + np.abs(z) * (1.0 - s)) if act == "silu" else s * (1.0 - s)
+    mdn = 0.5 * mdx * a
+    u, k = half_step(dtype), 256 * U32
+    if r is not None:
+        near(dR.view(B * T, W), dr, u * np.abs(dr) + k * mdx, "dR")
+    if z is not None:
+        near(dZ.view(B * T, W), dz, u * np.abs(dz) + k * 0.5 * mdx * nn * da, "dZ")
+    if wo is not None:
+        near(dwo, gwo, (k + B * T * U32) * (mdn * yh).sum(0) + 1e-30, "dw_post")
+        e = (mdn * np.abs(wo)).reshape(B * T, H, d)
+        yy = yh.reshape(B * T, H, d)
+        mdy = (e + yy * (e * yy).mean(-1, keepdims=True)) / ry
+    else:
+        mdy = mdn.reshape(B * T, H, d)
+    near(dY.reshape(B * T, H, d), dy, u * np.abs(dy) + k * mdy, "dY")
+    if wi is not None:
+        near(dwi, gwi, (k + B * T * U32) * (np.abs(gn) * mx / rx).sum(0) + 1e-30, "dw_pre")
+    if r is not None and gx is not None:               # dR over dX; the same order again
+        keep = [t.clone() for t in (dY, dZ, dwo, dwi) if t is not None]
+        c["dX"] = c["dX"].clone()
+        call(dY, dZ, c["dX"], dwo, dwi)
+        assert torch.equal(c["dX"], dR)
+        assert all(torch.equal(a, b) for a, b in zip(keep, [t for t in (dY, dZ, dwo, dwi)
+                                                            if t is not None]))
+
+
+def test_block_norm_without_rows(lib):
+    Y = torch.empty(0, 4, 2, 128, device="cuda")
+    w = torch.ones(256, device="cuda")
+    dw = torch.full((256,), 77.0, device="cuda")
+    none = torch.empty(0, 4, 256, device="cuda")
+    gdn.gdn_block_norm(Y, None, w, None, None, none, None)
+    gdn.gdn_block_norm_backward(Y, None, w, None, None, none, None, torch.empty_like(Y), None,
+                                None, dw, None, None)
+    assert (dw == 0).all()
+
+
+# --------------------------------------------------------------------------- #
+# together, on other streams, in graphs
+# --------------------------------------------------------------------------- #
+def layer(dtype, B, T, seed):
+    """Inputs of one layer: a fused projection, a gate, a residual stream."""
+    g = gen(seed)
+    H, W = 4, 512
+    c = dict(qkv=rand(g, B, T, 3 * H, 128, dtype=dtype, scale=128 ** -0.25),
+             z=rand(g, B, T, W, dtype=dtype), r=rand(g, B, T, W, dtype=dtype),
+             wo=rand(g, W, scale=0.1) + 1.0, wi=rand(g, W, scale=0.1) + 1.0,
+             lg=torch.tensor([-0.5, -0.05, -0.01, -0.001]).cuda(),
+             inv=gdn.gdn_rotary_frequencies(64)[0].cuda())
+    return c, H, W
+
+
+def layer_forward(c, H, W, first, S0, T0, T1):
+    """Rows [T0, T1) of the layer: rotary, linear attention, gated norm and residual."""
+    x = c["qkv"][:, T0:T1]
+    B, T = x.shape[:2]
+    q, k = (torch.empty(B, H, T, 128, dtype=x.dtype, device="cuda") for _ in range(2))
+    pos = torch.arange(T0, T1, device="cuda").expand(B, T).contiguous() + first
+    gdn.gdn_rotary(x[:, :, :H].transpose(1, 2), x[:, :, H:2 * H].transpose(1, 2), pos, c["inv"], q,
+                   k)
+    v = x[:, :, 2 * H:].transpose(1, 2).contiguous()
+    O, S = torch.empty_like(v), torch.empty(B, H, 128, 128, device="cuda")
+    if T == 1 and S0 is not None:
+        S.copy_(S0)
+        gdn.gdn_linear_decode(q, k, v, c["lg"], S, O)
+    else:
+        ws = torch.empty(gdn.gdn_linear_forward_workspace_bytes(k, v), dtype=torch.uint8,
+                         device="cuda")
+        gdn.gdn_linear_forward(q, k, v, c["lg"], S0, O, S, ws)
+    X, N = (torch.empty(B, T, W, dtype=x.dtype, device="cuda") for _ in range(2))
+    gdn.gdn_block_norm(O.transpose(1, 2), c["z"][:, T0:T1].contiguous(), c["wo"],
+                       c["r"][:, T0:T1].contiguous(), c["wi"], X, N, scale=0.5, eps=1e-5)
+    return X, N, S
+
+
+def layer_oracle(c, H, W):
+    x = f64(c["qkv"]).transpose(0, 2, 1, 3)
+    B, _, T, _ = x.shape
+    pos = np.arange(T)[None].repeat(B, 0)
+    q, k = (L.rotary(a, pos, f64(c["inv"])) for a in (x[:, :H], x[:, H:2 * H]))
+    o = np.stack([L.linear_forward(q[b], k[b], x[b, 2 * H:], f64(c["lg"]))[0] for b in range(B)])
+    row = lambda t: f64(t).reshape(B * T, W)
+    y = o.transpose(0, 2, 1, 3).reshape(B * T, H, 128)
+    X, N = L.block_norm(y, row(c["z"]), f64(c["wo"]), row(c["r"]), f64(c["wi"]), 0.5, 1e-5)
+    return X.reshape(B, T, W), N.reshape(B, T, W)
+
+
+@pytest.mark.parametrize("dtype,tol", [("f32", 1e-5), ("bf16", 1e-2)])
+def test_layer_prompt_then_tokens(lib, dtype, tol):
+    """The run a serving program makes: a prompt, then token by token from its
+    state, against the oracle's whole layer (relative Frobenius error, the
+    suite's tolerances per type)."""
+    B, T, P = 2, 135, 131
+    c, H, W = layer(dtype, B, T, 21)
+    X, N = layer_oracle(c, H, W)
+    x, n, S = layer_forward(c, H, W, 0, None, 0, P)
+    xs, ns = [x], [n]
+    for t in range(P, T):
+        x, n, S = layer_forward(c, H, W, 0, S, t, t + 1)
+        xs.append(x)
+        ns.append(n)
+    for got, want in ((torch.cat(xs, 1), X), (torch.cat(ns, 1), N)):
+        assert np.linalg.norm(f64(got) - want) <= tol * np.linalg.norm(want)
+
+
+def test_layer_gradients_against_differences(lib):
+    """The run's gradient (norm, attention, rotary backwards) against a
+    central difference of the float64 oracle along a random direction."""
+    B, T = 1, 150
+    c, H, W = layer("f32", B, T, 22)
+    g = gen(23)
+    dX, dN = rand(g, B, T, W), rand(g, B, T, W)
+    x = c["qkv"]
+    q0, k0 = x[:, :, :H].transpose(1, 2), x[:, :, H:2 * H].transpose(1, 2)
+    v = x[:, :, 2 * H:].transpose(1, 2).contiguous()
+    q, k = (torch.empty(B, H, T, 128, device="cuda") for _ in range(2))
+    pos = torch.arange(T, device="cuda")[None]
+    gdn.gdn_rotary(q0, k0, pos, c["inv"], q, k)
+    O = torch.empty_like(v)
+    ws = torch.empty(max(gdn.gdn_linear_forward_workspace_bytes(k, v),
+                         gdn.gdn_linear_backward_workspace_bytes(k, v)), dtype=torch.uint8,
+                     device="cuda")
+    gdn.gdn_linear_forward(q, k, v, c["lg"], None, O, None, ws)
+    Y = O.transpose(1, 2)
+    wn = torch.empty(gdn.gdn_block_norm_backward_workspace_bytes(Y), dtype=torch.uint8,
+                     device="cuda")
+    dO = torch.empty_like(O)
+    dz, dr = torch.empty_like(c["z"]), torch.empty_like(c["r"])
+    dwo, dwi = torch.empty_like(c["wo"]), torch.empty_like(c["wi"])
+    gdn.gdn_block_norm_backward(Y, c["z"], c["wo"], c["r"], c["wi"], dX, dN, dO.transpose(1, 2),
+                                dz, dr, dwo, dwi, wn, scale=0.5, eps=1e-5)
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    gdn.gdn_linear_backward(q, k, v, c["lg"], None, dO, None, dq, dk, dv, None, ws)
+    dx = torch.empty_like(x)
+    gdn.gdn_rotary(dq, dk, pos, c["inv"], dx[:, :, :H].transpose(1, 2),
+                   dx[:, :, H:2 * H].transpose(1, 2), inverse=True)
+    dx[:, :, 2 * H:] = dv.transpose(1, 2)
+    got = dict(qkv=dx, z=dz, r=dr, wo=dwo, wi=dwi)
+    gX, gN = f64(dX), f64(dN)
+    h = 1e-6
+    for name, grad in got.items():
+        along = torch.randn(grad.shape, generator=g, dtype=torch.float64)
+        ends = []
+        for s in (h, -h):
+            moved = dict(c, **{name: c[name].double().cpu() + s * along})
+            X, N = layer_oracle(moved, H, W)
+            ends.append((X * gX).sum() + (N * gN).sum())
+        slope = (ends[0] - ends[1]) / (2 * h)
+        mine = float((grad.double().cpu() * along).sum())
+        scale = float((grad.double().cpu() ** 2).sum() ** 0.5)
+        assert abs(mine - slope) <= 1e-4 * scale, (name, mine, slope)
+
+
+def test_layer_on_another_stream_and_in_a_graph(lib):
+    """The same bits on a side stream, and captured and replayed on new inputs."""
+    c, H, W = layer("bf16", 2, 200, 24)
+    c2, _, _ = layer("bf16", 2, 200, 25)
+    want, want2 = layer_forward(c, H, W, 0, None, 0, 200), layer_forward(c2, H, W, 0, None, 0, 200)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = layer_forward(c, H, W, 0, None, 0, 200)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = layer_forward(c, H, W, 0, None, 0, 200)
+    for x, w in ((c, want), (c2, want2)):
+        for name in ("qkv", "z", "r", "wo", "wi"):
+            c[name].copy_(x[name]) if x is not c else None
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+def test_binding_checks_shapes_and_types(lib):
+    c = linear_case(30, "bf16", 1, 1, 2, 64, None, False)
+    O = torch.empty_like(c["V"])
+    bad = [dict(Q=c["Q"][:, :, :32].contiguous()), dict(V=c["V"].float()),
+           dict(lg=c["lg"].double()), dict(lg=c["lg"][:1]), dict(K=c["K"].cpu()),
+           dict(V=c["V"].transpose(2, 3).contiguous().transpose(2, 3))]
+    for change in bad:
+        a = dict(c, **change)
+        with pytest.raises((ValueError, TypeError)):
+            gdn.gdn_linear_forward(a["Q"], a["K"], a["V"], a["lg"], None, O, None, None)
+    with pytest.raises(ValueError):
+        gdn.gdn_linear_forward(c["Q"], c["K"], c["V"], c["lg"], torch.zeros(2, 2, 128, 128).cuda(),
+                               O, None, None)
+    y = torch.zeros(1, 2, 1, 16, device="cuda")
+    with pytest.raises(ValueError):
+        gdn.gdn_block_norm(y, None, torch.ones(8).cuda(), None, None, torch.zeros(1, 2, 16).cuda(),
+                           None)
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_block_norm(y, None, None, None, None, None, None)
