@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["api.cu", "simt.cu", "tc.cu", "scan.cu", "forward_static.cu", "decode.cu", "linear.cu",
-           "norm.cu", "rotary.cu"]
+           "linear_tc.cu", "norm.cu", "rotary.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE]

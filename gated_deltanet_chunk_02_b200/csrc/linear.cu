@@ -116,7 +116,7 @@ struct SimtSmem {
 // each CTA carries 32 rows of the state, so four share a head and form the
 // chunk's scores again, which costs less than passing them on: the float32
 // peak of the CUDA cores is the bound either way.
-template <typename T, bool STATE_ONLY, bool REV>
+template <bool STATE_ONLY, bool REV>
 __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
                              int v0, SimtSmem& s) {
     const int tid = threadIdx.x;
@@ -142,9 +142,9 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
         const int64_t H = p.Hv / group;
         return ((g.b * H + hv / group) * p.T + g.t0) * kLinD;
     };
-    const T* ga = (const T*)q.a + base(q.ga);
-    const T* gb = (const T*)q.b + base(q.gb);
-    const T* gc = (const T*)q.c + base(q.gc) + v0;
+    const float* ga = (const float*)q.a + base(q.ga);
+    const float* gb = (const float*)q.b + base(q.gb);
+    const float* gc = (const float*)q.c + base(q.gc) + v0;
     const int64_t ob = ((g.b * p.Hv + hv) * p.T + g.t0) * kLinD + v0;
     const int64_t nch = (g.n + kSimtC - 1) / kSimtC;
     for (int64_t ci = 0; ci < nch; ++ci) {
@@ -156,18 +156,15 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
             if (r < n) {
                 const int64_t o = (r0 + r) * kLinD + c;
-                if (!STATE_ONLY)
-                    x = make_float4(ld_elem(ga, o), ld_elem(ga, o + 1), ld_elem(ga, o + 2),
-                                    ld_elem(ga, o + 3));
-                y = make_float4(ld_elem(gb, o), ld_elem(gb, o + 1), ld_elem(gb, o + 2),
-                                ld_elem(gb, o + 3));
+                if (!STATE_ONLY) x = *reinterpret_cast<const float4*>(ga + o);
+                y = *reinterpret_cast<const float4*>(gb + o);
             }
             if (!STATE_ONLY) *reinterpret_cast<float4*>(&s.a[r][c]) = x;
             *reinterpret_cast<float4*>(&s.b[r][c]) = y;
         }
         for (int e = tid; e < kSimtC * kSimtDV; e += kSimtThreads) {
             const int r = e / kSimtDV, c = e % kSimtDV;
-            s.ct[c][r] = r < n ? ld_elem(gc, (r0 + r) * kLinD + c) : 0.f;
+            s.ct[c][r] = r < n ? gc[(r0 + r) * kLinD + c] : 0.f;
         }
         __syncthreads();
         if (!STATE_ONLY) {
@@ -258,10 +255,8 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
                     const float d = q.s_inter * (REV ? s.dec[n - 1 - i] : s.dec[i + 1]);
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const float o = fmaf(d, st[u][w], in[u][w]);
-                        const int64_t at = ob + (r0 + i) * kLinD + cj + 8 * w;
-                        if (q.out_f32) static_cast<float*>(q.out)[at] = o;
-                        else st_elem(static_cast<T*>(q.out), at, o);
+                        static_cast<float*>(q.out)[ob + (r0 + i) * kLinD + cj + 8 * w] =
+                            fmaf(d, st[u][w], in[u][w]);
                     }
                 }
             }
@@ -321,7 +316,7 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
 }
 
 // grid: (segments or boundaries, 4 Hv, problems)
-template <typename T, bool STATE_ONLY>
+template <bool STATE_ONLY>
 __global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtSmem& s = *reinterpret_cast<SimtSmem*>(raw);
@@ -334,25 +329,24 @@ __global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
         g.t0 = g.seq_t0 + g.k * p.seg_len;
         g.n = g.seq_n - g.k * p.seg_len < p.seg_len ? g.seq_n - g.k * p.seg_len : p.seg_len;
     }
-    if (q.reverse) simt_segment<T, STATE_ONLY, true>(p, q, g, hv, v0, s);
-    else simt_segment<T, STATE_ONLY, false>(p, q, g, hv, v0, s);
+    if (q.reverse) simt_segment<STATE_ONLY, true>(p, q, g, hv, v0, s);
+    else simt_segment<STATE_ONLY, false>(p, q, g, hv, v0, s);
 }
 
-template <typename T>
 cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t bounds, bool states,
                      cudaStream_t st) {
     const int smem = (int)sizeof(SimtSmem);
     if (states) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<T, true>,
+        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<true>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        k_linear_simt<T, true><<<dim3((unsigned)bounds, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
+        k_linear_simt<true><<<dim3((unsigned)bounds, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
                                  smem, st>>>(a);
     } else {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<T, false>,
+        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        k_linear_simt<T, false><<<dim3((unsigned)segs, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
+        k_linear_simt<false><<<dim3((unsigned)segs, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
                                   smem, st>>>(a);
     }
     return cudaGetLastError();
@@ -381,8 +375,7 @@ int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int 
 LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16) {
     LinPlan pl;
     const bool packed = s.nseq > 0;
-    (void)bf16;
-    pl.seg_len = pick_segment(nprob, packed ? 1 : s.B, s.Hv, s.T, 4);
+    pl.seg_len = pick_segment(nprob, packed ? 1 : s.B, s.Hv, s.T, bf16 ? 1 : 4);
     // boundaries: a sequence of n rows has at most n / seg_len
     const int64_t m = s.T <= pl.seg_len ? 1 : (s.T + pl.seg_len - 1) / pl.seg_len;
     pl.bounds = packed ? (s.T <= pl.seg_len ? 0 : s.T / pl.seg_len) : s.B * (m - 1);
@@ -400,16 +393,16 @@ cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool 
     for (int i = 0; i < nprob; ++i) a.pr[i].ws = (float*)((uint8_t*)ws + i * pl.state_bytes);
     cudaError_t e;
     if (pl.bounds > 0) {
-        e = bf16 ? run_simt<__nv_bfloat16>(a, nprob, pl.segs, pl.bounds, true, st)
-                 : run_simt<float>(a, nprob, pl.segs, pl.bounds, true, st);
+        e = bf16 ? launch_linear_tc(a, nprob, pl, true, st)
+                 : run_simt(a, nprob, pl.segs, pl.bounds, true, st);
         if (e != cudaSuccess) return e;
         k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), kLinState / 1024, nprob), 256, 0, st>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         *launches += 2;
     }
-    e = bf16 ? run_simt<__nv_bfloat16>(a, nprob, pl.segs, pl.bounds, false, st)
-             : run_simt<float>(a, nprob, pl.segs, pl.bounds, false, st);
+    e = bf16 ? launch_linear_tc(a, nprob, pl, false, st)
+             : run_simt(a, nprob, pl.segs, pl.bounds, false, st);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -141,6 +141,9 @@ LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16);
 // ws: nprob * state_bytes; *launches counts the kernels
 cudaError_t launch_linear(const LinArgs& a, int nprob, const LinPlan& pl, bool bf16, void* ws,
                           int* launches, cudaStream_t st);
+// one of the two tensor-core kernels (linear_tc.cu): the boundary states, or the outputs
+cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, bool states,
+                             cudaStream_t st);
 // out[b, h] = sum of part[b, h * group + g] over g, float32 -> the data type
 cudaError_t launch_linear_group_sum(const LinArgs& a, const float* part, void* out, int group,
                                     bool bf16, cudaStream_t st);
