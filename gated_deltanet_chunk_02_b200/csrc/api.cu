@@ -579,7 +579,7 @@ int gdn_linear_forward(const void* Q, const void* K, const void* V, const float*
     if (pl.state_bytes > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
     const int group = (int)(s.Hv / s.Hk);
     gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
-    a.pr[0] = {Q, K, V, O, group, group, 1, 0, 0, S0, 0, S_final, scale, scale, 1.f, nullptr};
+    a.pr[0] = {Q, K, V, O, group, group, 1, 0, 0, S0, 0, S_final, scale, 1.f, 1.f, nullptr};
     int kernels = 0;
     return launched(gdn::launch_linear(a, 1, pl, dtype == GDN_BF16, workspace, &kernels,
                                        (cudaStream_t)stream),
@@ -622,10 +622,10 @@ int gdn_linear_backward(const void* Q, const void* K, const void* V, const float
     const int f32 = group > 1;
     gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
     a.pr[0] = {dO, V, K, f32 ? (void*)pq : dQ, 1, 1, group, 0, f32, S0, 1, nullptr,
-               scale, scale, 1.f, nullptr};
+               scale, 1.f, 1.f, nullptr};
     a.pr[1] = {V, dO, Q, f32 ? (void*)pk : dK, 1, 1, group, 1, f32, dS_final, 1, nullptr,
-               scale, 1.f, scale, nullptr};
-    a.pr[2] = {K, Q, dO, dV, group, group, 1, 1, 0, dS_final, 0, dS0, scale, 1.f, scale, nullptr};
+               1.f, scale, scale, nullptr};
+    a.pr[2] = {K, Q, dO, dV, group, group, 1, 1, 0, dS_final, 0, dS0, 1.f, scale, scale, nullptr};
     cudaStream_t st = (cudaStream_t)stream;
     int kernels = 0;
     GDN_TRY(launched(gdn::launch_linear(a, 3, pl, bf16, workspace, &kernels, st),

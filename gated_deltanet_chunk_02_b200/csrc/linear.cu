@@ -61,13 +61,25 @@ __global__ void __launch_bounds__(256) k_lin_combine(const LinArgs p) {
                             s[(c + 3) * kLinD + r]);
         }
     }
-    for (int i = 0; i < g.m - 1; ++i) {
-        const int k = q.reverse ? g.m - 2 - i : i;
-        const float a = q.reverse && i == 0 ? a_last : a_full;
-        float4* at = reinterpret_cast<float4*>(q.ws + ((g.slot0 + k) * p.Hv + hv) * kLinState + e);
-        const float4 u = *at;
-        m = make_float4(fmaf(a, m.x, u.x), fmaf(a, m.y, u.y), fmaf(a, m.z, u.z), fmaf(a, m.w, u.w));
-        *at = m;
+    float4* const base = reinterpret_cast<float4*>(q.ws + (g.slot0 * p.Hv + hv) * kLinState + e);
+    const int64_t step = p.Hv * kLinState / 4;
+    constexpr int kAhead = 8;                          // loads in flight
+    for (int i0 = 0; i0 < g.m - 1; i0 += kAhead) {
+        float4 u[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i < g.m - 1) u[j] = base[(q.reverse ? g.m - 2 - i : i) * step];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j;
+            if (i >= g.m - 1) break;
+            const float a = q.reverse && i == 0 ? a_last : a_full;
+            m = make_float4(fmaf(a, m.x, u[j].x), fmaf(a, m.y, u[j].y), fmaf(a, m.z, u[j].z),
+                            fmaf(a, m.w, u[j].w));
+            base[(q.reverse ? g.m - 2 - i : i) * step] = m;
+        }
     }
 }
 
@@ -199,7 +211,7 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int i = ti + 16 * u, j = tj + 16 * w, dist = REV ? j - i : i - j;
-                        s.pm[i][j] = dist >= 0 ? q.s_intra * s.dec[dist] * acc[u][w] : 0.f;
+                        s.pm[i][j] = dist >= 0 ? q.s_weight * s.dec[dist] * acc[u][w] : 0.f;
                     }
             }
             __syncthreads();
@@ -252,11 +264,11 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
                 for (int u = 0; u < 2; ++u) {
                     const int i = ri + 32 * u;
                     if (i >= n) continue;
-                    const float d = q.s_inter * (REV ? s.dec[n - 1 - i] : s.dec[i + 1]);
+                    const float d = REV ? s.dec[n - 1 - i] : s.dec[i + 1];
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         static_cast<float*>(q.out)[ob + (r0 + i) * kLinD + cj + 8 * w] =
-                            fmaf(d, st[u][w], in[u][w]);
+                            q.s_out * fmaf(d, st[u][w], in[u][w]);
                     }
                 }
             }
@@ -353,18 +365,21 @@ cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t bounds, 
 }
 
 // Segment length (a multiple of 128): one segment per sequence when that fills
-// the GPU, else as many as bring the two passes' steps down.  A step is a
-// chunk of 128 rows on one SM (CTA); the state pass costs about half of an
-// output step, and cutting at all costs two launches and the states' traffic,
-// about four steps.
+// the GPU, else as many as bring the two passes' time down.  In units of half
+// an output step (a chunk of 128 rows on one SM): the state pass takes one per
+// chunk; a CTA's start two in step 3 and one in step 1; a boundary's state
+// moves 256 KB, as much as two output steps; two more launches cost eight.
 int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int ctas_per_head) {
     const int64_t chunks = (rows + 127) / 128, sms = sm_count();
-    const int64_t lines = nprob * nseq * Hv * ctas_per_head;
+    const int64_t lines = nprob * nseq * Hv;
     int64_t best = chunks, cost = INT64_MAX;
-    for (int64_t m = 1; m <= chunks && m <= 64; ++m) {
+    for (int64_t m = 1; m <= chunks && m <= 128; ++m) {
         const int64_t len = (chunks + m - 1) / m;
-        const int64_t waves = (lines * m + sms - 1) / sms, waves1 = (lines * (m - 1) + sms - 1) / sms;
-        const int64_t c = 2 * waves * len + (m > 1 ? waves1 * len + 8 : 0);
+        if ((chunks + len - 1) / len != m) continue;   // the same cut with fewer pieces is listed
+        const int64_t waves = (lines * ctas_per_head * m + sms - 1) / sms;
+        const int64_t waves1 = (lines * ctas_per_head * (m - 1) + sms - 1) / sms;
+        const int64_t c = waves * (2 * len + 2) +
+                          (m > 1 ? waves1 * (len + 1) + 4 * lines * (m - 1) / sms + 8 : 0);
         if (c < cost) { cost = c; best = len; }
     }
     return best < 1 ? 128 : 128 * best;

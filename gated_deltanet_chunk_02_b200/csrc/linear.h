@@ -12,9 +12,9 @@ constexpr int kLinState = kLinD * kLinD;               // floats of one state
 
 // One decayed linear attention.  With queries a, keys b, values c of one head
 // and lambda = exp(loggate):
-//   forward:  out_i = s_intra sum_{j<=i} lambda^(i-j) (a_i.b_j) c_j + s_inter lambda^(i+1) M a_i
+//   forward:  out_i = s_out [ s_weight sum_{j<=i} lambda^(i-j) (a_i.b_j) c_j + lambda^(i+1) M a_i ]
 //             M'    = lambda^n M + s_state sum_j lambda^(n-1-j) c_j b_j^T
-//   reverse:  out_i = s_intra sum_{j>=i} lambda^(j-i) (a_i.b_j) c_j + s_inter lambda^(n-1-i) M a_i
+//   reverse:  out_i = s_out [ s_weight sum_{j>=i} lambda^(j-i) (a_i.b_j) c_j + lambda^(n-1-i) M a_i ]
 //             M'    = lambda^n M + s_state sum_j lambda^(j+1) c_j b_j^T
 // over n rows whose incoming state is M (entering at the first row, or at the
 // last one if reverse).  The forward pass is (a, b, c) = (q, k, v); the
@@ -28,7 +28,7 @@ struct LinProblem {
     int out_f32;               // out is float32 whatever the data type
     const float* m0; int m0_t; // incoming state of each sequence (or null); transposed
     float* mout;               // outgoing state of each sequence (or null)
-    float s_intra, s_inter, s_state;
+    float s_out, s_weight, s_state;
     float* ws;                 // states at the segment boundaries [boundary][Hv][128][128]
 };
 constexpr int kLinProblems = 3;
@@ -158,6 +158,12 @@ __device__ __forceinline__ double lin_log2(const float* loggate, int hv) {
 __device__ __forceinline__ float lin_pow(double lg, int64_t n) {
     const double x = lg * (double)n, i = rint(x);
     return ldexpf(exp2f((float)(x - i)), (int)fmin(fmax(i, -1000.0), 1000.0));
+}
+// the same as a sum of two floats
+__device__ __forceinline__ void lin_pow2(double lg, int64_t n, float& hi, float& lo) {
+    const double x = exp2(fmin(fmax(lg * (double)n, -1000.0), 1000.0));
+    hi = (float)x;
+    lo = (float)(x - (double)hi);
 }
 
 }  // namespace gdn

@@ -4,31 +4,39 @@
 // k_linear_tc walks one segment of one head in chunks of 128 rows.  Per chunk
 // (a, b, c: queries, keys, values; M: the incoming state, rows d_c, columns d_b;
 // all products 128 x 128 x 128, fp32 accumulators in TMEM):
-//   Sc = a b^T                    -> P_ij = s lambda^|i-j| Sc_ij on the causal side, bf16
-//   O1 = a M^T,  O2 = P c         -> out_i = lambda^(i+1) O1_i + O2_i
-//   Mu = c^T (w b)                -> M <- lambda^n M + Mu,  w_j = lambda^(n-1-j)
-// O1 and O2 keep accumulators of their own because their rows decay
-// differently, and a power of lambda below 1 cannot be divided out of a row.
-// The state lives in fp32 registers of the state warps; only its copy as an
-// operand of O1 is rounded to bf16.  w b is split into two bf16 parts, hi + lo,
-// and Mu takes a product with each (c is exact in bf16): the update then
-// carries 2^-17 per term instead of 2^-9, which the fp32 state is returned
-// with.  P goes back to TMEM (A operand), over Sc.
+//   Sc = a b^T              -> P_ij = s lambda^|i-j| Sc_ij / d_i on the causal side, bf16
+//   O  = a M^T + P c        -> out_i = s_out d_i O_i,  d_i = lambda^(i+1)
+//   Mu = c^T (w b)          -> M <- lambda^n M + Mu,   w_j = lambda^(n-1-j)
+// Both terms of an output share one accumulator: the row's decay d_i is taken
+// out of its weights.  d_i stops at 2^-60, so that the weights stay in range;
+// the state then reaches rows it should reach with less than 2^-60 with 2^-60,
+// far below the rounding of anything it could matter to.
 //
-// Bound: the tensor pipe needs five products (1.9 us at 11 TFLOP/s per SM) and
-// the 128 KB in and out 3.0 us per chunk at 1/148 of the copy bandwidth, so the
-// aim is to stream.  One CTA per SM, 18 warps, one thread each for TMA and MMA:
-//   warps 0-7   P from Sc, outputs from O1 and O2 (row = TMEM lane, half the columns)
-//   warps 8-15  hi + lo from b, the state
-//   warp 16     TMA: b, a, c of each chunk into a ring of five 32 KB tiles
-//   warp 17     MMA: Sc, O1, O2, Mu in this order, so that the next chunk's Sc
-//               follows Mu while this chunk's outputs and state are drained
-// hi overwrites b's tile (Sc has read it), lo and the bf16 state have a tile
-// each: 7 x 32 KB.  Every wait is bounded (2 s): on expiry the status word is
-// set and all roles leave.
+// The state lives in fp32 registers; only its copy as an operand of O is
+// rounded to bf16, and so is P (each term of an output passes one rounding).
+// w b is split into three bf16 parts, lo + mid + hi, and Mu takes a product
+// with each, smallest first: c is exact in bf16, so the update carries fp32
+// accuracy (two parts left 2e-6 in a returned state, three 2e-7).  Mu is
+// drained into the registers after every chunk: accumulation in TMEM rounds
+// towards zero, and over a segment that alone would cost 1e-5.
 //
-// k_linear_state_tc is step 1: Mu alone over a whole segment, with
-// w_j = lambda^(rows to the segment's end), accumulated in TMEM.
+// Bound: six products (3100 cycles of the tensor pipe) and 128 KB in and out per
+// chunk (5600 cycles at 1/148 of the copy bandwidth), so the aim is to stream.
+// One CTA per SM, 14 warps:
+//   warps 0-3   P from Sc; the previous chunk's outputs (lane = row)
+//   warps 4-11  the parts of w b; the state (lane = row, half the columns)
+//   warp 12     TMA: b, a, c of each chunk into a ring of five 32 KB tiles
+//   warp 13     MMA: Sc, a M^T, Mu (lo, mid, hi), P c
+// hi overwrites b's tile (Sc has read it), mid has a tile, and lo takes the
+// bf16 state's (a M^T has read it): 7 x 32 KB.  O has two accumulators, so that
+// a chunk's outputs leave while the next is formed; P goes back to TMEM (A
+// operand) over Sc.  The warps' loops are kept rolled: unrolled, the roles'
+// code (80 KB a chunk) ran at the rate it could be fetched, 11000 cycles a
+// chunk.  Every wait is bounded (2 s): on expiry the status word is set and
+// all roles leave.
+//
+// k_linear_state_tc is step 1: the state part alone.
+#include <cstddef>
 #include <cstring>
 
 #include "linear.h"
@@ -39,7 +47,7 @@ namespace tcg {
 
 constexpr int kLtTile = kRows * kD * 2;                // one bf16 [2][128][64] operand: 32 KB
 constexpr int kLtRing = 5;
-constexpr int kLtThreads = 18 * 32;
+constexpr int kLtThreads = 14 * 32;
 
 struct LinTcArgs {
     CUtensorMap map[4];                                // the call's distinct tensors
@@ -47,29 +55,57 @@ struct LinTcArgs {
     LinArgs a;
 };
 
-struct __align__(8) LtCtrl {
+struct __align__(16) LtCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t sc, p, split, o, drained, mu, state, drain;
-    float pw[kRows];                                   // s_intra lambda^n
-    float step[32];                                    // lambda^(31 - n), lambda^n if reverse
+    uint64_t sc, am, p, parts, o, drained, mu, state, drain;
+    __align__(16) float pw[kRows];                     // s lambda^n
+    __align__(16) float step[32];                                    // lambda^(31 - n), lambda^n if reverse
     uint32_t tmem;
     int abort;
 };
 constexpr int kLtSmem = 7 * kLtTile + (int)sizeof(LtCtrl);
 static_assert(kLtSmem <= 232448, "shared memory budget");
+static_assert(offsetof(LtCtrl, step) % 16 == 0, "step is read 16 bytes at a time");
 
-// eight bf16 of one 16-byte group times w, as hi + lo
-__device__ __forceinline__ void split8(const uint4& u, float w, uint4& hi, uint4& lo) {
+// Bounded wait; false once it ran out or another role's did.
+__device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
+    if (mbar_try(b, parity)) return true;
+    unsigned long long t0 = 0;
+    for (int i = 0;; ++i) {
+        if (mbar_try(b, parity)) return true;
+        if ((i & 63) == 63) {
+            if (*(volatile int*)abort) return false;
+            const unsigned long long t = gtime();
+            if (!t0) t0 = t;
+            if (t - t0 > kTimeoutNs) break;
+        }
+    }
+    atomicExch(abort, 1);
+    raise_status(status, kStatusTimeout);
+    return false;
+}
+
+// the same for a whole warp, with one answer
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
+    return __all_sync(0xffffffffu, lt_wait(b, parity, abort, status));
+}
+
+// eight bf16 of one 16-byte group times w, as hi + mid + lo
+__device__ __forceinline__ void split8(const uint4& u, float w, uint4& hi, uint4& mid, uint4& lo) {
     const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-    uint32_t h[4], l[4];
+    uint32_t h[4], m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float a = __uint_as_float(x[i] << 16) * w;
-        const float b = __uint_as_float(x[i] & 0xffff0000u) * w;
+        float a = __uint_as_float(x[i] << 16) * w;
+        float b = __uint_as_float(x[i] & 0xffff0000u) * w;
         h[i] = pack_b2(a, b);
-        l[i] = pack_b2(a - __uint_as_float(h[i] << 16), b - __uint_as_float(h[i] & 0xffff0000u));
+        a -= __uint_as_float(h[i] << 16);
+        b -= __uint_as_float(h[i] & 0xffff0000u);
+        m[i] = pack_b2(a, b);
+        l[i] = pack_b2(a - __uint_as_float(m[i] << 16), b - __uint_as_float(m[i] & 0xffff0000u));
     }
     hi = make_uint4(h[0], h[1], h[2], h[3]);
+    mid = make_uint4(m[0], m[1], m[2], m[3]);
     lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 // 32 values -> 16 TMEM columns of bf16 pairs
@@ -91,169 +127,255 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8]) {
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-__device__ __forceinline__ uint32_t lt_op_kmajor(uint32_t base, int kk) {
-    return base + (kk >> 2) * (kRows * 128) + (kk & 3) * 32;
+// one arrival for the warp, behind what all its lanes did
+__device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
 }
-
-// rows n .. 127 of a tile become zero (this thread's row r, column half h)
-__device__ __forceinline__ void zero_row(uint32_t tile, int r, int h) {
+// D (+)= A B over 128: both K-major, A in TMEM with B MN-major, both MN-major.
+// A step of 16 is 32 bytes on in a K-major operand (64 columns to a half) and
+// 2048 in an MN-major one.
+__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b) {
+    const uint64_t da = sdesc(a, 16, 1024), db = sdesc(b, 16, 1024);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) sts128(tile + op_off(r, 8 * h + q), make_uint4(0, 0, 0, 0));
-}
-// b's row r (column half h) times w into hi (in place) and lo; zero if off
-__device__ __forceinline__ void split_row(uint32_t tile, uint32_t lo_tile, int r, int h, float w,
-                                          bool on) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const uint32_t at = op_off(r, 8 * h + q);
-        uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
-        if (on) split8(lds128(tile + at), w, hi, lo);
-        sts128(tile + at, hi);
-        sts128(lo_tile + at, lo);
+    for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t o = ((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4;
+        mma_ss(d, da + o, db + o, idesc_f16(1, 0, 0, 128, 128), kk > 0);
     }
+}
+__device__ __forceinline__ void mma_pc(uint32_t d, uint32_t a, uint32_t b) {
+    const uint64_t db = sdesc(b, kRows * 128, 1024);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_ts(d, a + kk * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128), 1);
+}
+__device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool fresh) {
+    const uint64_t da = sdesc(a, kRows * 128, 1024), db = sdesc(b, kRows * 128, 1024);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_ss(d, da + kk * 128, db + kk * 128, idesc_f16(1, 1, 1, 128, 128), !fresh || kk > 0);
 }
 
 __device__ __forceinline__ int lt_row0(const LinArgs& p, const LinSeg& g, int hv, int group) {
     const int64_t H = p.Hv / group;
     return (int)((g.b * H + hv / group) * p.T + g.t0);
 }
+__device__ __forceinline__ int lt_slot(int t) { return t % kLtRing; }
+__device__ __forceinline__ uint32_t lt_phase(int t) { return (uint32_t)(t / kLtRing) & 1; }
 
-// The bounded waits of one CTA.
-struct LtWait {
-    LtCtrl* c;
-    int* status;
-    __device__ bool live() const { return *(const volatile int*)&c->abort == 0; }
-    __device__ bool operator()(uint64_t* b, uint32_t parity) const {
-        if (!live()) return false;
-        if (mbar_wait(b, parity)) return true;
-        atomicExch(&c->abort, 1);
-        raise_status(status, kStatusTimeout);
-        return false;
+// this thread's row r of the incoming state, columns 64 h ..
+__device__ __forceinline__ void load_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
+                                           int hv, bool rev, int r, int h, float (&m)[64]) {
+    const bool first = rev ? g.k == g.m - 1 : g.k == 0;
+    const float* src = nullptr;
+    bool across = false;
+    if (!first) {
+        src = q.ws + ((g.slot0 + (rev ? g.k : g.k - 1)) * p.Hv + hv) * kLinState;
+    } else if (q.m0) {
+        src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
+        across = q.m0_t != 0;
     }
+#pragma unroll
+    for (int i = 0; i < 64; ++i) m[i] = 0.f;
+    if (src && across) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m[i] = src[(64 * h + i) * kD + r];
+    } else if (src) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(src + r * kD + 64 * h + i);
+            m[i] = f.x; m[i + 1] = f.y; m[i + 2] = f.z; m[i + 3] = f.w;
+        }
+    }
+}
+__device__ __forceinline__ void store_state(float* dst, int r, int h, const float (&m)[64]) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(m[i + e]);
+        st_global32(dst + r * kD + 64 * h + i, w);
+    }
+}
+// M <- (a + a_lo) M + Mu: a's own rounding would add up over the chunks that a
+// slow decay remembers
+__device__ __forceinline__ void take_update(uint32_t mu, float a, float a_lo, float (&m)[64]) {
+#pragma unroll
+    for (int pc = 0; pc < 2; ++pc) {
+        float u[32];
+        tmem_ld32(mu + 32 * pc, u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m[32 * pc + i] = fmaf(a, m[32 * pc + i], fmaf(a_lo, m[32 * pc + i], u[i]));
+    }
+}
+// row r (columns 64 h ..) of b times w: hi in its place, mid and lo in their
+// tiles.  Rows that are not this segment's (off) may hold anything: zero.
+__device__ __forceinline__ void split_row(uint32_t b, uint32_t mid_tile, uint32_t lo_tile, int r,
+                                          int h, float w, bool off) {
+#pragma unroll 2
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t at = op_off(r, 8 * h + e);
+        uint4 u = lds128(b + at), hi, mid, lo;
+        if (off) u = make_uint4(0, 0, 0, 0);
+        split8(u, w, hi, mid, lo);
+        sts128(b + at, hi);
+        sts128(mid_tile + at, mid);
+        sts128(lo_tile + at, lo);
+    }
+}
+__device__ __forceinline__ void zero_row(uint32_t tile, int r, int h) {
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) sts128(tile + op_off(r, 8 * h + q), make_uint4(0, 0, 0, 0));
+}
+
+// ---- the roles of k_linear_tc ----
+struct LtWalk {                                        // chunks of a segment, in walking order
+    int n, nch;
+    bool rev;
+    __device__ int first(int ci) const { return (rev ? nch - 1 - ci : ci) * kRows; }
+    __device__ int rows(int r0) const { return n - r0 < kRows ? n - r0 : kRows; }
 };
 
-template <bool REV>
-__device__ void lt_segment(const LinTcArgs& k, const LinProblem& q, const LinSeg& g, int hv,
-                           uint8_t* smem, LtCtrl* ctrl) {
-    const LinArgs& p = k.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const LtWait wait{ctrl, p.status};
-    const int nch = (int)((g.n + kRows - 1) / kRows);
-    const uint32_t tm = ctrl->tmem;
-    const uint32_t tSc = tm, tO1 = tm + 128, tO2 = tm + 256, tMu = tm + 384;
-    const uint32_t tiles = su32(smem), lo_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
-    const double lg = lin_log2(p.loggate, hv);
-    // chunk number ci of the walk: its first row in the segment, its rows
-    auto first_row = [&](int ci) { return (REV ? nch - 1 - ci : ci) * kRows; };
-    auto rows_of = [&](int r0) { return (int)(g.n - r0 < kRows ? g.n - r0 : kRows); };
-    // tile number 3 ci + {0: b, 1: a, 2: c} of the ring
-    auto slot = [](int t) { return t % kLtRing; };
-    auto phase = [](int t) { return (uint32_t)(t / kLtRing) & 1; };
+__device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g, int hv,
+                        const LtWalk& wk, uint8_t* smem, LtCtrl* c) {
+    const int z = blockIdx.z;
+    const CUtensorMap *mb = &k.map[k.ib[z]], *ma = &k.map[k.ia[z]], *mc = &k.map[k.ic[z]];
+    const int yb = lt_row0(k.a, g, hv, q.gb), ya = lt_row0(k.a, g, hv, q.ga),
+              yc = lt_row0(k.a, g, hv, q.gc);
+    int t = 0;
+    for (; t < 3 * wk.nch; ++t) {
+        const int s = lt_slot(t), m = t % 3, r0 = wk.first(t / 3);
+        if (t >= kLtRing && !lt_wait(&c->empty[s], lt_phase(t) ^ 1, &c->abort, k.a.status)) break;
+        const CUtensorMap* mp = m == 0 ? mb : (m == 1 ? ma : mc);
+        const int y = r0 + (m == 0 ? yb : (m == 1 ? ya : yc));
+        mbar_expect_tx(&c->full[s], kLtTile);
+        tma_load_2d(smem + s * kLtTile, mp, 0, y, &c->full[s]);
+        tma_load_2d(smem + s * kLtTile + kRows * 128, mp, 64, y, &c->full[s]);
+    }
+    // whatever stopped the walk, copies in flight land before the CTA ends
+    for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
+        mbar_wait(&c->full[lt_slot(i)], lt_phase(i));
+}
 
-    if (warp == 16) {
-        if (lane == 0) {
-            const int z = blockIdx.z;
-            const CUtensorMap* mp[3] = {&k.map[k.ib[z]], &k.map[k.ia[z]], &k.map[k.ic[z]]};
-            const int row[3] = {lt_row0(p, g, hv, q.gb), lt_row0(p, g, hv, q.ga),
-                                lt_row0(p, g, hv, q.gc)};
-            int t = 0;
-            for (; t < 3 * nch; ++t) {
-                const int s = slot(t), m = t % 3, y = row[m] + first_row(t / 3);
-                if (t >= kLtRing && !wait(&ctrl->empty[s], phase(t) ^ 1)) break;
-                if (!wait.live()) break;
-                mbar_expect_tx(&ctrl->full[s], kLtTile);
-                tma_load_2d(smem + s * kLtTile, mp[m], 0, y, &ctrl->full[s]);
-                tma_load_2d(smem + s * kLtTile + kRows * 128, mp[m], 64, y, &ctrl->full[s]);
-            }
-            // whatever stopped the walk, copies in flight land before the CTA ends
-            for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
-                mbar_wait(&ctrl->full[slot(i)], phase(i));
+__device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* status) {
+    const uint32_t tSc = c->tmem, tO = tSc + 128, tMu = tSc + 384;
+    const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
+    int* const ab = &c->abort;
+    for (int ci = 0; ci < wk.nch; ++ci) {
+        const uint32_t par = ci & 1;
+        const int tb = 3 * ci, ta = tb + 1, tc = tb + 2;
+        const uint32_t sb = tiles + lt_slot(tb) * kLtTile, sa = tiles + lt_slot(ta) * kLtTile,
+                       sv = tiles + lt_slot(tc) * kLtTile, to = tO + 128 * par;
+        if (!lt_wait(&c->full[lt_slot(tb)], lt_phase(tb), ab, status) ||
+            !lt_wait(&c->full[lt_slot(ta)], lt_phase(ta), ab, status) ||
+            (ci > 0 && !lt_wait(&c->o, par ^ 1, ab, status)) ||    // P c of the last chunk is done
+            (ci > 1 && !lt_wait(&c->drained, par, ab, status)))    // outputs of ci - 2 have left
+            break;
+        tc_fence_after();
+        mma_kk(tSc, sa, sb);
+        mma_commit(&c->sc);
+        if (!lt_wait(&c->state, par, ab, status)) break;
+        tc_fence_after();
+        mma_kk(to, sa, m_tile);
+        mma_commit(&c->am);
+        mma_commit(&c->empty[lt_slot(ta)]);
+        if (!lt_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, status) ||
+            !lt_wait(&c->parts, par, ab, status) || !lt_wait(&c->p, par, ab, status))
+            break;
+        tc_fence_after();
+        mma_pc(to, tSc, sv);
+        mma_commit(&c->o);
+        mma_mm(tMu, sv, m_tile, true);                 // lo
+        mma_mm(tMu, sv, mid_tile, false);
+        mma_mm(tMu, sv, sb, false);                    // hi
+        mma_commit(&c->mu);
+        mma_commit(&c->empty[lt_slot(tb)]);
+        mma_commit(&c->empty[lt_slot(tc)]);
+    }
+    mma_commit(&c->drain);                             // nothing in flight when TMEM is freed
+    mbar_wait(&c->drain, 0);
+}
+
+// one row's outputs from its accumulator, to global memory
+__device__ __forceinline__ void lt_output(uint32_t to, float d, bool in, const LinProblem& q,
+                                          int64_t at, LtCtrl* c, int lane) {
+#pragma unroll 1
+    for (int pc = 0; pc < 4; ++pc) {
+        float x[32];
+        tmem_ld32(to + 32 * pc, x);
+        if (pc == 3) {
+            tc_fence_before();
+            warp_arrive(&c->drained, lane);
         }
-    } else if (warp == 17) {
-        if (lane == 0) {
-            constexpr uint32_t idKK = idesc_f16(1, 0, 0, 128, 128);
-            constexpr uint32_t idKM = idesc_f16(1, 0, 1, 128, 128);
-            constexpr uint32_t idMM = idesc_f16(1, 1, 1, 128, 128);
-            bool ok = true;
-            for (int ci = 0; ci < nch && ok; ++ci) {
-                const uint32_t par = ci & 1;
-                const int tb = 3 * ci, ta = tb + 1, tc = tb + 2;
-                const uint32_t sb = tiles + slot(tb) * kLtTile, sa = tiles + slot(ta) * kLtTile,
-                               sv = tiles + slot(tc) * kLtTile;
-                ok = wait(&ctrl->full[slot(tb)], phase(tb)) &&
-                     wait(&ctrl->full[slot(ta)], phase(ta)) &&
-                     (ci == 0 || wait(&ctrl->o, par ^ 1));         // P of the last chunk is read
-                if (!ok) break;
-                tc_fence_after();
+        if (!in) continue;
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tSc, sdesc(lt_op_kmajor(sa, kk), 16, 1024),
-                           sdesc(lt_op_kmajor(sb, kk), 16, 1024), idKK, kk > 0);
-                mma_commit(&ctrl->sc);
-                ok = wait(&ctrl->state, par) && (ci == 0 || wait(&ctrl->drained, par ^ 1));
-                if (!ok) break;
-                tc_fence_after();
+        for (int i = 0; i < 32; ++i) x[i] *= d;
+        uint32_t w[8];
+        if (q.out_f32) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tO1, sdesc(lt_op_kmajor(sa, kk), 16, 1024),
-                           sdesc(lt_op_kmajor(m_tile, kk), 16, 1024), idKK, kk > 0);
-                mma_commit(&ctrl->empty[slot(ta)]);
-                ok = wait(&ctrl->full[slot(tc)], phase(tc)) && wait(&ctrl->split, par) &&
-                     wait(&ctrl->p, par);
-                if (!ok) break;
-                tc_fence_after();
+            for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(tO2, tSc + (kk >> 2) * 64 + (kk & 3) * 8,
-                           sdesc(sv + kk * 2048, kRows * 128, 1024), idKM, kk > 0);
-                mma_commit(&ctrl->o);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tMu, sdesc(sv + kk * 2048, kRows * 128, 1024),
-                           sdesc(sb + kk * 2048, kRows * 128, 1024), idMM, kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tMu, sdesc(sv + kk * 2048, kRows * 128, 1024),
-                           sdesc(lo_tile + kk * 2048, kRows * 128, 1024), idMM, 1);
-                mma_commit(&ctrl->mu);
-                mma_commit(&ctrl->empty[slot(tb)]);
-                mma_commit(&ctrl->empty[slot(tc)]);
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * e + i]);
+                st_global32((float*)q.out + at + 32 * pc + 8 * e, w);
             }
-            mma_commit(&ctrl->drain);                  // nothing in flight when TMEM is freed
-            mbar_wait(&ctrl->drain, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_b2(x[16 * e + 2 * i], x[16 * e + 2 * i + 1]);
+                st_global32((__nv_bfloat16*)q.out + at + 32 * pc + 16 * e, w);
+            }
         }
-    } else if (warp < 8) {
-        const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const int64_t orow = (g.b * p.Hv + hv) * p.T + g.t0;
-        float din = REV ? 0.f : q.s_inter * lin_pow(lg, r + 1);
-        int n_of_din = 0;
-        for (int ci = 0; ci < nch; ++ci) {
-            const uint32_t par = ci & 1;
-            const int r0 = first_row(ci), n = rows_of(r0);
-            if (!wait(&ctrl->sc, par)) break;
+    }
+}
+
+__device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
+                        const LtWalk& wk, LtCtrl* c) {
+    const int quarter = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x;
+    const bool rev = wk.rev;
+    const uint32_t tSc = c->tmem + ((uint32_t)(quarter * 32) << 16), tO = tSc + 128;
+    const double lg = lin_log2(p.loggate, hv);
+    const int64_t orow = (g.b * p.Hv + hv) * p.T + g.t0;
+    // d of this row; in reverse it depends on the chunk's rows
+    auto decay = [&](int n) {
+        return fmaxf(lin_pow(lg, rev ? (r < n ? n - 1 - r : 0) : r + 1), 0x1p-60f);
+    };
+    float d = 0.f, d_prev = 0.f;
+    int n_prev = 0;
+    for (int ci = 0; ci <= wk.nch; ++ci) {
+        if (ci < wk.nch) {
+            const int n = wk.rows(wk.first(ci));
+            d_prev = d;
+            if (ci == 0 || (rev && n != n_prev)) d = decay(n);
+            n_prev = n;
+            const float inv = 1.f / d;
+            // o of the last chunk is over too (Sc waited for it); it is looked at
+            // before p arrives, as the next o may come any time after that
+            if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status) ||
+                (ci > 0 && !warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)))
+                return;
             tc_fence_after();
-#pragma unroll
-            for (int pc = 0; pc < 2; ++pc) {
-                const int piece = 2 * h + pc, j0 = 32 * piece;
-                const bool off = REV ? piece < quarter : piece > quarter;
+#pragma unroll 1
+            for (int piece = 0; piece < 4; ++piece) {
+                const int j0 = 32 * piece;
                 float v[32];
-                if (off) {
+                if (rev ? piece < quarter : piece > quarter) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0.f;
                 } else {
-                    tmem_ld32(tSc + lanes + j0, v);
-                    if (piece == quarter || n < kRows) {           // the border: element by element
+                    tmem_ld32(tSc + j0, v);
+                    if (piece == quarter || n < kRows) {           // the border: one by one
+                        const int dist0 = rev ? j0 - r : r - j0, sgn = rev ? 1 : -1;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            const int j = j0 + i, dist = REV ? j - r : r - j;
-                            v[i] = dist >= 0 && j < n ? v[i] * ctrl->pw[dist & 127] : 0.f;
+                            const int dist = dist0 + sgn * i;
+                            v[i] = dist >= 0 && j0 + i < n ? v[i] * (c->pw[dist & 127] * inv) : 0.f;
                         }
                     } else {
-                        const float f = ctrl->pw[REV ? j0 - r : r - j0 - 31];
+                        const float f = c->pw[rev ? j0 - r : r - j0 - 31] * inv;
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            const float4 s = *reinterpret_cast<const float4*>(&ctrl->step[i]);
+                            const float4 s = *reinterpret_cast<const float4*>(&c->step[i]);
                             v[i] *= f * s.x;
                             v[i + 1] *= f * s.y;
                             v[i + 2] *= f * s.z;
@@ -261,138 +383,73 @@ __device__ void lt_segment(const LinTcArgs& k, const LinProblem& q, const LinSeg
                         }
                     }
                 }
-                tmem_st_b16(tSc + lanes + 64 * h + 16 * pc, v);
+                tmem_st_b16(tSc + 16 * piece, v);      // behind the columns still to be read
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&ctrl->p);
-            if (REV && n != n_of_din) {
-                din = r < n ? q.s_inter * lin_pow(lg, n - 1 - r) : 0.f;
-                n_of_din = n;
-            }
-            if (!wait(&ctrl->o, par)) break;
-            tc_fence_after();
-            const int64_t at = (orow + r0 + r) * kD + 64 * h;
-            if (q.out_f32) {
-#pragma unroll
-                for (int pc = 0; pc < 2; ++pc) {
-                    float x[32], y[32];
-                    tmem_ld2(tO1 + lanes + 64 * h + 32 * pc, x, tO2 + lanes + 64 * h + 32 * pc, y);
-                    if (r < n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                w[i] = __float_as_uint(fmaf(din, x[8 * e + i], y[8 * e + i]));
-                            st_global32((float*)q.out + at + 32 * pc + 8 * e, w);
-                        }
-                }
-                tc_fence_before();
-                mbar_arrive(&ctrl->drained);
-            } else {
-                uint32_t w[4][8];
-#pragma unroll
-                for (int pc = 0; pc < 2; ++pc) {
-                    float x[32], y[32];
-                    tmem_ld2(tO1 + lanes + 64 * h + 32 * pc, x, tO2 + lanes + 64 * h + 32 * pc, y);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        w[2 * pc + i / 8][i % 8] = pack_b2(fmaf(din, x[2 * i], y[2 * i]),
-                                                           fmaf(din, x[2 * i + 1], y[2 * i + 1]));
-                }
-                tc_fence_before();
-                mbar_arrive(&ctrl->drained);
-                if (r < n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        st_global32((__nv_bfloat16*)q.out + at + 16 * e, w[e]);
-            }
+            warp_arrive(&c->p, lane);
         }
-    } else {
-        const int h = (warp - 8) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        float m[64];
-        {   // the incoming state: this thread's row, 64 columns
-            const bool first = REV ? g.k == g.m - 1 : g.k == 0;
-            const float* src = nullptr;
-            int rs = kD, cs = 1;
-            if (!first) {
-                src = q.ws + ((g.slot0 + (REV ? g.k : g.k - 1)) * p.Hv + hv) * kLinState;
-            } else if (q.m0) {
-                src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
-                if (q.m0_t) { rs = 1; cs = kD; }
+        if (ci > 0) {
+            const int r0 = wk.first(ci - 1);
+            if (ci == wk.nch) {
+                if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) return;
+                tc_fence_after();
             }
-            if (!src) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) m[i] = 0.f;
-            } else if (cs == 1) {
-#pragma unroll
-                for (int i = 0; i < 64; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(src + r * rs + 64 * h + i);
-                    m[i] = f.x; m[i + 1] = f.y; m[i + 2] = f.z; m[i + 3] = f.w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) m[i] = src[(64 * h + i) * kD + r];
-            }
-        }
-        float w = 0.f, an = 0.f;
-        int n_of_w = 0;
-        bool ok = true;
-        for (int ci = 0; ci <= nch; ++ci) {
-            // the state as an operand (read by O1 of chunk ci; O1 of ci - 1 is done)
-            if (ci < nch) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint4 u = make_uint4(pack_b2(m[8 * e], m[8 * e + 1]),
-                                               pack_b2(m[8 * e + 2], m[8 * e + 3]),
-                                               pack_b2(m[8 * e + 4], m[8 * e + 5]),
-                                               pack_b2(m[8 * e + 6], m[8 * e + 7]));
-                    sts128(m_tile + op_off(r, 8 * h + e), u);
-                }
-                fence_async_smem();
-                tc_fence_before();
-                mbar_arrive(&ctrl->state);
-            }
-            if (ci == nch) break;
-            const uint32_t par = ci & 1;
-            const int n = rows_of(first_row(ci));
-            if (n != n_of_w) {
-                w = q.s_state * lin_pow(lg, REV ? r + 1 : (r < n ? n - 1 - r : 0));
-                an = lin_pow(lg, n);
-                n_of_w = n;
-            }
-            const int tb = 3 * ci, tc = tb + 2;
-            ok = wait(&ctrl->full[slot(tb)], phase(tb)) &&
-                 wait(&ctrl->sc, par);                 // Sc has read b; Mu of ci - 1 has read lo
-            if (!ok) break;
-            split_row(tiles + slot(tb) * kLtTile, lo_tile, r, h, w, r < n);
-            if (n < kRows) {                           // rows of others may hold NaN
-                ok = wait(&ctrl->full[slot(tc)], phase(tc));
-                if (!ok) break;
-                if (r >= n) zero_row(tiles + slot(tc) * kLtTile, r, h);
-            }
-            fence_async_smem();
-            mbar_arrive(&ctrl->split);
-            ok = wait(&ctrl->mu, par);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int pc = 0; pc < 2; ++pc) {
-                float u[32];
-                tmem_ld32(tMu + lanes + 64 * h + 32 * pc, u);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) m[32 * pc + i] = fmaf(an, m[32 * pc + i], u[i]);
-            }
-        }
-        if (ok && q.mout && (REV ? g.k == 0 : g.k == g.m - 1)) {
-            float* dst = q.mout + (g.seq * p.Hv + hv) * kLinState + r * kD + 64 * h;
-#pragma unroll
-            for (int i = 0; i < 64; i += 4)
-                *reinterpret_cast<float4*>(dst + i) = make_float4(m[i], m[i + 1], m[i + 2], m[i + 3]);
+            lt_output(tO + 128 * ((ci - 1) & 1), q.s_out * (ci < wk.nch ? d_prev : d),
+                      r < wk.rows(r0), q, (orow + r0 + r) * kD, c, lane);
         }
     }
+}
+
+__device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
+                         const LtWalk& wk, uint32_t tiles, LtCtrl* c) {
+    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31, h = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const bool rev = wk.rev;
+    const uint32_t tMu = c->tmem + ((uint32_t)((warp & 3) * 32) << 16) + 384 + 64 * h;
+    const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
+    float m[64];
+    load_state(p, q, g, hv, rev, r, h, m);
+    float w = 0.f, an = 0.f, an_lo = 0.f;
+    int n_prev = 0;
+#pragma unroll 1
+    for (int ci = 0; ci < wk.nch; ++ci) {
+        const uint32_t par = ci & 1;
+        // the state as an operand of chunk ci (lo was in its tile, and has been read)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sts128(m_tile + op_off(r, 8 * h + e),
+                   make_uint4(pack_b2(m[8 * e], m[8 * e + 1]), pack_b2(m[8 * e + 2], m[8 * e + 3]),
+                              pack_b2(m[8 * e + 4], m[8 * e + 5]),
+                              pack_b2(m[8 * e + 6], m[8 * e + 7])));
+        fence_async_smem();
+        tc_fence_before();
+        warp_arrive(&c->state, lane);
+        const int n = wk.rows(wk.first(ci));
+        if (n != n_prev) {
+            const double lg = lin_log2(p.loggate, hv);
+            w = r < n ? q.s_state * lin_pow(lg, rev ? r + 1 : n - 1 - r) : 0.f;
+            lin_pow2(lg, n, an, an_lo);
+            n_prev = n;
+        }
+        const int tb = 3 * ci, tc = tb + 2;
+        const uint32_t sb = tiles + lt_slot(tb) * kLtTile;
+        if (!warp_wait(&c->full[lt_slot(tb)], lt_phase(tb), &c->abort, p.status) ||
+            !warp_wait(&c->am, par, &c->abort, p.status))          // Sc has read b, a M^T the state
+            return;
+        split_row(sb, mid_tile, m_tile, r, h, w, r >= n);
+        if (n < kRows) {
+            if (!warp_wait(&c->full[lt_slot(tc)], lt_phase(tc), &c->abort, p.status)) return;
+            if (r >= n) zero_row(tiles + lt_slot(tc) * kLtTile, r, h);
+        }
+        fence_async_smem();
+        warp_arrive(&c->parts, lane);
+        if (!warp_wait(&c->mu, par, &c->abort, p.status)) return;
+        tc_fence_after();
+        take_update(tMu, an, an_lo, m);
+    }
+    if (q.mout && (rev ? g.k == 0 : g.k == g.m - 1))
+        store_state(q.mout + (g.seq * p.Hv + hv) * kLinState, r, h, m);
 }
 
 // grid: (segments, Hv, problems)
@@ -406,68 +463,67 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     const LinProblem& q = p.pr[blockIdx.z];
     const LinSeg g = lin_find(p, blockIdx.x, 0);
     if (!g.ok) return;
-    const int hv = blockIdx.y, warp = threadIdx.x >> 5;
-    LtCtrl* ctrl = reinterpret_cast<LtCtrl*>(smem + 7 * kLtTile);
+    const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + 7 * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLtRing; ++i) {
-            mbar_init(&ctrl->full[i], 1);
-            mbar_init(&ctrl->empty[i], 1);
+            mbar_init(&c->full[i], 1);
+            mbar_init(&c->empty[i], 1);
         }
-        mbar_init(&ctrl->sc, 1);
-        mbar_init(&ctrl->p, 256);
-        mbar_init(&ctrl->split, 256);
-        mbar_init(&ctrl->o, 1);
-        mbar_init(&ctrl->drained, 256);
-        mbar_init(&ctrl->mu, 1);
-        mbar_init(&ctrl->state, 256);
-        mbar_init(&ctrl->drain, 1);
-        ctrl->abort = 0;
+        mbar_init(&c->sc, 1);
+        mbar_init(&c->p, 4);
+        mbar_init(&c->am, 1);
+        mbar_init(&c->parts, 8);
+        mbar_init(&c->o, 1);
+        mbar_init(&c->drained, 4);
+        mbar_init(&c->mu, 1);
+        mbar_init(&c->state, 8);
+        mbar_init(&c->drain, 1);
+        c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 17) tmem_alloc(&ctrl->tmem, 512);
+    if (warp == 13) tmem_alloc(&c->tmem, 512);
     if (threadIdx.x < kRows + 32) {
         const double lg = lin_log2(p.loggate, hv);
         const int i = threadIdx.x;
-        if (i < kRows) ctrl->pw[i] = q.s_intra * lin_pow(lg, i);
-        else ctrl->step[i - kRows] = lin_pow(lg, q.reverse ? i - kRows : 31 - (i - kRows));
+        if (i < kRows) c->pw[i] = q.s_weight * lin_pow(lg, i);
+        else c->step[i - kRows] = lin_pow(lg, q.reverse ? i - kRows : 31 - (i - kRows));
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (q.reverse) lt_segment<true>(k, q, g, hv, smem, ctrl);
-    else lt_segment<false>(k, q, g, hv, smem, ctrl);
+    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0};
+    const uint32_t tiles = su32(smem);
+    if (warp < 4) {
+        lt_rows(p, q, g, hv, wk, c);
+    } else if (warp < 12) {
+        lt_state(p, q, g, hv, wk, tiles, c);
+    } else if (warp == 12) {
+        if (lane == 0) lt_load(k, q, g, hv, wk, smem, c);
+    } else if (lane == 0) {
+        lt_multiply(wk, tiles, c, p.status);
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == 13) {
         tc_fence_after();
-        tmem_dealloc(ctrl->tmem, 512);
+        tmem_dealloc(c->tmem, 512);
     }
 }
 
 // ---- step 1: what a segment adds to the state ----
-// Warps 0-7 split b, warp 8 loads, warp 9 multiplies.  Five ring tiles, two lo
-// tiles, so that a chunk is split while the one before it is multiplied.
+// Warps 0-7 split b and carry the state, warp 8 loads, warp 9 multiplies.
+// Five ring tiles, one each for mid and lo; the parts of a chunk are formed
+// while hi of the one before is multiplied, which needs two accumulators.
 constexpr int kLsThreads = 10 * 32;
 struct __align__(8) LsCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t split[2], mu[2], drain;
+    uint64_t parts, read, mu[2], drain;
     uint32_t tmem;
     int abort;
 };
 constexpr int kLsSmem = 7 * kLtTile + (int)sizeof(LsCtrl);
-
-struct LsWait {
-    LsCtrl* c;
-    int* status;
-    __device__ bool live() const { return *(const volatile int*)&c->abort == 0; }
-    __device__ bool operator()(uint64_t* b, uint32_t parity) const {
-        if (!live()) return false;
-        if (mbar_wait(b, parity)) return true;
-        atomicExch(&c->abort, 1);
-        raise_status(status, kStatusTimeout);
-        return false;
-    }
-};
 
 // grid: (boundaries, Hv, problems)
 __global__ void __launch_bounds__(kLsThreads, 1)
@@ -487,118 +543,119 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         g.n = g.seq_n - g.k * p.seg_len < p.seg_len ? g.seq_n - g.k * p.seg_len : p.seg_len;
     }
     const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    LsCtrl* ctrl = reinterpret_cast<LsCtrl*>(smem + 7 * kLtTile);
+    LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + 7 * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLtRing; ++i) {
-            mbar_init(&ctrl->full[i], 1);
-            mbar_init(&ctrl->empty[i], 1);
+            mbar_init(&c->full[i], 1);
+            mbar_init(&c->empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctrl->split[i], 256);
-            mbar_init(&ctrl->mu[i], 1);
-        }
-        mbar_init(&ctrl->drain, 1);
-        ctrl->abort = 0;
+        mbar_init(&c->parts, 8);
+        mbar_init(&c->read, 1);
+        mbar_init(&c->mu[0], 1);
+        mbar_init(&c->mu[1], 1);
+        mbar_init(&c->drain, 1);
+        c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(&ctrl->tmem, 128);
+    if (warp == 9) tmem_alloc(&c->tmem, 256);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = ctrl->tmem, tiles = su32(smem), lo_tile = tiles + 5 * kLtTile;
-    const LsWait wait{ctrl, p.status};
-    const int nch = (int)((g.n + kRows - 1) / kRows);
-    auto slot = [](int t) { return t % kLtRing; };
-    auto phase = [](int t) { return (uint32_t)(t / kLtRing) & 1; };
+    const uint32_t tm = c->tmem, tiles = su32(smem);
+    const uint32_t mid_tile = tiles + 5 * kLtTile, lo_tile = tiles + 6 * kLtTile;
+    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0};
+    int* const ab = &c->abort;
     if (warp == 8) {
         if (lane == 0) {
             const int z = blockIdx.z;
-            const CUtensorMap* mp[2] = {&k.map[k.ib[z]], &k.map[k.ic[z]]};
-            const int row[2] = {lt_row0(p, g, hv, q.gb), lt_row0(p, g, hv, q.gc)};
+            const CUtensorMap *mb = &k.map[k.ib[z]], *mc = &k.map[k.ic[z]];
+            const int yb = lt_row0(p, g, hv, q.gb), yc = lt_row0(p, g, hv, q.gc);
             int t = 0;
-            for (; t < 2 * nch; ++t) {
-                const int s = slot(t), y = row[t & 1] + (t >> 1) * kRows;
-                if (t >= kLtRing && !wait(&ctrl->empty[s], phase(t) ^ 1)) break;
-                if (!wait.live()) break;
-                mbar_expect_tx(&ctrl->full[s], kLtTile);
-                tma_load_2d(smem + s * kLtTile, mp[t & 1], 0, y, &ctrl->full[s]);
-                tma_load_2d(smem + s * kLtTile + kRows * 128, mp[t & 1], 64, y, &ctrl->full[s]);
+            for (; t < 2 * wk.nch; ++t) {
+                const int s = lt_slot(t), y = wk.first(t >> 1) + (t & 1 ? yc : yb);
+                if (t >= kLtRing && !lt_wait(&c->empty[s], lt_phase(t) ^ 1, ab, p.status)) break;
+                mbar_expect_tx(&c->full[s], kLtTile);
+                tma_load_2d(smem + s * kLtTile, t & 1 ? mc : mb, 0, y, &c->full[s]);
+                tma_load_2d(smem + s * kLtTile + kRows * 128, t & 1 ? mc : mb, 64, y, &c->full[s]);
             }
             for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
-                mbar_wait(&ctrl->full[slot(i)], phase(i));
+                mbar_wait(&c->full[lt_slot(i)], lt_phase(i));
         }
     } else if (warp == 9) {
         if (lane == 0) {
-            constexpr uint32_t idMM = idesc_f16(1, 1, 1, 128, 128);
-            for (int ci = 0; ci < nch; ++ci) {
+            for (int ci = 0; ci < wk.nch; ++ci) {
                 const int tb = 2 * ci, tc = tb + 1;
-                if (!wait(&ctrl->full[slot(tc)], phase(tc)) ||
-                    !wait(&ctrl->split[ci & 1], (ci >> 1) & 1))
+                if (!lt_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, p.status) ||
+                    !lt_wait(&c->parts, ci & 1, ab, p.status))
                     break;
                 tc_fence_after();
-                const uint32_t sb = tiles + slot(tb) * kLtTile, sv = tiles + slot(tc) * kLtTile,
-                               sl = lo_tile + (ci & 1) * kLtTile;
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tm, sdesc(sv + kk * 2048, kRows * 128, 1024),
-                           sdesc(sb + kk * 2048, kRows * 128, 1024), idMM, ci > 0 || kk > 0);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ss(tm, sdesc(sv + kk * 2048, kRows * 128, 1024),
-                           sdesc(sl + kk * 2048, kRows * 128, 1024), idMM, 1);
-                mma_commit(&ctrl->mu[ci & 1]);
-                mma_commit(&ctrl->empty[slot(tb)]);
-                mma_commit(&ctrl->empty[slot(tc)]);
+                const uint32_t sb = tiles + lt_slot(tb) * kLtTile,
+                               sv = tiles + lt_slot(tc) * kLtTile, d = tm + 128 * (ci & 1);
+                mma_mm(d, sv, lo_tile, true);
+                mma_mm(d, sv, mid_tile, false);
+                mma_commit(&c->read);
+                mma_mm(d, sv, sb, false);
+                mma_commit(&c->mu[ci & 1]);
+                mma_commit(&c->empty[lt_slot(tb)]);
+                mma_commit(&c->empty[lt_slot(tc)]);
             }
-            mma_commit(&ctrl->drain);
-            mbar_wait(&ctrl->drain, 0);
+            mma_commit(&c->drain);
+            mbar_wait(&c->drain, 0);
         }
     } else {
-        const int h = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const int h = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t tMu = tm + ((uint32_t)((warp & 3) * 32) << 16) + 64 * h;
         const double lg = lin_log2(p.loggate, hv);
+        float m[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) m[i] = 0.f;
+        float w = 0.f, a[2] = {0.f, 0.f}, a_lo[2] = {0.f, 0.f};  // this chunk's decay, the last one's
+        int n_prev = 0;
         bool ok = true;
-        for (int ci = 0; ci < nch; ++ci) {
-            const int tb = 2 * ci, tc = tb + 1, row = ci * kRows + r;
-            const int n = (int)(g.n - ci * kRows < kRows ? g.n - ci * kRows : kRows);
-            const float w =
-                r < n ? q.s_state * lin_pow(lg, q.reverse ? row + 1 : g.n - 1 - row) : 0.f;
-            ok = wait(&ctrl->full[slot(tb)], phase(tb)) &&
-                 (ci < 2 || wait(&ctrl->mu[ci & 1], ((ci >> 1) & 1) ^ 1));
-            if (!ok) break;
-            split_row(tiles + slot(tb) * kLtTile, lo_tile + (ci & 1) * kLtTile, r, h, w, r < n);
-            if (n < kRows) {
-                ok = wait(&ctrl->full[slot(tc)], phase(tc));
-                if (!ok) break;
-                if (r >= n) zero_row(tiles + slot(tc) * kLtTile, r, h);
-            }
-            fence_async_smem();
-            mbar_arrive(&ctrl->split[ci & 1]);
-        }
-        if (ok) ok = wait(&ctrl->mu[(nch - 1) & 1], ((nch - 1) >> 1) & 1);
-        if (ok) {
-            tc_fence_after();
-            float* dst = q.ws + ((g.slot0 + (q.reverse ? g.k - 1 : g.k)) * p.Hv + hv) * kLinState +
-                         r * kD + 64 * h;
-#pragma unroll
-            for (int pc = 0; pc < 2; ++pc) {
-                float u[32];
-                tmem_ld32(tm + lanes + 64 * h + 32 * pc, u);
-#pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    uint32_t x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __float_as_uint(u[i + e]);
-                    st_global32(dst + 32 * pc + i, x);
+#pragma unroll 1
+        for (int ci = 0; ci <= wk.nch; ++ci) {
+            if (ci < wk.nch) {
+                const int tb = 2 * ci, tc = tb + 1, n = wk.rows(wk.first(ci));
+                a[1] = a[0];
+                a_lo[1] = a_lo[0];
+                if (n != n_prev) {
+                    w = r < n ? q.s_state * lin_pow(lg, q.reverse ? r + 1 : n - 1 - r) : 0.f;
+                    lin_pow2(lg, n, a[0], a_lo[0]);
+                    n_prev = n;
                 }
+                const uint32_t sb = tiles + lt_slot(tb) * kLtTile;
+                ok = warp_wait(&c->full[lt_slot(tb)], lt_phase(tb), ab, p.status) &&
+                     (ci == 0 || warp_wait(&c->read, (ci - 1) & 1, ab, p.status));
+                if (!ok) break;
+                split_row(sb, mid_tile, lo_tile, r, h, w, r >= n);
+                if (n < kRows) {
+                    ok = warp_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, p.status);
+                    if (!ok) break;
+                    if (r >= n) zero_row(tiles + lt_slot(tc) * kLtTile, r, h);
+                }
+                fence_async_smem();
+                tc_fence_before();                     // the update of ci - 2 has left its accumulator
+                warp_arrive(&c->parts, lane);
+            }
+            if (ci > 0) {
+                ok = warp_wait(&c->mu[(ci - 1) & 1], ((ci - 1) >> 1) & 1, ab, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const bool last = ci == wk.nch;
+                take_update(tMu + 128 * ((ci - 1) & 1), last ? a[0] : a[1],
+                            last ? a_lo[0] : a_lo[1], m);
             }
         }
+        if (ok)
+            store_state(q.ws + ((g.slot0 + (q.reverse ? g.k - 1 : g.k)) * p.Hv + hv) * kLinState, r,
+                        h, m);
     }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 9) {
         tc_fence_after();
-        tmem_dealloc(tm, 128);
+        tmem_dealloc(tm, 256);
     }
 }
 
