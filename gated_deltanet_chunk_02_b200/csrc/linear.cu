@@ -6,8 +6,8 @@
 // products are dense (queries with keys, weights with values); between chunks
 // only the 128 x 128 state is carried, so the work is linear in the length.
 // A sequence's recurrence is cut into segments that run in parallel:
-//   1. the states that segments add, each from zero (k_state kernels);
-//   2. k_lin_combine: the states at the boundaries, in order;
+//   1. the states that segments add, each from zero (the state kernels);
+//   2. k_lin_combine: the states at the boundaries and the outgoing one, in order;
 //   3. every segment's outputs from its incoming state.
 // One segment per sequence needs step 3 alone.  Step 1 reads keys and values
 // once more, so the cut is made only where sequences times heads leave SMs
@@ -80,6 +80,14 @@ __global__ void __launch_bounds__(256) k_lin_combine(const LinArgs p) {
                             fmaf(a, m.w, u[j].w));
             base[(q.reverse ? g.m - 2 - i : i) * step] = m;
         }
+    }
+    if (q.mout) {                                      // the walk's last segment left its part here
+        float4* const out =
+            reinterpret_cast<float4*>(q.mout + (seq * p.Hv + hv) * kLinState + e);
+        const float a = q.reverse ? a_full : a_last;
+        const float4 u = *out;
+        *out = make_float4(fmaf(a, m.x, u.x), fmaf(a, m.y, u.y), fmaf(a, m.z, u.z),
+                           fmaf(a, m.w, u.w));
     }
 }
 
@@ -317,42 +325,37 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
         }
     }
     __syncthreads();
+    // a sequence of several segments has its outgoing state from steps 1 and 2
     float* dst = nullptr;
-    if (STATE_ONLY)
-        dst = q.ws + ((g.slot0 + (REV ? g.k - 1 : g.k)) * p.Hv + hv) * kLinState;
-    else if (q.mout && (REV ? g.k == 0 : g.k == g.m - 1))
-        dst = q.mout + (g.seq * p.Hv + hv) * kLinState;
+    if (STATE_ONLY) dst = lin_added(p, q, g, hv);
+    else if (q.mout && g.m == 1) dst = q.mout + (g.seq * p.Hv + hv) * kLinState;
     if (dst)
         for (int e = tid; e < kSimtDV * kLinD; e += kSimtThreads)
             dst[v0 * kLinD + e] = s.m[e / kLinD][e % kLinD];
 }
 
-// grid: (segments or boundaries, 4 Hv, problems)
+// grid: (segments (of sequences that have several), 4 Hv, problems)
 template <bool STATE_ONLY>
 __global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtSmem& s = *reinterpret_cast<SimtSmem*>(raw);
     const LinProblem& q = p.pr[blockIdx.z];
-    LinSeg g = lin_find(p, blockIdx.x, STATE_ONLY ? 1 : 0);
+    const LinSeg g = lin_find(p, blockIdx.x, STATE_ONLY ? kCutSegments : kAllSegments);
     if (!g.ok) return;
     const int hv = blockIdx.y >> 2, v0 = (blockIdx.y & 3) * kSimtDV;
-    if (STATE_ONLY && q.reverse) {                     // boundary k: what segment k + 1 adds
-        g.k += 1;
-        g.t0 = g.seq_t0 + g.k * p.seg_len;
-        g.n = g.seq_n - g.k * p.seg_len < p.seg_len ? g.seq_n - g.k * p.seg_len : p.seg_len;
-    }
+    if (STATE_ONLY && !lin_added(p, q, g, hv)) return;
     if (q.reverse) simt_segment<STATE_ONLY, true>(p, q, g, hv, v0, s);
     else simt_segment<STATE_ONLY, false>(p, q, g, hv, v0, s);
 }
 
-cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t bounds, bool states,
+cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t cut_segs, bool states,
                      cudaStream_t st) {
     const int smem = (int)sizeof(SimtSmem);
     if (states) {
         cudaError_t e = cudaFuncSetAttribute(k_linear_simt<true>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        k_linear_simt<true><<<dim3((unsigned)bounds, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
+        k_linear_simt<true><<<dim3((unsigned)cut_segs, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
                                  smem, st>>>(a);
     } else {
         cudaError_t e = cudaFuncSetAttribute(k_linear_simt<false>,
@@ -395,6 +398,8 @@ LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16) {
     const int64_t m = s.T <= pl.seg_len ? 1 : (s.T + pl.seg_len - 1) / pl.seg_len;
     pl.bounds = packed ? (s.T <= pl.seg_len ? 0 : s.T / pl.seg_len) : s.B * (m - 1);
     pl.segs = packed ? s.nseq + pl.bounds : s.B * m;
+    const int64_t cut = packed ? (s.nseq < pl.bounds ? s.nseq : pl.bounds) : s.B;
+    pl.cut_segs = m > 1 ? pl.bounds + cut : 0;         // each cut sequence has one more segment
     pl.state_bytes = pl.bounds * s.Hv * kLinState * 4;
     return pl;
 }
@@ -409,7 +414,7 @@ cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool 
     cudaError_t e;
     if (pl.bounds > 0) {
         e = bf16 ? launch_linear_tc(a, nprob, pl, true, st)
-                 : run_simt(a, nprob, pl.segs, pl.bounds, true, st);
+                 : run_simt(a, nprob, pl.segs, pl.cut_segs, true, st);
         if (e != cudaSuccess) return e;
         k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), kLinState / 1024, nprob), 256, 0, st>>>(a);
         e = cudaGetLastError();
@@ -417,7 +422,7 @@ cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool 
         *launches += 2;
     }
     e = bf16 ? launch_linear_tc(a, nprob, pl, false, st)
-             : run_simt(a, nprob, pl.segs, pl.bounds, false, st);
+             : run_simt(a, nprob, pl.segs, pl.cut_segs, false, st);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -69,14 +69,19 @@ __device__ __forceinline__ void lin_bounds(const LinArgs& p, int64_t s, int64_t&
         n = hi - lo;
     }
 }
-// The idx-th segment (sub = 0), or the idx-th boundary (sub = 1: boundary k of
-// a sequence lies between its segments k and k + 1).  Called by whole warps;
-// packed sequences are counted 32 at a time.
-__device__ __forceinline__ LinSeg lin_find(const LinArgs& p, int64_t idx, int sub) {
+// What lin_find counts: every segment (one at least per sequence), or the
+// segments of the sequences that have several.
+enum : int { kAllSegments = 0, kCutSegments = 1 };
+__device__ __forceinline__ int64_t lin_counted(int64_t m, int which) {
+    return which == kCutSegments && m < 2 ? 0 : m;
+}
+// The idx-th of them.  Called by whole warps; packed sequences are counted 32
+// at a time.
+__device__ __forceinline__ LinSeg lin_find(const LinArgs& p, int64_t idx, int which) {
     LinSeg g;
     g.ok = false;
     if (!p.cu) {
-        const int64_t m = lin_segments(p.T, p.seg_len), per = m - sub;
+        const int64_t m = lin_segments(p.T, p.seg_len), per = lin_counted(m, which);
         if (per <= 0 || idx >= per * p.nseq) return g;
         g.seq = idx / per;
         g.k = (int)(idx - g.seq * per);
@@ -95,7 +100,7 @@ __device__ __forceinline__ LinSeg lin_find(const LinArgs& p, int64_t idx, int su
                 lin_bounds(p, s0 + lane, t0, n);
                 m = lin_segments(n, p.seg_len);
             }
-            const int64_t mine = m ? m - sub : 0;
+            const int64_t mine = lin_counted(m, which);
             int64_t inc = mine, sinc = m ? m - 1 : 0;  // inclusive sums over the lanes
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -134,7 +139,7 @@ __device__ __forceinline__ LinSeg lin_find(const LinArgs& p, int64_t idx, int su
 
 // How a call is cut: the same for its workspace size and its launches.
 struct LinPlan {
-    int64_t seg_len, segs, bounds;                     // upper bounds of the counts if packed
+    int64_t seg_len, segs, cut_segs, bounds;           // upper bounds of the counts if packed
     int64_t state_bytes;                               // boundary states of one problem
 };
 LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16);
@@ -147,6 +152,16 @@ cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, boo
 // out[b, h] = sum of part[b, h * group + g] over g, float32 -> the data type
 cudaError_t launch_linear_group_sum(const LinArgs& a, const float* part, void* out, int group,
                                     bool bf16, cudaStream_t st);
+
+// Where step 1 leaves what segment k adds to the state: the slot of the
+// boundary that it ends at in walking order; the walk's last segment ends at
+// none, its place is the outgoing state itself (null if that is not wanted).
+__device__ __forceinline__ float* lin_added(const LinArgs& p, const LinProblem& q, const LinSeg& g,
+                                            int hv) {
+    const bool last = q.reverse ? g.k == 0 : g.k == g.m - 1;
+    if (last) return q.mout ? q.mout + (g.seq * p.Hv + hv) * kLinState : nullptr;
+    return q.ws + ((g.slot0 + (q.reverse ? g.k - 1 : g.k)) * p.Hv + hv) * kLinState;
+}
 
 // log2 of the decay; -inf (no memory at all) becomes a finite number whose
 // product with a distance of zero is zero

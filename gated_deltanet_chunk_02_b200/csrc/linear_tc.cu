@@ -12,30 +12,31 @@
 // the state then reaches rows it should reach with less than 2^-60 with 2^-60,
 // far below the rounding of anything it could matter to.
 //
-// The state lives in fp32 registers; only its copy as an operand of O is
-// rounded to bf16, and so is P (each term of an output passes one rounding).
-// w b is split into three bf16 parts, lo + mid + hi, and Mu takes a product
-// with each, smallest first: c is exact in bf16, so the update carries fp32
-// accuracy (two parts left 2e-6 in a returned state, three 2e-7).  Mu is
-// drained into the registers after every chunk: accumulation in TMEM rounds
-// towards zero, and over a segment that alone would cost 1e-5.
+// The state lives in TMEM in fp32; only its copy as an operand of O is rounded
+// to bf16, and so is P (each term of an output passes one rounding).
+// c is exact in bf16 and w b is split into bf16 parts with a product each,
+// smallest first: two parts (2^-16) where the state is only an operand later,
+// three (exact) where it is returned or starts other segments.  Mu is added to
+// the state in fp32 after every chunk: accumulation in TMEM rounds towards
+// zero, and over a segment that alone would cost 1e-5.
 //
-// Bound: six products (3100 cycles of the tensor pipe) and 128 KB in and out per
-// chunk (5600 cycles at 1/148 of the copy bandwidth), so the aim is to stream.
-// One CTA per SM, 14 warps:
-//   warps 0-3   P from Sc; the previous chunk's outputs (lane = row)
-//   warps 4-11  the parts of w b; the state (lane = row, half the columns)
-//   warp 12     TMA: b, a, c of each chunk into a ring of five 32 KB tiles
-//   warp 13     MMA: Sc, a M^T, Mu (lo, mid, hi), P c
-// hi overwrites b's tile (Sc has read it), mid has a tile, and lo takes the
-// bf16 state's (a M^T has read it): 7 x 32 KB.  O has two accumulators, so that
-// a chunk's outputs leave while the next is formed; P goes back to TMEM (A
-// operand) over Sc.  The warps' loops are kept rolled: unrolled, the roles'
-// code (80 KB a chunk) ran at the rate it could be fetched, 11000 cycles a
-// chunk.  Every wait is bounded (2 s): on expiry the status word is set and
-// all roles leave.
+// Bound: five products (2600 cycles of the tensor pipe) and 128 KB in and out
+// per chunk (5600 cycles at 1/148 of the copy bandwidth), so the aim is to
+// stream.  One CTA per SM, 18 warps:
+//   warps 0-7   P from Sc; the last chunk's outputs (lane = row, half the columns)
+//   warps 8-15  the parts of w b; the state (lane = row, half the columns)
+//   warp 16     TMA: b, a, c of each chunk into a ring of five 32 KB tiles
+//   warp 17     MMA: Sc, a M^T, P c, Mu
+// hi overwrites b's tile (Sc has read it), mid has a tile, the bf16 state the
+// seventh; a third part, lo, takes the state's once a M^T has read it.  TMEM
+// holds Sc, O, Mu and M; P goes back over Sc (A operand).  Outputs leave while
+// Mu is formed.  Two things ruined first versions, both at 8600 to 11000 cycles
+// a chunk: unrolled loops (80 KB of code a chunk run at the rate it can be
+// fetched), and the state in registers (a spilled register's reload is an L2
+// access, as shared memory leaves L1 no room).  Every wait is bounded (2 s): on
+// expiry the status word is set and all roles leave.
 //
-// k_linear_state_tc is step 1: the state part alone.
+// k_linear_state_tc is step 1: the state part alone, always with three parts.
 #include <cstddef>
 #include <cstring>
 
@@ -47,7 +48,7 @@ namespace tcg {
 
 constexpr int kLtTile = kRows * kD * 2;                // one bf16 [2][128][64] operand: 32 KB
 constexpr int kLtRing = 5;
-constexpr int kLtThreads = 14 * 32;
+constexpr int kLtThreads = 18 * 32;
 
 struct LinTcArgs {
     CUtensorMap map[4];                                // the call's distinct tensors
@@ -59,7 +60,11 @@ struct __align__(16) LtCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
     uint64_t sc, am, p, parts, o, drained, mu, state, drain;
     __align__(16) float pw[kRows];                     // s lambda^n
-    __align__(16) float step[32];                                    // lambda^(31 - n), lambda^n if reverse
+    __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
+    // by row, for whole chunks [0] and for the segment's last rows [1]: the
+    // weight of b, d; and lambda^n as a sum of two floats
+    float w[2][kRows], d[2][kRows];
+    float an[2], an_lo[2];
     uint32_t tmem;
     int abort;
 };
@@ -84,35 +89,84 @@ __device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort
     raise_status(status, kStatusTimeout);
     return false;
 }
-
 // the same for a whole warp, with one answer
 __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
     return __all_sync(0xffffffffu, lt_wait(b, parity, abort, status));
 }
 
-// eight bf16 of one 16-byte group times w, as hi + mid + lo
-__device__ __forceinline__ void split8(const uint4& u, float w, uint4& hi, uint4& mid, uint4& lo) {
+// two floats in one register pair
+struct F2 {
+    uint64_t v;
+    F2() = default;
+    __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ void get(float& a, float& b) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+    }
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+    F2 r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+// The upper 16 bits of both (truncated to bf16) as a pair, and what is left.
+__device__ __forceinline__ uint32_t take_upper(F2& x) {
+    float a, b;
+    x.get(a, b);
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    x = sub2(x, F2(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)));
+    return __byte_perm(ua, ub, 0x7632);
+}
+// eight bf16 of one 16-byte group times w, as hi + mid (+ lo): truncation
+// leaves 16, then 8 bits, so that three parts are exact
+template <int PARTS>
+__device__ __forceinline__ void split8(const uint4& u, float w, uint4 (&part)[PARTS]) {
     const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-    uint32_t h[4], m[4], l[4];
+    uint32_t y[PARTS][4];
+    const F2 w2(w, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float a = __uint_as_float(x[i] << 16) * w;
-        float b = __uint_as_float(x[i] & 0xffff0000u) * w;
-        h[i] = pack_b2(a, b);
-        a -= __uint_as_float(h[i] << 16);
-        b -= __uint_as_float(h[i] & 0xffff0000u);
-        m[i] = pack_b2(a, b);
-        l[i] = pack_b2(a - __uint_as_float(m[i] << 16), b - __uint_as_float(m[i] & 0xffff0000u));
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    mid = make_uint4(m[0], m[1], m[2], m[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-// 32 values -> 16 TMEM columns of bf16 pairs
-__device__ __forceinline__ void tmem_st_b16(uint32_t taddr, const float (&v)[32]) {
-    uint32_t w[16];
+        F2 v = mul2(F2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), w2);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack_b2(v[2 * i], v[2 * i + 1]);
+        for (int k = 0; k < PARTS - 1; ++k) y[k][i] = take_upper(v);
+        float a, b;
+        v.get(a, b);
+        y[PARTS - 1][i] = pack_b2(a, b);
+    }
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) part[k] = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+}
+// row r (columns 64 h ..) of b times w: hi in its place, mid (and lo) in their
+// tiles.  Rows that are not this segment's (off) may hold anything: zero.
+template <int PARTS>
+__device__ __forceinline__ void split_row(uint32_t b, uint32_t mid_tile, uint32_t lo_tile, int r,
+                                          int h, float w, bool off) {
+#pragma unroll 2
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t at = op_off(r, 8 * h + e);
+        uint4 u = lds128(b + at), part[PARTS];
+        if (off) u = make_uint4(0, 0, 0, 0);
+        split8<PARTS>(u, w, part);
+        sts128(b + at, part[0]);
+        sts128(mid_tile + at, part[1]);
+        if (PARTS == 3) sts128(lo_tile + at, part[PARTS - 1]);
+    }
+}
+__device__ __forceinline__ void zero_row(uint32_t tile, int r, int h) {
+#pragma unroll 1
+    for (int q = 0; q < 8; ++q) sts128(tile + op_off(r, 8 * h + q), make_uint4(0, 0, 0, 0));
+}
+// 32 columns as 16 TMEM columns of bf16 pairs
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
         "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -122,7 +176,7 @@ __device__ __forceinline__ void tmem_st_b16(uint32_t taddr, const float (&v)[32]
         : "memory");
 }
 // 32 bytes, one whole sector
-__device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8]) {
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
@@ -147,7 +201,7 @@ __device__ __forceinline__ void mma_pc(uint32_t d, uint32_t a, uint32_t b) {
     const uint64_t db = sdesc(b, kRows * 128, 1024);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        mma_ts(d, a + kk * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128), 1);
+        mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128), 1);
 }
 __device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool fresh) {
     const uint64_t da = sdesc(a, kRows * 128, 1024), db = sdesc(b, kRows * 128, 1024);
@@ -163,30 +217,12 @@ __device__ __forceinline__ int lt_row0(const LinArgs& p, const LinSeg& g, int hv
 __device__ __forceinline__ int lt_slot(int t) { return t % kLtRing; }
 __device__ __forceinline__ uint32_t lt_phase(int t) { return (uint32_t)(t / kLtRing) & 1; }
 
-// this thread's row r of the incoming state, columns 64 h ..
-__device__ __forceinline__ void load_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
-                                           int hv, bool rev, int r, int h, float (&m)[64]) {
-    const bool first = rev ? g.k == g.m - 1 : g.k == 0;
-    const float* src = nullptr;
-    bool across = false;
-    if (!first) {
-        src = q.ws + ((g.slot0 + (rev ? g.k : g.k - 1)) * p.Hv + hv) * kLinState;
-    } else if (q.m0) {
-        src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
-        across = q.m0_t != 0;
-    }
+// 16 columns of this thread's lane -> TMEM, raw
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) m[i] = 0.f;
-    if (src && across) {
-#pragma unroll
-        for (int i = 0; i < 64; ++i) m[i] = src[(64 * h + i) * kD + r];
-    } else if (src) {
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(src + r * kD + 64 * h + i);
-            m[i] = f.x; m[i + 1] = f.y; m[i + 2] = f.z; m[i + 3] = f.w;
-        }
-    }
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
+    tmem_st16(taddr, w);
 }
 __device__ __forceinline__ void store_state(float* dst, int r, int h, const float (&m)[64]) {
 #pragma unroll
@@ -200,38 +236,26 @@ __device__ __forceinline__ void store_state(float* dst, int r, int h, const floa
 // M <- (a + a_lo) M + Mu: a's own rounding would add up over the chunks that a
 // slow decay remembers
 __device__ __forceinline__ void take_update(uint32_t mu, float a, float a_lo, float (&m)[64]) {
+    const F2 a2(a, a), l2(a_lo, a_lo);
 #pragma unroll
-    for (int pc = 0; pc < 2; ++pc) {
-        float u[32];
-        tmem_ld32(mu + 32 * pc, u);
+    for (int pc = 0; pc < 4; ++pc) {
+        float u[16];
+        tmem_ld16(mu + 16 * pc, u);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) m[32 * pc + i] = fmaf(a, m[32 * pc + i], fmaf(a_lo, m[32 * pc + i], u[i]));
+        for (int i = 0; i < 16; i += 2) {
+            float& x = m[16 * pc + i];
+            float& y = m[16 * pc + i + 1];
+            const F2 v(x, y);
+            fma2(a2, v, fma2(l2, v, F2(u[i], u[i + 1]))).get(x, y);
+        }
     }
-}
-// row r (columns 64 h ..) of b times w: hi in its place, mid and lo in their
-// tiles.  Rows that are not this segment's (off) may hold anything: zero.
-__device__ __forceinline__ void split_row(uint32_t b, uint32_t mid_tile, uint32_t lo_tile, int r,
-                                          int h, float w, bool off) {
-#pragma unroll 2
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t at = op_off(r, 8 * h + e);
-        uint4 u = lds128(b + at), hi, mid, lo;
-        if (off) u = make_uint4(0, 0, 0, 0);
-        split8(u, w, hi, mid, lo);
-        sts128(b + at, hi);
-        sts128(mid_tile + at, mid);
-        sts128(lo_tile + at, lo);
-    }
-}
-__device__ __forceinline__ void zero_row(uint32_t tile, int r, int h) {
-#pragma unroll 1
-    for (int q = 0; q < 8; ++q) sts128(tile + op_off(r, 8 * h + q), make_uint4(0, 0, 0, 0));
 }
 
 // ---- the roles of k_linear_tc ----
 struct LtWalk {                                        // chunks of a segment, in walking order
     int n, nch;
     bool rev;
+    bool exact;                                        // the state is returned: three parts
     __device__ int first(int ci) const { return (rev ? nch - 1 - ci : ci) * kRows; }
     __device__ int rows(int r0) const { return n - r0 < kRows ? n - r0 : kRows; }
 };
@@ -258,35 +282,36 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
 }
 
 __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* status) {
-    const uint32_t tSc = c->tmem, tO = tSc + 128, tMu = tSc + 384;
+    const uint32_t tSc = c->tmem, tO = tSc + 128, tMu = tSc + 256;
     const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
     int* const ab = &c->abort;
     for (int ci = 0; ci < wk.nch; ++ci) {
         const uint32_t par = ci & 1;
         const int tb = 3 * ci, ta = tb + 1, tc = tb + 2;
         const uint32_t sb = tiles + lt_slot(tb) * kLtTile, sa = tiles + lt_slot(ta) * kLtTile,
-                       sv = tiles + lt_slot(tc) * kLtTile, to = tO + 128 * par;
+                       sv = tiles + lt_slot(tc) * kLtTile;
         if (!lt_wait(&c->full[lt_slot(tb)], lt_phase(tb), ab, status) ||
             !lt_wait(&c->full[lt_slot(ta)], lt_phase(ta), ab, status) ||
-            (ci > 0 && !lt_wait(&c->o, par ^ 1, ab, status)) ||    // P c of the last chunk is done
-            (ci > 1 && !lt_wait(&c->drained, par, ab, status)))    // outputs of ci - 2 have left
+            (ci > 0 && !lt_wait(&c->o, par ^ 1, ab, status)))      // P c of the last chunk is done
             break;
         tc_fence_after();
         mma_kk(tSc, sa, sb);
         mma_commit(&c->sc);
-        if (!lt_wait(&c->state, par, ab, status)) break;
+        if (!lt_wait(&c->state, par, ab, status) ||
+            (ci > 0 && !lt_wait(&c->drained, par ^ 1, ab, status)))
+            break;
         tc_fence_after();
-        mma_kk(to, sa, m_tile);
+        mma_kk(tO, sa, m_tile);
         mma_commit(&c->am);
         mma_commit(&c->empty[lt_slot(ta)]);
         if (!lt_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, status) ||
             !lt_wait(&c->parts, par, ab, status) || !lt_wait(&c->p, par, ab, status))
             break;
         tc_fence_after();
-        mma_pc(to, tSc, sv);
+        mma_pc(tO, tSc, sv);
         mma_commit(&c->o);
-        mma_mm(tMu, sv, m_tile, true);                 // lo
-        mma_mm(tMu, sv, mid_tile, false);
+        if (wk.exact) mma_mm(tMu, sv, m_tile, true);   // lo
+        mma_mm(tMu, sv, mid_tile, !wk.exact);
         mma_mm(tMu, sv, sb, false);                    // hi
         mma_commit(&c->mu);
         mma_commit(&c->empty[lt_slot(tb)]);
@@ -296,148 +321,174 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
     mbar_wait(&c->drain, 0);
 }
 
-// one row's outputs from its accumulator, to global memory
+// half of one row's outputs from its accumulator, to global memory
 __device__ __forceinline__ void lt_output(uint32_t to, float d, bool in, const LinProblem& q,
                                           int64_t at, LtCtrl* c, int lane) {
-#pragma unroll 1
-    for (int pc = 0; pc < 4; ++pc) {
-        float x[32];
-        tmem_ld32(to + 32 * pc, x);
-        if (pc == 3) {
-            tc_fence_before();
-            warp_arrive(&c->drained, lane);
-        }
-        if (!in) continue;
+    uint32_t x[2][32];
+    tmem_ld32_async(to, x[0]);
+    tmem_ld32_async(to + 32, x[1]);
+    tmem_wait_ld();
+    tc_fence_before();
+    warp_arrive(&c->drained, lane);
+    if (!in) return;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] *= d;
-        uint32_t w[8];
+    for (int pc = 0; pc < 2; ++pc) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[pc][i] = __float_as_uint(d * __uint_as_float(x[pc][i]));
         if (q.out_f32) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[8 * e + i]);
-                st_global32((float*)q.out + at + 32 * pc + 8 * e, w);
-            }
+            for (int e = 0; e < 4; ++e) st_global32((float*)q.out + at + 32 * pc + 8 * e, &x[pc][8 * e]);
         } else {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack_b2(x[16 * e + 2 * i], x[16 * e + 2 * i + 1]);
-                st_global32((__nv_bfloat16*)q.out + at + 32 * pc + 16 * e, w);
-            }
+            for (int i = 0; i < 16; ++i)
+                w[i] = pack_b2(__uint_as_float(x[pc][2 * i]), __uint_as_float(x[pc][2 * i + 1]));
+            st_global32((__nv_bfloat16*)q.out + at + 32 * pc, w);
+            st_global32((__nv_bfloat16*)q.out + at + 32 * pc + 16, w + 8);
         }
     }
 }
 
 __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
                         const LtWalk& wk, LtCtrl* c) {
-    const int quarter = threadIdx.x >> 5, lane = threadIdx.x & 31, r = threadIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
     const bool rev = wk.rev;
-    const uint32_t tSc = c->tmem + ((uint32_t)(quarter * 32) << 16), tO = tSc + 128;
-    const double lg = lin_log2(p.loggate, hv);
+    const uint32_t tSc = c->tmem + ((uint32_t)(quarter * 32) << 16) + 64 * h, tO = tSc + 128;
     const int64_t orow = (g.b * p.Hv + hv) * p.T + g.t0;
-    // d of this row; in reverse it depends on the chunk's rows
-    auto decay = [&](int n) {
-        return fmaxf(lin_pow(lg, rev ? (r < n ? n - 1 - r : 0) : r + 1), 0x1p-60f);
-    };
-    float d = 0.f, d_prev = 0.f;
-    int n_prev = 0;
+    float d = 0.f;
+#pragma unroll 1
     for (int ci = 0; ci <= wk.nch; ++ci) {
+        if (ci > 0) {                                  // the last chunk's outputs, while Mu is formed
+            const int r0 = wk.first(ci - 1);
+            if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) return;
+            tc_fence_after();
+            lt_output(tO, q.s_out * d, r < wk.rows(r0), q, (orow + r0 + r) * kD + 64 * h, c, lane);
+        }
         if (ci < wk.nch) {
             const int n = wk.rows(wk.first(ci));
-            d_prev = d;
-            if (ci == 0 || (rev && n != n_prev)) d = decay(n);
-            n_prev = n;
+            d = c->d[n < kRows][r];
             const float inv = 1.f / d;
-            // o of the last chunk is over too (Sc waited for it); it is looked at
-            // before p arrives, as the next o may come any time after that
-            if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status) ||
-                (ci > 0 && !warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)))
-                return;
+            if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status)) return;
             tc_fence_after();
 #pragma unroll 1
-            for (int piece = 0; piece < 4; ++piece) {
-                const int j0 = 32 * piece;
-                float v[32];
+            for (int pc = 0; pc < 2; ++pc) {
+                const int piece = 2 * h + pc, j0 = 32 * piece;
+                uint32_t w[16];
                 if (rev ? piece < quarter : piece > quarter) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0.f;
+                    for (int i = 0; i < 16; ++i) w[i] = 0;
                 } else {
-                    tmem_ld32(tSc + j0, v);
+                    uint32_t v[32];
+                    tmem_ld32_async(tSc + 32 * pc, v);
                     if (piece == quarter || n < kRows) {           // the border: one by one
                         const int dist0 = rev ? j0 - r : r - j0, sgn = rev ? 1 : -1;
+                        tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const int dist = dist0 + sgn * i;
-                            v[i] = dist >= 0 && j0 + i < n ? v[i] * (c->pw[dist & 127] * inv) : 0.f;
+                            const float x = __uint_as_float(v[i]) * (c->pw[dist & 127] * inv);
+                            v[i] = dist >= 0 && j0 + i < n ? __float_as_uint(x) : 0u;
                         }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_b2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                     } else {
                         const float f = c->pw[rev ? j0 - r : r - j0 - 31] * inv;
+                        const F2 f2(f, f);
+                        F2 s[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 s = *reinterpret_cast<const float4*>(&c->step[i]);
-                            v[i] *= f * s.x;
-                            v[i + 1] *= f * s.y;
-                            v[i + 2] *= f * s.z;
-                            v[i + 3] *= f * s.w;
+                        for (int i = 0; i < 16; i += 2) {
+                            const float4 t = *reinterpret_cast<const float4*>(&c->step[2 * i]);
+                            s[i] = mul2(F2(t.x, t.y), f2);
+                            s[i + 1] = mul2(F2(t.z, t.w), f2);
+                        }
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x, y;
+                            mul2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s[i])
+                                .get(x, y);
+                            w[i] = pack_b2(x, y);
                         }
                     }
                 }
-                tmem_st_b16(tSc + 16 * piece, v);      // behind the columns still to be read
+                tmem_st16(tSc + 16 * pc, w);           // behind the columns still to be read
             }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&c->p, lane);
-        }
-        if (ci > 0) {
-            const int r0 = wk.first(ci - 1);
-            if (ci == wk.nch) {
-                if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) return;
-                tc_fence_after();
-            }
-            lt_output(tO + 128 * ((ci - 1) & 1), q.s_out * (ci < wk.nch ? d_prev : d),
-                      r < wk.rows(r0), q, (orow + r0 + r) * kD, c, lane);
         }
     }
 }
 
 __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
                          const LtWalk& wk, uint32_t tiles, LtCtrl* c) {
-    const int warp = (threadIdx.x >> 5) - 4, lane = threadIdx.x & 31, h = warp >> 2;
+    const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, h = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const bool rev = wk.rev;
-    const uint32_t tMu = c->tmem + ((uint32_t)((warp & 3) * 32) << 16) + 384 + 64 * h;
+    const uint32_t tMu = c->tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + 64 * h;
+    const uint32_t tM = tMu + 128;
     const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
-    float m[64];
-    load_state(p, q, g, hv, rev, r, h, m);
-    float w = 0.f, an = 0.f, an_lo = 0.f;
-    int n_prev = 0;
-#pragma unroll 1
-    for (int ci = 0; ci < wk.nch; ++ci) {
-        const uint32_t par = ci & 1;
-        // the state as an operand of chunk ci (lo was in its tile, and has been read)
+    float* const out = wk.exact && q.mout
+                           ? q.mout + (g.seq * p.Hv + hv) * kLinState + r * kD + 64 * h
+                           : nullptr;
+    // 16 columns of the state to where they are needed next: TMEM and, in bf16,
+    // the operand tile, or behind the last chunk the outgoing state
+    auto put = [&](int pc, const float(&m)[16], bool last) {
+        if (last) {
+            if (!out) return;
+            uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            sts128(m_tile + op_off(r, 8 * h + e),
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(m[i]);
+            st_global32(out + 16 * pc, w);
+            st_global32(out + 16 * pc + 8, w + 8);
+            return;
+        }
+        tmem_st16f(tM + 16 * pc, m);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            sts128(m_tile + op_off(r, 8 * h + 2 * pc + e),
                    make_uint4(pack_b2(m[8 * e], m[8 * e + 1]), pack_b2(m[8 * e + 2], m[8 * e + 3]),
                               pack_b2(m[8 * e + 4], m[8 * e + 5]),
                               pack_b2(m[8 * e + 6], m[8 * e + 7])));
+    };
+    auto ready = [&]() {
+        tmem_wait_st();
         fence_async_smem();
         tc_fence_before();
         warp_arrive(&c->state, lane);
-        const int n = wk.rows(wk.first(ci));
-        if (n != n_prev) {
-            const double lg = lin_log2(p.loggate, hv);
-            w = r < n ? q.s_state * lin_pow(lg, rev ? r + 1 : n - 1 - r) : 0.f;
-            lin_pow2(lg, n, an, an_lo);
-            n_prev = n;
+    };
+    {   // the incoming state
+        const bool first = wk.rev ? g.k == g.m - 1 : g.k == 0;
+        const float* src = nullptr;
+        int rs = kD, cs = 1;
+        if (!first) {
+            src = q.ws + ((g.slot0 + (wk.rev ? g.k : g.k - 1)) * p.Hv + hv) * kLinState;
+        } else if (q.m0) {
+            src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
+            if (q.m0_t) { rs = 1; cs = kD; }
         }
+#pragma unroll 1
+        for (int pc = 0; pc < 4; ++pc) {
+            float m[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i] = src ? src[r * rs + (64 * h + 16 * pc + i) * cs] : 0.f;
+            put(pc, m, wk.nch == 0);
+        }
+        ready();
+    }
+#pragma unroll 1
+    for (int ci = 0; ci < wk.nch; ++ci) {
+        const uint32_t par = ci & 1;
+        const int n = wk.rows(wk.first(ci)), part = n < kRows;
+        const float w = c->w[part][r];
         const int tb = 3 * ci, tc = tb + 2;
         const uint32_t sb = tiles + lt_slot(tb) * kLtTile;
         if (!warp_wait(&c->full[lt_slot(tb)], lt_phase(tb), &c->abort, p.status) ||
-            !warp_wait(&c->am, par, &c->abort, p.status))          // Sc has read b, a M^T the state
-            return;
-        split_row(sb, mid_tile, m_tile, r, h, w, r >= n);
+            !warp_wait(wk.exact ? &c->am : &c->sc, par, &c->abort, p.status))
+            return;                                    // Sc has read b (a M^T the state)
+        if (wk.exact) split_row<3>(sb, mid_tile, m_tile, r, h, w, r >= n);
+        else split_row<2>(sb, mid_tile, m_tile, r, h, w, r >= n);
         if (n < kRows) {
             if (!warp_wait(&c->full[lt_slot(tc)], lt_phase(tc), &c->abort, p.status)) return;
             if (r >= n) zero_row(tiles + lt_slot(tc) * kLtTile, r, h);
@@ -446,10 +497,23 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
         warp_arrive(&c->parts, lane);
         if (!warp_wait(&c->mu, par, &c->abort, p.status)) return;
         tc_fence_after();
-        take_update(tMu, an, an_lo, m);
+        // M <- (an + an_lo) M + Mu: an's own rounding would add up over the
+        // chunks that a slow decay remembers
+        const float an = c->an[part], an_lo = c->an_lo[part];
+        const F2 a2(an, an), l2(an_lo, an_lo);
+#pragma unroll 1
+        for (int pc = 0; pc < 4; ++pc) {
+            float m[16], u[16];
+            tmem_ld2x16(tM + 16 * pc, m, tMu + 16 * pc, u);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const F2 v(m[i], m[i + 1]);
+                fma2(a2, v, fma2(l2, v, F2(u[i], u[i + 1]))).get(m[i], m[i + 1]);
+            }
+            put(pc, m, ci == wk.nch - 1);
+        }
+        if (ci < wk.nch - 1) ready();
     }
-    if (q.mout && (rev ? g.k == 0 : g.k == g.m - 1))
-        store_state(q.mout + (g.seq * p.Hv + hv) * kLinState, r, h, m);
 }
 
 // grid: (segments, Hv, problems)
@@ -461,7 +525,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         return;
     }
     const LinProblem& q = p.pr[blockIdx.z];
-    const LinSeg g = lin_find(p, blockIdx.x, 0);
+    const LinSeg g = lin_find(p, blockIdx.x, kAllSegments);
     if (!g.ok) return;
     const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + 7 * kLtTile);
@@ -471,34 +535,48 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
             mbar_init(&c->empty[i], 1);
         }
         mbar_init(&c->sc, 1);
-        mbar_init(&c->p, 4);
         mbar_init(&c->am, 1);
+        mbar_init(&c->p, 8);
         mbar_init(&c->parts, 8);
         mbar_init(&c->o, 1);
-        mbar_init(&c->drained, 4);
+        mbar_init(&c->drained, 8);
         mbar_init(&c->mu, 1);
         mbar_init(&c->state, 8);
         mbar_init(&c->drain, 1);
         c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 13) tmem_alloc(&c->tmem, 512);
-    if (threadIdx.x < kRows + 32) {
+    if (warp == 17) tmem_alloc(&c->tmem, 512);
+    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0,
+                    // a sequence of several segments has its outgoing state from steps 1
+                    // and 2; whether it is asked for changes no output
+                    g.m == 1};
+    {
         const double lg = lin_log2(p.loggate, hv);
-        const int i = threadIdx.x;
-        if (i < kRows) c->pw[i] = q.s_weight * lin_pow(lg, i);
-        else c->step[i - kRows] = lin_pow(lg, q.reverse ? i - kRows : 31 - (i - kRows));
+        const int t = threadIdx.x, i = t % kRows, n1 = wk.n - (wk.nch - 1) * kRows;
+        if (t < 2 * kRows) {
+            const int n = t < kRows ? kRows : n1;
+            c->w[t / kRows][i] = i < n ? q.s_state * lin_pow(lg, wk.rev ? i + 1 : n - 1 - i) : 0.f;
+        } else if (t < 4 * kRows) {
+            const int n = t < 3 * kRows ? kRows : n1;
+            c->d[t / kRows - 2][i] =
+                fmaxf(lin_pow(lg, wk.rev ? (i < n ? n - 1 - i : 0) : i + 1), 0x1p-60f);
+        } else if (i < 32) {
+            c->step[i] = lin_pow(lg, wk.rev ? i : 31 - i);
+        } else if (i < 34) {
+            lin_pow2(lg, i == 32 ? kRows : n1, c->an[i - 32], c->an_lo[i - 32]);
+        }
+        if (t < kRows) c->pw[t] = q.s_weight * lin_pow(lg, t);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0};
     const uint32_t tiles = su32(smem);
-    if (warp < 4) {
+    if (warp < 8) {
         lt_rows(p, q, g, hv, wk, c);
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         lt_state(p, q, g, hv, wk, tiles, c);
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         if (lane == 0) lt_load(k, q, g, hv, wk, smem, c);
     } else if (lane == 0) {
         lt_multiply(wk, tiles, c, p.status);
@@ -506,7 +584,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(c->tmem, 512);
     }
@@ -517,7 +595,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
 // Five ring tiles, one each for mid and lo; the parts of a chunk are formed
 // while hi of the one before is multiplied, which needs two accumulators.
 constexpr int kLsThreads = 10 * 32;
-struct __align__(8) LsCtrl {
+struct __align__(16) LsCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
     uint64_t parts, read, mu[2], drain;
     uint32_t tmem;
@@ -525,7 +603,7 @@ struct __align__(8) LsCtrl {
 };
 constexpr int kLsSmem = 7 * kLtTile + (int)sizeof(LsCtrl);
 
-// grid: (boundaries, Hv, problems)
+// grid: (segments of sequences that have several, Hv, problems)
 __global__ void __launch_bounds__(kLsThreads, 1)
 k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -535,14 +613,11 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         return;
     }
     const LinProblem& q = p.pr[blockIdx.z];
-    LinSeg g = lin_find(p, blockIdx.x, 1);
+    const LinSeg g = lin_find(p, blockIdx.x, kCutSegments);
     if (!g.ok) return;
-    if (q.reverse) {                                   // boundary k: what segment k + 1 adds
-        g.k += 1;
-        g.t0 = g.seq_t0 + g.k * p.seg_len;
-        g.n = g.seq_n - g.k * p.seg_len < p.seg_len ? g.seq_n - g.k * p.seg_len : p.seg_len;
-    }
     const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* const dst = lin_added(p, q, g, hv);
+    if (!dst) return;
     LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + 7 * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLtRing; ++i) {
@@ -563,7 +638,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     tc_fence_after();
     const uint32_t tm = c->tmem, tiles = su32(smem);
     const uint32_t mid_tile = tiles + 5 * kLtTile, lo_tile = tiles + 6 * kLtTile;
-    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0};
+    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0, true};
     int* const ab = &c->abort;
     if (warp == 8) {
         if (lane == 0) {
@@ -627,7 +702,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
                 ok = warp_wait(&c->full[lt_slot(tb)], lt_phase(tb), ab, p.status) &&
                      (ci == 0 || warp_wait(&c->read, (ci - 1) & 1, ab, p.status));
                 if (!ok) break;
-                split_row(sb, mid_tile, lo_tile, r, h, w, r >= n);
+                split_row<3>(sb, mid_tile, lo_tile, r, h, w, r >= n);
                 if (n < kRows) {
                     ok = warp_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, p.status);
                     if (!ok) break;
@@ -646,9 +721,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
                             last ? a_lo[0] : a_lo[1], m);
             }
         }
-        if (ok)
-            store_state(q.ws + ((g.slot0 + (q.reverse ? g.k - 1 : g.k)) * p.Hv + hv) * kLinState, r,
-                        h, m);
+        if (ok) store_state(dst, r, h, m);
     }
     __syncwarp();
     tc_fence_before();
@@ -693,7 +766,7 @@ cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, boo
         e = cudaFuncSetAttribute(tcg::k_linear_state_tc,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, tcg::kLsSmem);
         if (e != cudaSuccess) return e;
-        tcg::k_linear_state_tc<<<dim3((unsigned)pl.bounds, (unsigned)a.Hv, nprob),
+        tcg::k_linear_state_tc<<<dim3((unsigned)pl.cut_segs, (unsigned)a.Hv, nprob),
                                  tcg::kLsThreads, tcg::kLsSmem, st>>>(k);
     } else {
         e = cudaFuncSetAttribute(tcg::k_linear_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
