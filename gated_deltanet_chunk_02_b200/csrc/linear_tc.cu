@@ -51,20 +51,21 @@ constexpr int kLtRing = 5;
 constexpr int kLtThreads = 18 * 32;
 
 struct LinTcArgs {
-    CUtensorMap map[4];                                // the call's distinct tensors
+    CUtensorMap map[4];                                // the call's distinct inputs
+    CUtensorMap out[kLinProblems];                     // bf16 outputs, boxes of 32 rows
     int8_t ia[kLinProblems], ib[kLinProblems], ic[kLinProblems];
     LinArgs a;
 };
 
 struct __align__(16) LtCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t sc, am, p, parts, o, drained, mu, state, drain;
+    uint64_t sc, am, p, parts, o, drained, mu, state, stored[2], drain;
     __align__(16) float pw[kRows];                     // s lambda^n
     __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
     // by row, for whole chunks [0] and for the segment's last rows [1]: the
     // weight of b, d; and lambda^n as a sum of two floats
     float w[2][kRows], d[2][kRows];
-    float an[2], an_lo[2];
+    float an[2], an_lo[2], lambda;
     uint32_t tmem;
     int abort;
 };
@@ -72,9 +73,10 @@ constexpr int kLtSmem = 7 * kLtTile + (int)sizeof(LtCtrl);
 static_assert(kLtSmem <= 232448, "shared memory budget");
 static_assert(offsetof(LtCtrl, step) % 16 == 0, "step is read 16 bytes at a time");
 
-// Bounded wait; false once it ran out or another role's did.
-__device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
-    if (mbar_try(b, parity)) return true;
+// Bounded wait; false once it ran out or another role's did.  The loop is a
+// function of its own: a dozen copies of it would not leave the roles' code in
+// the instruction cache.
+__device__ __noinline__ bool lt_wait_long(uint64_t* b, uint32_t parity, int* abort, int* status) {
     unsigned long long t0 = 0;
     for (int i = 0;; ++i) {
         if (mbar_try(b, parity)) return true;
@@ -88,6 +90,9 @@ __device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort
     atomicExch(abort, 1);
     raise_status(status, kStatusTimeout);
     return false;
+}
+__device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
+    return mbar_try(b, parity) || lt_wait_long(b, parity, abort, status);
 }
 // the same for a whole warp, with one answer
 __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
@@ -181,6 +186,14 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t* w) {
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(p));
+    return p != 0;
+}
 // one arrival for the warp, behind what all its lanes did
 __device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
     __syncwarp();
@@ -214,15 +227,23 @@ __device__ __forceinline__ int lt_row0(const LinArgs& p, const LinSeg& g, int hv
     const int64_t H = p.Hv / group;
     return (int)((g.b * H + hv / group) * p.T + g.t0);
 }
-__device__ __forceinline__ int lt_slot(int t) { return t % kLtRing; }
-__device__ __forceinline__ uint32_t lt_phase(int t) { return (uint32_t)(t / kLtRing) & 1; }
+// A place in the ring: counted on, as a division per tile costs a single
+// thread more than the tile's products take to issue.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ void next() {
+        if (++slot == kLtRing) { slot = 0; phase ^= 1; }
+    }
+    __device__ uint32_t tile(uint32_t tiles) const { return tiles + slot * kLtTile; }
+};
 
-// 16 columns of this thread's lane -> TMEM, raw
-__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
-    uint32_t w[16];
+// 32 columns of this thread's lane -> TMEM, raw
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&w)[32]) {
+    float v[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
-    tmem_st16(taddr, w);
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
+    tmem_st32(taddr, v);
 }
 __device__ __forceinline__ void store_state(float* dst, int r, int h, const float (&m)[64]) {
 #pragma unroll
@@ -251,6 +272,12 @@ __device__ __forceinline__ void take_update(uint32_t mu, float a, float a_lo, fl
     }
 }
 
+// Whatever stopped a walk after t tiles, copies in flight land before the CTA ends.
+__device__ __forceinline__ void land(uint64_t* full, int t) {
+    for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
+        mbar_wait(&full[i % kLtRing], (uint32_t)(i / kLtRing) & 1);
+}
+
 // ---- the roles of k_linear_tc ----
 struct LtWalk {                                        // chunks of a segment, in walking order
     int n, nch;
@@ -266,110 +293,178 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
     const CUtensorMap *mb = &k.map[k.ib[z]], *ma = &k.map[k.ia[z]], *mc = &k.map[k.ic[z]];
     const int yb = lt_row0(k.a, g, hv, q.gb), ya = lt_row0(k.a, g, hv, q.ga),
               yc = lt_row0(k.a, g, hv, q.gc);
-    int t = 0;
-    for (; t < 3 * wk.nch; ++t) {
-        const int s = lt_slot(t), m = t % 3, r0 = wk.first(t / 3);
-        if (t >= kLtRing && !lt_wait(&c->empty[s], lt_phase(t) ^ 1, &c->abort, k.a.status)) break;
+    const int tiles = 3 * wk.nch;
+    Ring at;
+    int t = 0, m = 0, r0 = wk.first(0);
+    for (; t < tiles; ++t) {
+        const int s = at.slot;
+        if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, &c->abort, k.a.status)) break;
+        // b comes where the a of two chunks ago was, and after that chunk's outputs
+        if (m == 0 && t >= 6 &&
+            !lt_wait(&c->stored[t / 3 & 1], ((t / 3 - 2) >> 1) & 1, &c->abort, k.a.status))
+            break;
         const CUtensorMap* mp = m == 0 ? mb : (m == 1 ? ma : mc);
         const int y = r0 + (m == 0 ? yb : (m == 1 ? ya : yc));
         mbar_expect_tx(&c->full[s], kLtTile);
         tma_load_2d(smem + s * kLtTile, mp, 0, y, &c->full[s]);
         tma_load_2d(smem + s * kLtTile + kRows * 128, mp, 64, y, &c->full[s]);
+        at.next();
+        if (++m == 3) { m = 0; r0 += wk.rev ? -kRows : kRows; }
     }
-    // whatever stopped the walk, copies in flight land before the CTA ends
-    for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
-        mbar_wait(&c->full[lt_slot(i)], lt_phase(i));
+    land(c->full, t);
 }
 
+// The whole warp walks and one lane issues: descriptors and addresses are then
+// uniform values; in a walk of one lane each of them is moved to a uniform
+// register first, and the eight steps of a product took 1500 cycles to issue.
 __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* status) {
-    const uint32_t tSc = c->tmem, tO = tSc + 128, tMu = tSc + 256;
+    const uint32_t tSc = __shfl_sync(0xffffffffu, c->tmem, 0), tO = tSc + 128, tMu = tSc + 256;
     const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
     int* const ab = &c->abort;
+    const bool lead = elect_one();
+    Ring at;
+#pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
         const uint32_t par = ci & 1;
-        const int tb = 3 * ci, ta = tb + 1, tc = tb + 2;
-        const uint32_t sb = tiles + lt_slot(tb) * kLtTile, sa = tiles + lt_slot(ta) * kLtTile,
-                       sv = tiles + lt_slot(tc) * kLtTile;
-        if (!lt_wait(&c->full[lt_slot(tb)], lt_phase(tb), ab, status) ||
-            !lt_wait(&c->full[lt_slot(ta)], lt_phase(ta), ab, status) ||
-            (ci > 0 && !lt_wait(&c->o, par ^ 1, ab, status)))      // P c of the last chunk is done
+        const Ring b = at;
+        at.next();
+        const Ring a = at;
+        at.next();
+        const Ring v = at;
+        at.next();
+        const uint32_t sb = b.tile(tiles), sa = a.tile(tiles), sv = v.tile(tiles);
+        if (!warp_wait(&c->full[b.slot], b.phase, ab, status) ||
+            !warp_wait(&c->full[a.slot], a.phase, ab, status) ||
+            (ci > 0 && !warp_wait(&c->o, par ^ 1, ab, status)))    // P c of the last chunk is done
             break;
         tc_fence_after();
-        mma_kk(tSc, sa, sb);
-        mma_commit(&c->sc);
-        if (!lt_wait(&c->state, par, ab, status) ||
-            (ci > 0 && !lt_wait(&c->drained, par ^ 1, ab, status)))
+        if (lead) {
+            mma_kk(tSc, sa, sb);
+            mma_commit(&c->sc);
+        }
+        __syncwarp();
+        if (!warp_wait(&c->state, par, ab, status) ||
+            (ci > 0 && !warp_wait(&c->drained, par ^ 1, ab, status)))
             break;
         tc_fence_after();
-        mma_kk(tO, sa, m_tile);
-        mma_commit(&c->am);
-        mma_commit(&c->empty[lt_slot(ta)]);
-        if (!lt_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, status) ||
-            !lt_wait(&c->parts, par, ab, status) || !lt_wait(&c->p, par, ab, status))
+        if (lead) {
+            mma_kk(tO, sa, m_tile);
+            mma_commit(&c->am);
+            mma_commit(&c->empty[a.slot]);
+        }
+        __syncwarp();
+        if (!warp_wait(&c->full[v.slot], v.phase, ab, status) ||
+            !warp_wait(&c->parts, par, ab, status))
             break;
         tc_fence_after();
-        mma_pc(tO, tSc, sv);
-        mma_commit(&c->o);
-        if (wk.exact) mma_mm(tMu, sv, m_tile, true);   // lo
-        mma_mm(tMu, sv, mid_tile, !wk.exact);
-        mma_mm(tMu, sv, sb, false);                    // hi
-        mma_commit(&c->mu);
-        mma_commit(&c->empty[lt_slot(tb)]);
-        mma_commit(&c->empty[lt_slot(tc)]);
+        if (lead) {
+            if (wk.exact) mma_mm(tMu, sv, m_tile, true);           // lo
+            mma_mm(tMu, sv, mid_tile, !wk.exact);
+            mma_mm(tMu, sv, sb, false);                            // hi
+            mma_commit(&c->mu);                        // first: the state is the longer chain
+            mma_commit(&c->empty[b.slot]);
+        }
+        __syncwarp();
+        if (!warp_wait(&c->p, par, ab, status)) break;
+        tc_fence_after();
+        if (lead) {
+            mma_pc(tO, tSc, sv);
+            mma_commit(&c->o);
+            mma_commit(&c->empty[v.slot]);
+        }
+        __syncwarp();
     }
-    mma_commit(&c->drain);                             // nothing in flight when TMEM is freed
-    mbar_wait(&c->drain, 0);
+    if (lead) {
+        mma_commit(&c->drain);                         // nothing in flight when TMEM is freed
+        mbar_wait(&c->drain, 0);
+    }
+    __syncwarp();
 }
 
-// half of one row's outputs from its accumulator, to global memory
-__device__ __forceinline__ void lt_output(uint32_t to, float d, bool in, const LinProblem& q,
-                                          int64_t at, LtCtrl* c, int lane) {
+// Half of one row's outputs from its accumulator: through the tile of a (its
+// products are done) and out by TMA, 32 rows a warp; straight to memory where
+// rows of the chunk are not the segment's, or in float32.  Direct stores of
+// whole rows take the shared-memory pipe for 1000 cycles a chunk.
+__device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, int h, int64_t row,
+                                          const LinProblem& q, const CUtensorMap* map,
+                                          uint32_t a_tile, LtCtrl* c, int chunk) {
+    const int lane = threadIdx.x & 31;
     uint32_t x[2][32];
     tmem_ld32_async(to, x[0]);
     tmem_ld32_async(to + 32, x[1]);
     tmem_wait_ld();
     tc_fence_before();
     warp_arrive(&c->drained, lane);
-    if (!in) return;
+    const bool by_tma = n == kRows && !q.out_f32;
+    const int64_t at = (row + r) * kD + 64 * h;
 #pragma unroll
     for (int pc = 0; pc < 2; ++pc) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[pc][i] = __float_as_uint(d * __uint_as_float(x[pc][i]));
         if (q.out_f32) {
+            if (r < n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) st_global32((float*)q.out + at + 32 * pc + 8 * e, &x[pc][8 * e]);
-        } else {
-            uint32_t w[16];
+                for (int e = 0; e < 4; ++e)
+                    st_global32((float*)q.out + at + 32 * pc + 8 * e, &x[pc][8 * e]);
+            continue;
+        }
+        uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                w[i] = pack_b2(__uint_as_float(x[pc][2 * i]), __uint_as_float(x[pc][2 * i + 1]));
+        for (int i = 0; i < 16; ++i)
+            w[i] = pack_b2(__uint_as_float(x[pc][2 * i]), __uint_as_float(x[pc][2 * i + 1]));
+        if (by_tma) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sts128(a_tile + op_off(r, 8 * h + 4 * pc + e),
+                       make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+        } else if (r < n) {
             st_global32((__nv_bfloat16*)q.out + at + 32 * pc, w);
             st_global32((__nv_bfloat16*)q.out + at + 32 * pc + 16, w + 8);
         }
     }
+    if (by_tma) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile(
+                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                    map),
+                "r"(64 * h), "r"((int)(row + r)), "r"(a_tile + op_off(r, 8 * h))
+                : "memory");
+            bulk_commit();
+            bulk_wait_read();
+        }
+    }
+    warp_arrive(&c->stored[chunk & 1], lane);
 }
 
 __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
-                        const LtWalk& wk, LtCtrl* c) {
+                        const LtWalk& wk, uint32_t tiles, const CUtensorMap* map, LtCtrl* c) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const bool rev = wk.rev;
     const uint32_t tSc = c->tmem + ((uint32_t)(quarter * 32) << 16) + 64 * h, tO = tSc + 128;
     const int64_t orow = (g.b * p.Hv + hv) * p.T + g.t0;
+    const float lam = c->lambda;
     float d = 0.f;
+    Ring at;
 #pragma unroll 1
     for (int ci = 0; ci <= wk.nch; ++ci) {
         if (ci > 0) {                                  // the last chunk's outputs, while Mu is formed
             const int r0 = wk.first(ci - 1);
-            if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) return;
+            at.next();
+            const uint32_t a_tile = at.tile(tiles);
+            at.next();
+            at.next();
+            if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) break;
             tc_fence_after();
-            lt_output(tO, q.s_out * d, r < wk.rows(r0), q, (orow + r0 + r) * kD + 64 * h, c, lane);
+            lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, map, a_tile, c, ci - 1);
         }
         if (ci < wk.nch) {
             const int n = wk.rows(wk.first(ci));
             d = c->d[n < kRows][r];
             const float inv = 1.f / d;
-            if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status)) return;
+            if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int pc = 0; pc < 2; ++pc) {
@@ -381,14 +476,24 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
                 } else {
                     uint32_t v[32];
                     tmem_ld32_async(tSc + 32 * pc, v);
-                    if (piece == quarter || n < kRows) {           // the border: one by one
-                        const int dist0 = rev ? j0 - r : r - j0, sgn = rev ? 1 : -1;
+                    if (piece == quarter) {
+                        // the border: 1, lambda, lambda^2, .. away from the diagonal
+                        float t = 0.f;
+                        const float one = q.s_weight * inv;
                         tmem_wait_ld();
+                        if (!rev) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int dist = dist0 + sgn * i;
-                            const float x = __uint_as_float(v[i]) * (c->pw[dist & 127] * inv);
-                            v[i] = dist >= 0 && j0 + i < n ? __float_as_uint(x) : 0u;
+                            for (int i = 31; i >= 0; --i) {
+                                t = i == lane ? one : t * lam;
+                                v[i] = i <= lane ? __float_as_uint(__uint_as_float(v[i]) * t) : 0u;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                t = i == lane ? one : t * lam;
+                                v[i] = i >= lane && j0 + i < n
+                                           ? __float_as_uint(__uint_as_float(v[i]) * t) : 0u;
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -404,6 +509,10 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
                             s[i + 1] = mul2(F2(t.z, t.w), f2);
                         }
                         tmem_wait_ld();
+                        if (rev && n < kRows) {        // columns that are not the segment's rows
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = j0 + i < n ? v[i] : 0u;
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float x, y;
@@ -420,6 +529,7 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
             warp_arrive(&c->p, lane);
         }
     }
+    if (lane == 0) bulk_wait_all();
 }
 
 __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
@@ -432,25 +542,25 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
     float* const out = wk.exact && q.mout
                            ? q.mout + (g.seq * p.Hv + hv) * kLinState + r * kD + 64 * h
                            : nullptr;
-    // 16 columns of the state to where they are needed next: TMEM and, in bf16,
+    // 32 columns of the state to where they are needed next: TMEM and, in bf16,
     // the operand tile, or behind the last chunk the outgoing state
-    auto put = [&](int pc, const float(&m)[16], bool last) {
+    auto put = [&](int pc, const uint32_t(&m)[32], bool last) {
         if (last) {
             if (!out) return;
-            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(m[i]);
-            st_global32(out + 16 * pc, w);
-            st_global32(out + 16 * pc + 8, w + 8);
+            for (int e = 0; e < 4; ++e) st_global32(out + 32 * pc + 8 * e, &m[8 * e]);
             return;
         }
-        tmem_st16f(tM + 16 * pc, m);
+        tmem_st32u(tM + 32 * pc, m);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            sts128(m_tile + op_off(r, 8 * h + 2 * pc + e),
-                   make_uint4(pack_b2(m[8 * e], m[8 * e + 1]), pack_b2(m[8 * e + 2], m[8 * e + 3]),
-                              pack_b2(m[8 * e + 4], m[8 * e + 5]),
-                              pack_b2(m[8 * e + 6], m[8 * e + 7])));
+        for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = pack_b2(__uint_as_float(m[8 * e + 2 * i]),
+                               __uint_as_float(m[8 * e + 2 * i + 1]));
+            sts128(m_tile + op_off(r, 8 * h + 4 * pc + e), make_uint4(w[0], w[1], w[2], w[3]));
+        }
     };
     auto ready = [&]() {
         tmem_wait_st();
@@ -469,29 +579,35 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
             if (q.m0_t) { rs = 1; cs = kD; }
         }
 #pragma unroll 1
-        for (int pc = 0; pc < 4; ++pc) {
-            float m[16];
+        for (int pc = 0; pc < 2; ++pc) {
+            uint32_t m[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m[i] = src ? src[r * rs + (64 * h + 16 * pc + i) * cs] : 0.f;
+            for (int i = 0; i < 32; ++i)
+                m[i] = src ? __float_as_uint(src[r * rs + (64 * h + 32 * pc + i) * cs]) : 0u;
             put(pc, m, wk.nch == 0);
         }
         ready();
     }
+    Ring at;
 #pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
         const uint32_t par = ci & 1;
         const int n = wk.rows(wk.first(ci)), part = n < kRows;
         const float w = c->w[part][r];
-        const int tb = 3 * ci, tc = tb + 2;
-        const uint32_t sb = tiles + lt_slot(tb) * kLtTile;
-        if (!warp_wait(&c->full[lt_slot(tb)], lt_phase(tb), &c->abort, p.status) ||
+        const Ring b = at;
+        at.next();
+        at.next();
+        const Ring v = at;
+        at.next();
+        const uint32_t sb = b.tile(tiles);
+        if (!warp_wait(&c->full[b.slot], b.phase, &c->abort, p.status) ||
             !warp_wait(wk.exact ? &c->am : &c->sc, par, &c->abort, p.status))
             return;                                    // Sc has read b (a M^T the state)
         if (wk.exact) split_row<3>(sb, mid_tile, m_tile, r, h, w, r >= n);
         else split_row<2>(sb, mid_tile, m_tile, r, h, w, r >= n);
         if (n < kRows) {
-            if (!warp_wait(&c->full[lt_slot(tc)], lt_phase(tc), &c->abort, p.status)) return;
-            if (r >= n) zero_row(tiles + lt_slot(tc) * kLtTile, r, h);
+            if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status)) return;
+            if (r >= n) zero_row(v.tile(tiles), r, h);
         }
         fence_async_smem();
         warp_arrive(&c->parts, lane);
@@ -502,13 +618,19 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
         const float an = c->an[part], an_lo = c->an_lo[part];
         const F2 a2(an, an), l2(an_lo, an_lo);
 #pragma unroll 1
-        for (int pc = 0; pc < 4; ++pc) {
-            float m[16], u[16];
-            tmem_ld2x16(tM + 16 * pc, m, tMu + 16 * pc, u);
+        for (int pc = 0; pc < 2; ++pc) {
+            uint32_t m[32], u[32];
+            tmem_ld32_async(tM + 32 * pc, m);
+            tmem_ld32_async(tMu + 32 * pc, u);
+            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const F2 v(m[i], m[i + 1]);
-                fma2(a2, v, fma2(l2, v, F2(u[i], u[i + 1]))).get(m[i], m[i + 1]);
+            for (int i = 0; i < 32; i += 2) {
+                const F2 x(__uint_as_float(m[i]), __uint_as_float(m[i + 1]));
+                float y, z;
+                fma2(a2, x, fma2(l2, x, F2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]))))
+                    .get(y, z);
+                m[i] = __float_as_uint(y);
+                m[i + 1] = __float_as_uint(z);
             }
             put(pc, m, ci == wk.nch - 1);
         }
@@ -542,6 +664,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         mbar_init(&c->drained, 8);
         mbar_init(&c->mu, 1);
         mbar_init(&c->state, 8);
+        mbar_init(&c->stored[0], 8);
+        mbar_init(&c->stored[1], 8);
         mbar_init(&c->drain, 1);
         c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -565,6 +689,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
             c->step[i] = lin_pow(lg, wk.rev ? i : 31 - i);
         } else if (i < 34) {
             lin_pow2(lg, i == 32 ? kRows : n1, c->an[i - 32], c->an_lo[i - 32]);
+        } else if (i == 34) {
+            c->lambda = lin_pow(lg, 1);
         }
         if (t < kRows) c->pw[t] = q.s_weight * lin_pow(lg, t);
     }
@@ -573,12 +699,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     tc_fence_after();
     const uint32_t tiles = su32(smem);
     if (warp < 8) {
-        lt_rows(p, q, g, hv, wk, c);
+        lt_rows(p, q, g, hv, wk, tiles, &k.out[blockIdx.z], c);
     } else if (warp < 16) {
         lt_state(p, q, g, hv, wk, tiles, c);
     } else if (warp == 16) {
         if (lane == 0) lt_load(k, q, g, hv, wk, smem, c);
-    } else if (lane == 0) {
+    } else {
         lt_multiply(wk, tiles, c, p.status);
     }
     __syncwarp();
@@ -591,17 +717,21 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
 }
 
 // ---- step 1: what a segment adds to the state ----
-// Warps 0-7 split b and carry the state, warp 8 loads, warp 9 multiplies.
-// Five ring tiles, one each for mid and lo; the parts of a chunk are formed
-// while hi of the one before is multiplied, which needs two accumulators.
-constexpr int kLsThreads = 10 * 32;
+// Warps 0-7 split b, warps 8-15 carry the state in registers, warp 16 loads,
+// warp 17 multiplies.  Five ring tiles, one each for mid and lo; the parts of a
+// chunk are formed while hi of the one before is multiplied and its sum is
+// taken, from two accumulators in turn.
+constexpr int kLsThreads = 18 * 32;
 struct __align__(16) LsCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t parts, read, mu[2], drain;
+    uint64_t parts, read, mu[2], taken[2], drain;
+    float w[2][kRows];                                 // as in LtCtrl
+    float an[2], an_lo[2];
     uint32_t tmem;
     int abort;
 };
 constexpr int kLsSmem = 7 * kLtTile + (int)sizeof(LsCtrl);
+static_assert(kLsSmem <= 232448, "shared memory budget");
 
 // grid: (segments of sequences that have several, Hv, problems)
 __global__ void __launch_bounds__(kLsThreads, 1)
@@ -628,105 +758,124 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         mbar_init(&c->read, 1);
         mbar_init(&c->mu[0], 1);
         mbar_init(&c->mu[1], 1);
+        mbar_init(&c->taken[0], 8);
+        mbar_init(&c->taken[1], 8);
         mbar_init(&c->drain, 1);
         c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc(&c->tmem, 256);
+    if (warp == 17) tmem_alloc(&c->tmem, 256);
+    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0, true};
+    {
+        const double lg = lin_log2(p.loggate, hv);
+        const int t = threadIdx.x, i = t % kRows, n1 = wk.n - (wk.nch - 1) * kRows;
+        if (t < 2 * kRows) {
+            const int n = t < kRows ? kRows : n1;
+            c->w[t / kRows][i] = i < n ? q.s_state * lin_pow(lg, wk.rev ? i + 1 : n - 1 - i) : 0.f;
+        } else if (t < 2 * kRows + 2) {
+            lin_pow2(lg, i == 0 ? kRows : n1, c->an[i], c->an_lo[i]);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = c->tmem, tiles = su32(smem);
     const uint32_t mid_tile = tiles + 5 * kLtTile, lo_tile = tiles + 6 * kLtTile;
-    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0, true};
     int* const ab = &c->abort;
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             const int z = blockIdx.z;
             const CUtensorMap *mb = &k.map[k.ib[z]], *mc = &k.map[k.ic[z]];
             const int yb = lt_row0(p, g, hv, q.gb), yc = lt_row0(p, g, hv, q.gc);
-            int t = 0;
+            Ring at;
+            int t = 0, r0 = wk.first(0);
             for (; t < 2 * wk.nch; ++t) {
-                const int s = lt_slot(t), y = wk.first(t >> 1) + (t & 1 ? yc : yb);
-                if (t >= kLtRing && !lt_wait(&c->empty[s], lt_phase(t) ^ 1, ab, p.status)) break;
+                const int s = at.slot, y = r0 + (t & 1 ? yc : yb);
+                if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, ab, p.status)) break;
                 mbar_expect_tx(&c->full[s], kLtTile);
                 tma_load_2d(smem + s * kLtTile, t & 1 ? mc : mb, 0, y, &c->full[s]);
                 tma_load_2d(smem + s * kLtTile + kRows * 128, t & 1 ? mc : mb, 64, y, &c->full[s]);
+                at.next();
+                if (t & 1) r0 += wk.rev ? -kRows : kRows;
             }
-            for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
-                mbar_wait(&c->full[lt_slot(i)], lt_phase(i));
+            land(c->full, t);
         }
-    } else if (warp == 9) {
-        if (lane == 0) {
-            for (int ci = 0; ci < wk.nch; ++ci) {
-                const int tb = 2 * ci, tc = tb + 1;
-                if (!lt_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, p.status) ||
-                    !lt_wait(&c->parts, ci & 1, ab, p.status))
-                    break;
-                tc_fence_after();
-                const uint32_t sb = tiles + lt_slot(tb) * kLtTile,
-                               sv = tiles + lt_slot(tc) * kLtTile, d = tm + 128 * (ci & 1);
+    } else if (warp == 17) {
+        const bool lead = elect_one();
+        const uint32_t td = __shfl_sync(0xffffffffu, tm, 0);
+        Ring at;
+#pragma unroll 1
+        for (int ci = 0; ci < wk.nch; ++ci) {
+            const Ring b = at;
+            at.next();
+            const Ring v = at;
+            at.next();
+            if (!warp_wait(&c->full[v.slot], v.phase, ab, p.status) ||
+                !warp_wait(&c->parts, ci & 1, ab, p.status) ||
+                (ci > 1 &&                             // the sum of ci - 2 has left
+                 !warp_wait(&c->taken[ci & 1], ((ci >> 1) & 1) ^ 1, ab, p.status)))
+                break;
+            tc_fence_after();
+            const uint32_t sb = b.tile(tiles), sv = v.tile(tiles), d = td + 128 * (ci & 1);
+            if (lead) {
                 mma_mm(d, sv, lo_tile, true);
                 mma_mm(d, sv, mid_tile, false);
                 mma_commit(&c->read);
                 mma_mm(d, sv, sb, false);
                 mma_commit(&c->mu[ci & 1]);
-                mma_commit(&c->empty[lt_slot(tb)]);
-                mma_commit(&c->empty[lt_slot(tc)]);
+                mma_commit(&c->empty[b.slot]);
+                mma_commit(&c->empty[v.slot]);
             }
+            __syncwarp();
+        }
+        if (lead) {
             mma_commit(&c->drain);
             mbar_wait(&c->drain, 0);
         }
-    } else {
+    } else if (warp < 8) {
         const int h = warp >> 2, r = (warp & 3) * 32 + lane;
+        Ring at;
+#pragma unroll 1
+        for (int ci = 0; ci < wk.nch; ++ci) {
+            const int n = wk.rows(wk.first(ci));
+            const Ring b = at;
+            at.next();
+            const Ring v = at;
+            at.next();
+            if (!warp_wait(&c->full[b.slot], b.phase, ab, p.status) ||
+                (ci > 0 && !warp_wait(&c->read, (ci - 1) & 1, ab, p.status)))
+                break;
+            split_row<3>(b.tile(tiles), mid_tile, lo_tile, r, h, c->w[n < kRows][r], r >= n);
+            if (n < kRows) {
+                if (!warp_wait(&c->full[v.slot], v.phase, ab, p.status)) break;
+                if (r >= n) zero_row(v.tile(tiles), r, h);
+            }
+            fence_async_smem();
+            warp_arrive(&c->parts, lane);
+        }
+    } else {
+        const int h = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t tMu = tm + ((uint32_t)((warp & 3) * 32) << 16) + 64 * h;
-        const double lg = lin_log2(p.loggate, hv);
         float m[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) m[i] = 0.f;
-        float w = 0.f, a[2] = {0.f, 0.f}, a_lo[2] = {0.f, 0.f};  // this chunk's decay, the last one's
-        int n_prev = 0;
         bool ok = true;
 #pragma unroll 1
-        for (int ci = 0; ci <= wk.nch; ++ci) {
-            if (ci < wk.nch) {
-                const int tb = 2 * ci, tc = tb + 1, n = wk.rows(wk.first(ci));
-                a[1] = a[0];
-                a_lo[1] = a_lo[0];
-                if (n != n_prev) {
-                    w = r < n ? q.s_state * lin_pow(lg, q.reverse ? r + 1 : n - 1 - r) : 0.f;
-                    lin_pow2(lg, n, a[0], a_lo[0]);
-                    n_prev = n;
-                }
-                const uint32_t sb = tiles + lt_slot(tb) * kLtTile;
-                ok = warp_wait(&c->full[lt_slot(tb)], lt_phase(tb), ab, p.status) &&
-                     (ci == 0 || warp_wait(&c->read, (ci - 1) & 1, ab, p.status));
-                if (!ok) break;
-                split_row<3>(sb, mid_tile, lo_tile, r, h, w, r >= n);
-                if (n < kRows) {
-                    ok = warp_wait(&c->full[lt_slot(tc)], lt_phase(tc), ab, p.status);
-                    if (!ok) break;
-                    if (r >= n) zero_row(tiles + lt_slot(tc) * kLtTile, r, h);
-                }
-                fence_async_smem();
-                tc_fence_before();                     // the update of ci - 2 has left its accumulator
-                warp_arrive(&c->parts, lane);
-            }
-            if (ci > 0) {
-                ok = warp_wait(&c->mu[(ci - 1) & 1], ((ci - 1) >> 1) & 1, ab, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                const bool last = ci == wk.nch;
-                take_update(tMu + 128 * ((ci - 1) & 1), last ? a[0] : a[1],
-                            last ? a_lo[0] : a_lo[1], m);
-            }
+        for (int ci = 0; ci < wk.nch && ok; ++ci) {
+            const int part = wk.rows(wk.first(ci)) < kRows;
+            ok = warp_wait(&c->mu[ci & 1], (ci >> 1) & 1, ab, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            take_update(tMu + 128 * (ci & 1), c->an[part], c->an_lo[part], m);
+            tc_fence_before();
+            warp_arrive(&c->taken[ci & 1], lane);
         }
         if (ok) store_state(dst, r, h, m);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tm, 256);
     }
@@ -761,6 +910,10 @@ cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, boo
             k.ib[i] = (int8_t)mb;
             k.ic[i] = (int8_t)mc;
         }
+    if (a.T > 0 && !states)
+        for (int i = 0; i < nprob; ++i)
+            if (!a.pr[i].out_f32 && !tcg::map_kd(&k.out[i], a.pr[i].out, a.B * a.Hv * a.T, 32))
+                return cudaErrorInvalidValue;
     cudaError_t e;
     if (states) {
         e = cudaFuncSetAttribute(tcg::k_linear_state_tc,

@@ -396,13 +396,13 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// [rows, 128] bf16, box 64 x 128 rows, 128-byte swizzle
-inline bool map_kd(CUtensorMap* m, const void* base, int64_t rows) {
+// [rows, 128] bf16, box 64 x 128 rows (or fewer), 128-byte swizzle
+inline bool map_kd(CUtensorMap* m, const void* base, int64_t rows, int box_rows = kRows) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;
     cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)kRows};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     cuuint32_t es[2] = {1, 1};
     return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
