@@ -22,11 +22,12 @@
 //
 // Bound: five products (2600 cycles of the tensor pipe) and 128 KB in and out
 // per chunk (5600 cycles at 1/148 of the copy bandwidth), so the aim is to
-// stream.  One CTA per SM, 18 warps:
+// stream.  One CTA per SM, 19 warps:
 //   warps 0-7   P from Sc; the last chunk's outputs (lane = row, half the columns)
 //   warps 8-15  the parts of w b; the state (lane = row, half the columns)
 //   warp 16     TMA: b, a, c of each chunk into a ring of five 32 KB tiles
-//   warp 17     MMA: Sc, a M^T, P c, Mu
+//   warp 17     MMA: Sc, a M^T, Mu, P c
+//   warp 18     TMA: outputs, staged in the tile of a
 // hi overwrites b's tile (Sc has read it), mid has a tile, the bf16 state the
 // seventh; a third part, lo, takes the state's once a M^T has read it.  TMEM
 // holds Sc, O, Mu and M; P goes back over Sc (A operand).  Outputs leave while
@@ -48,18 +49,18 @@ namespace tcg {
 
 constexpr int kLtTile = kRows * kD * 2;                // one bf16 [2][128][64] operand: 32 KB
 constexpr int kLtRing = 5;
-constexpr int kLtThreads = 18 * 32;
+constexpr int kLtThreads = 19 * 32;
 
 struct LinTcArgs {
     CUtensorMap map[4];                                // the call's distinct inputs
-    CUtensorMap out[kLinProblems];                     // bf16 outputs, boxes of 32 rows
+    CUtensorMap out[kLinProblems];                     // bf16 outputs
     int8_t ia[kLinProblems], ib[kLinProblems], ic[kLinProblems];
     LinArgs a;
 };
 
 struct __align__(16) LtCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t sc, am, p, parts, o, drained, mu, state, stored[2], drain;
+    uint64_t sc, am, p, parts, o, drained, mu, state, staged[2], stored[2], drain;
     __align__(16) float pw[kRows];                     // s lambda^n
     __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
     // by row, for whole chunks [0] and for the segment's last rows [1]: the
@@ -229,14 +230,20 @@ __device__ __forceinline__ int lt_row0(const LinArgs& p, const LinSeg& g, int hv
 }
 // A place in the ring: counted on, as a division per tile costs a single
 // thread more than the tile's products take to issue.
+template <int N>
 struct Ring {
     int slot = 0;
     uint32_t phase = 0;
     __device__ void next() {
-        if (++slot == kLtRing) { slot = 0; phase ^= 1; }
+        if (++slot == N) { slot = 0; phase ^= 1; }
     }
     __device__ uint32_t tile(uint32_t tiles) const { return tiles + slot * kLtTile; }
 };
+// Whatever stopped a walk after t tiles, copies in flight land before the CTA ends.
+template <int N>
+__device__ __forceinline__ void land(uint64_t* full, int t) {
+    for (int i = t > N ? t - N : 0; i < t; ++i) mbar_wait(&full[i % N], (uint32_t)(i / N) & 1);
+}
 
 // 32 columns of this thread's lane -> TMEM, raw
 __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&w)[32]) {
@@ -272,12 +279,6 @@ __device__ __forceinline__ void take_update(uint32_t mu, float a, float a_lo, fl
     }
 }
 
-// Whatever stopped a walk after t tiles, copies in flight land before the CTA ends.
-__device__ __forceinline__ void land(uint64_t* full, int t) {
-    for (int i = t > kLtRing ? t - kLtRing : 0; i < t; ++i)
-        mbar_wait(&full[i % kLtRing], (uint32_t)(i / kLtRing) & 1);
-}
-
 // ---- the roles of k_linear_tc ----
 struct LtWalk {                                        // chunks of a segment, in walking order
     int n, nch;
@@ -294,7 +295,7 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
     const int yb = lt_row0(k.a, g, hv, q.gb), ya = lt_row0(k.a, g, hv, q.ga),
               yc = lt_row0(k.a, g, hv, q.gc);
     const int tiles = 3 * wk.nch;
-    Ring at;
+    Ring<kLtRing> at;
     int t = 0, m = 0, r0 = wk.first(0);
     for (; t < tiles; ++t) {
         const int s = at.slot;
@@ -311,7 +312,7 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
         at.next();
         if (++m == 3) { m = 0; r0 += wk.rev ? -kRows : kRows; }
     }
-    land(c->full, t);
+    land<kLtRing>(c->full, t);
 }
 
 // The whole warp walks and one lane issues: descriptors and addresses are then
@@ -322,15 +323,15 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
     const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
     int* const ab = &c->abort;
     const bool lead = elect_one();
-    Ring at;
+    Ring<kLtRing> at;
 #pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
         const uint32_t par = ci & 1;
-        const Ring b = at;
+        const Ring<kLtRing> b = at;
         at.next();
-        const Ring a = at;
+        const Ring<kLtRing> a = at;
         at.next();
-        const Ring v = at;
+        const Ring<kLtRing> v = at;
         at.next();
         const uint32_t sb = b.tile(tiles), sa = a.tile(tiles), sv = v.tile(tiles);
         if (!warp_wait(&c->full[b.slot], b.phase, ab, status) ||
@@ -381,13 +382,13 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
     __syncwarp();
 }
 
-// Half of one row's outputs from its accumulator: through the tile of a (its
-// products are done) and out by TMA, 32 rows a warp; straight to memory where
-// rows of the chunk are not the segment's, or in float32.  Direct stores of
-// whole rows take the shared-memory pipe for 1000 cycles a chunk.
+// Half of one row's outputs from its accumulator: to the tile of a (its
+// products are done), for the store warp; straight to memory where rows of the
+// chunk are not the segment's, or in float32.  Direct stores of whole rows take
+// the shared-memory pipe for 1000 cycles a chunk.
 __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, int h, int64_t row,
-                                          const LinProblem& q, const CUtensorMap* map,
-                                          uint32_t a_tile, LtCtrl* c, int chunk) {
+                                          const LinProblem& q, uint32_t a_tile, LtCtrl* c,
+                                          int chunk) {
     const int lane = threadIdx.x & 31;
     uint32_t x[2][32];
     tmem_ld32_async(to, x[0]);
@@ -422,24 +423,35 @@ __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, in
             st_global32((__nv_bfloat16*)q.out + at + 32 * pc + 16, w + 8);
         }
     }
-    if (by_tma) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile(
-                "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                    map),
-                "r"(64 * h), "r"((int)(row + r)), "r"(a_tile + op_off(r, 8 * h))
-                : "memory");
+    fence_async_smem();
+    warp_arrive(&c->staged[chunk & 1], lane);
+}
+
+// The store warp's lane: a chunk's staged outputs to memory; then b may come
+// into their tile.
+__device__ void lt_store(const LtWalk& wk, const LinProblem& q, const CUtensorMap* map, int row,
+                         uint8_t* smem, LtCtrl* c, int* status) {
+    Ring<kLtRing> at;
+    for (int ci = 0; ci < wk.nch; ++ci) {
+        at.next();
+        const uint8_t* tile = smem + at.slot * kLtTile;
+        at.next();
+        at.next();
+        const int r0 = wk.first(ci);
+        if (!lt_wait(&c->staged[ci & 1], (ci >> 1) & 1, &c->abort, status)) break;
+        if (wk.rows(r0) == kRows && !q.out_f32) {
+            tma_store_2d(map, 0, row + r0, tile);
+            tma_store_2d(map, 64, row + r0, tile + kRows * 128);
             bulk_commit();
             bulk_wait_read();
         }
+        mbar_arrive(&c->stored[ci & 1]);
     }
-    warp_arrive(&c->stored[chunk & 1], lane);
+    bulk_wait_all();
 }
 
 __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
-                        const LtWalk& wk, uint32_t tiles, const CUtensorMap* map, LtCtrl* c) {
+                        const LtWalk& wk, uint32_t tiles, LtCtrl* c) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const bool rev = wk.rev;
@@ -447,7 +459,7 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
     const int64_t orow = (g.b * p.Hv + hv) * p.T + g.t0;
     const float lam = c->lambda;
     float d = 0.f;
-    Ring at;
+    Ring<kLtRing> at;
 #pragma unroll 1
     for (int ci = 0; ci <= wk.nch; ++ci) {
         if (ci > 0) {                                  // the last chunk's outputs, while Mu is formed
@@ -458,7 +470,7 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
             at.next();
             if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) break;
             tc_fence_after();
-            lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, map, a_tile, c, ci - 1);
+            lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, a_tile, c, ci - 1);
         }
         if (ci < wk.nch) {
             const int n = wk.rows(wk.first(ci));
@@ -529,7 +541,6 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
             warp_arrive(&c->p, lane);
         }
     }
-    if (lane == 0) bulk_wait_all();
 }
 
 __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
@@ -588,16 +599,16 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
         }
         ready();
     }
-    Ring at;
+    Ring<kLtRing> at;
 #pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
         const uint32_t par = ci & 1;
         const int n = wk.rows(wk.first(ci)), part = n < kRows;
         const float w = c->w[part][r];
-        const Ring b = at;
+        const Ring<kLtRing> b = at;
         at.next();
         at.next();
-        const Ring v = at;
+        const Ring<kLtRing> v = at;
         at.next();
         const uint32_t sb = b.tile(tiles);
         if (!warp_wait(&c->full[b.slot], b.phase, &c->abort, p.status) ||
@@ -664,8 +675,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         mbar_init(&c->drained, 8);
         mbar_init(&c->mu, 1);
         mbar_init(&c->state, 8);
-        mbar_init(&c->stored[0], 8);
-        mbar_init(&c->stored[1], 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->staged[i], 8);
+            mbar_init(&c->stored[i], 1);
+        }
         mbar_init(&c->drain, 1);
         c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -699,13 +712,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     tc_fence_after();
     const uint32_t tiles = su32(smem);
     if (warp < 8) {
-        lt_rows(p, q, g, hv, wk, tiles, &k.out[blockIdx.z], c);
+        lt_rows(p, q, g, hv, wk, tiles, c);
     } else if (warp < 16) {
         lt_state(p, q, g, hv, wk, tiles, c);
     } else if (warp == 16) {
         if (lane == 0) lt_load(k, q, g, hv, wk, smem, c);
-    } else {
+    } else if (warp == 17) {
         lt_multiply(wk, tiles, c, p.status);
+    } else if (lane == 0) {
+        lt_store(wk, q, &k.out[blockIdx.z], (int)((g.b * p.Hv + hv) * p.T + g.t0), smem, c,
+                 p.status);
     }
     __syncwarp();
     tc_fence_before();
@@ -717,21 +733,50 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
 }
 
 // ---- step 1: what a segment adds to the state ----
-// Warps 0-7 split b, warps 8-15 carry the state in registers, warp 16 loads,
-// warp 17 multiplies.  Five ring tiles, one each for mid and lo; the parts of a
-// chunk are formed while hi of the one before is multiplied and its sum is
-// taken, from two accumulators in turn.
+// Here the parts are c's: (w c)^T b, with A = (w c)^T in TMEM, so that a product
+// reads shared memory for b alone and all seven tiles are the ring's.  ldmatrix
+// transposes c on the way: a thread gets pairs of tokens of one column of c,
+// which is a 32-bit column of A's row in TMEM (16x128b stores).  With the parts
+// of b in shared memory, as in k_linear_tc, a chunk's parts had to wait for the
+// last chunk's products: 5000 cycles a chunk.
+//   warps 0-7   the parts of c (32 rows of A, half the tokens), two buffers
+//   warps 8-15  the state, in registers
+//   warp 16     TMA: b, c of each chunk;   warp 17  MMA
 constexpr int kLsThreads = 18 * 32;
+constexpr int kLsRing = 7;
+constexpr int kLsPart = 64;                            // TMEM columns of a part
 struct __align__(16) LsCtrl {
-    uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t parts, read, mu[2], taken[2], drain;
-    float w[2][kRows];                                 // as in LtCtrl
+    uint64_t full[kLsRing], empty[kLsRing];
+    uint64_t parts[2], read[2], mu, taken, drain;
+    __align__(16) float w[2][kRows];                   // as in LtCtrl
     float an[2], an_lo[2];
     uint32_t tmem;
     int abort;
 };
-constexpr int kLsSmem = 7 * kLtTile + (int)sizeof(LsCtrl);
+constexpr int kLsSmem = kLsRing * kLtTile + (int)sizeof(LsCtrl);
 static_assert(kLsSmem <= 232448, "shared memory budget");
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 lanes x 8 columns; thread t: lanes t / 4 (a0, b0) and t / 4 + 8 (a1, b1),
+// columns t % 4 (a) and 4 + t % 4 (b)
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, uint32_t a0, uint32_t a1,
+                                                uint32_t b0, uint32_t b1) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(a0), "r"(a1), "r"(b0), "r"(b1)
+                 : "memory");
+}
+// D (+)= A B over 128 tokens, A in TMEM, B MN-major
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, uint32_t b, bool fresh) {
+    const uint64_t db = sdesc(b, kRows * 128, 1024);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+        mma_ts(d, a + kk * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128), !fresh || kk > 0);
+}
 
 // grid: (segments of sequences that have several, Hv, problems)
 __global__ void __launch_bounds__(kLsThreads, 1)
@@ -748,23 +793,23 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* const dst = lin_added(p, q, g, hv);
     if (!dst) return;
-    LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + 7 * kLtTile);
+    LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + kLsRing * kLtTile);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kLtRing; ++i) {
+        for (int i = 0; i < kLsRing; ++i) {
             mbar_init(&c->full[i], 1);
             mbar_init(&c->empty[i], 1);
         }
-        mbar_init(&c->parts, 8);
-        mbar_init(&c->read, 1);
-        mbar_init(&c->mu[0], 1);
-        mbar_init(&c->mu[1], 1);
-        mbar_init(&c->taken[0], 8);
-        mbar_init(&c->taken[1], 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->parts[i], 8);
+            mbar_init(&c->read[i], 1);
+        }
+        mbar_init(&c->mu, 1);
+        mbar_init(&c->taken, 8);
         mbar_init(&c->drain, 1);
         c->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 17) tmem_alloc(&c->tmem, 256);
+    if (warp == 17) tmem_alloc(&c->tmem, 512);
     const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0, true};
     {
         const double lg = lin_log2(p.loggate, hv);
@@ -779,52 +824,51 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = c->tmem, tiles = su32(smem);
-    const uint32_t mid_tile = tiles + 5 * kLtTile, lo_tile = tiles + 6 * kLtTile;
+    // TMEM: Mu, then two sets of hi, mid, lo
+    const uint32_t tm = c->tmem, tiles = su32(smem), tPart = tm + 128;
     int* const ab = &c->abort;
     if (warp == 16) {
         if (lane == 0) {
             const int z = blockIdx.z;
             const CUtensorMap *mb = &k.map[k.ib[z]], *mc = &k.map[k.ic[z]];
             const int yb = lt_row0(p, g, hv, q.gb), yc = lt_row0(p, g, hv, q.gc);
-            Ring at;
+            Ring<kLsRing> at;
             int t = 0, r0 = wk.first(0);
-            for (; t < 2 * wk.nch; ++t) {
-                const int s = at.slot, y = r0 + (t & 1 ? yc : yb);
-                if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, ab, p.status)) break;
+            for (; t < 2 * wk.nch; ++t) {              // c first: its parts are made of it
+                const int s = at.slot, y = r0 + (t & 1 ? yb : yc);
+                if (t >= kLsRing && !lt_wait(&c->empty[s], at.phase ^ 1, ab, p.status)) break;
                 mbar_expect_tx(&c->full[s], kLtTile);
-                tma_load_2d(smem + s * kLtTile, t & 1 ? mc : mb, 0, y, &c->full[s]);
-                tma_load_2d(smem + s * kLtTile + kRows * 128, t & 1 ? mc : mb, 64, y, &c->full[s]);
+                tma_load_2d(smem + s * kLtTile, t & 1 ? mb : mc, 0, y, &c->full[s]);
+                tma_load_2d(smem + s * kLtTile + kRows * 128, t & 1 ? mb : mc, 64, y, &c->full[s]);
                 at.next();
                 if (t & 1) r0 += wk.rev ? -kRows : kRows;
             }
-            land(c->full, t);
+            land<kLsRing>(c->full, t);
         }
     } else if (warp == 17) {
         const bool lead = elect_one();
         const uint32_t td = __shfl_sync(0xffffffffu, tm, 0);
-        Ring at;
+        Ring<kLsRing> at;
 #pragma unroll 1
         for (int ci = 0; ci < wk.nch; ++ci) {
-            const Ring b = at;
+            const Ring<kLsRing> v = at;
             at.next();
-            const Ring v = at;
+            const Ring<kLsRing> b = at;
             at.next();
-            if (!warp_wait(&c->full[v.slot], v.phase, ab, p.status) ||
-                !warp_wait(&c->parts, ci & 1, ab, p.status) ||
-                (ci > 1 &&                             // the sum of ci - 2 has left
-                 !warp_wait(&c->taken[ci & 1], ((ci >> 1) & 1) ^ 1, ab, p.status)))
+            if (!warp_wait(&c->full[b.slot], b.phase, ab, p.status) ||
+                !warp_wait(&c->parts[ci & 1], (ci >> 1) & 1, ab, p.status) ||
+                (ci > 0 && !warp_wait(&c->taken, (ci - 1) & 1, ab, p.status)))
                 break;
             tc_fence_after();
-            const uint32_t sb = b.tile(tiles), sv = v.tile(tiles), d = td + 128 * (ci & 1);
+            const uint32_t sb = b.tile(tiles), pt = td + 128 + (ci & 1) * 3 * kLsPart;
             if (lead) {
-                mma_mm(d, sv, lo_tile, true);
-                mma_mm(d, sv, mid_tile, false);
-                mma_commit(&c->read);
-                mma_mm(d, sv, sb, false);
-                mma_commit(&c->mu[ci & 1]);
-                mma_commit(&c->empty[b.slot]);
+                mma_tm(td, pt + 2 * kLsPart, sb, true);            // lo
+                mma_tm(td, pt + kLsPart, sb, false);
+                mma_tm(td, pt, sb, false);                         // hi
+                mma_commit(&c->mu);
+                mma_commit(&c->read[ci & 1]);
                 mma_commit(&c->empty[v.slot]);
+                mma_commit(&c->empty[b.slot]);
             }
             __syncwarp();
         }
@@ -833,25 +877,66 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
             mbar_wait(&c->drain, 0);
         }
     } else if (warp < 8) {
-        const int h = warp >> 2, r = (warp & 3) * 32 + lane;
-        Ring at;
+        const int quarter = warp & 3, tok0 = 64 * (warp >> 2);
+        Ring<kLsRing> at;
 #pragma unroll 1
         for (int ci = 0; ci < wk.nch; ++ci) {
             const int n = wk.rows(wk.first(ci));
-            const Ring b = at;
+            const Ring<kLsRing> v = at;
             at.next();
-            const Ring v = at;
+            const Ring<kLsRing> b = at;
             at.next();
-            if (!warp_wait(&c->full[b.slot], b.phase, ab, p.status) ||
-                (ci > 0 && !warp_wait(&c->read, (ci - 1) & 1, ab, p.status)))
+            if (!warp_wait(&c->full[v.slot], v.phase, ab, p.status) ||
+                (ci > 1 && !warp_wait(&c->read[ci & 1], ((ci >> 1) & 1) ^ 1, ab, p.status)))
                 break;
-            split_row<3>(b.tile(tiles), mid_tile, lo_tile, r, h, c->w[n < kRows][r], r >= n);
-            if (n < kRows) {
-                if (!warp_wait(&c->full[v.slot], v.phase, ab, p.status)) break;
-                if (r >= n) zero_row(v.tile(tiles), r, h);
+            tc_fence_after();
+            const uint32_t sv = v.tile(tiles);
+            const uint32_t pt = tPart + (ci & 1) * 3 * kLsPart + ((uint32_t)(quarter * 32) << 16);
+#pragma unroll 1
+            for (int t0 = tok0; t0 < tok0 + 64; t0 += 16) {
+                uint32_t part[3][2][4];                // [part][eight tokens][eight columns of c]
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t x[4];
+                    ldmatrix_x4_trans(
+                        sv + op_off(t0 + 8 * j + (lane & 7), 4 * quarter + (lane >> 3)), x);
+                    const int tok = t0 + 8 * j + 2 * (lane & 3);
+                    if (n < kRows) {                   // rows that are not the segment's
+                        const uint32_t keep = tok + 1 < n ? 0xffffffffu : (tok < n ? 0xffffu : 0u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] &= keep;
+                    }
+                    const float2 w = *reinterpret_cast<const float2*>(&c->w[n < kRows][tok]);
+                    const F2 w2(w.x, w.y);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        F2 y = mul2(F2(__uint_as_float(x[i] << 16),
+                                       __uint_as_float(x[i] & 0xffff0000u)), w2);
+                        part[0][j][i] = take_upper(y);
+                        part[1][j][i] = take_upper(y);
+                        float lo, hi;
+                        y.get(lo, hi);
+                        part[2][j][i] = pack_b2(lo, hi);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    const uint32_t at2 = pt + e * kLsPart + t0 / 2;
+                    tmem_st_16x128b(at2, part[e][0][0], part[e][0][1], part[e][1][0],
+                                    part[e][1][1]);
+                    tmem_st_16x128b(at2 + (16u << 16), part[e][0][2], part[e][0][3],
+                                    part[e][1][2], part[e][1][3]);
+                }
             }
-            fence_async_smem();
-            warp_arrive(&c->parts, lane);
+            if (n < kRows) {
+                const int r = (warp & 3) * 32 + lane;
+                if (!warp_wait(&c->full[b.slot], b.phase, ab, p.status)) break;
+                if (r >= n) zero_row(b.tile(tiles), r, warp >> 2);
+                fence_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&c->parts[ci & 1], lane);
         }
     } else {
         const int h = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;
@@ -863,12 +948,12 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
 #pragma unroll 1
         for (int ci = 0; ci < wk.nch && ok; ++ci) {
             const int part = wk.rows(wk.first(ci)) < kRows;
-            ok = warp_wait(&c->mu[ci & 1], (ci >> 1) & 1, ab, p.status);
+            ok = warp_wait(&c->mu, ci & 1, ab, p.status);
             if (!ok) break;
             tc_fence_after();
-            take_update(tMu + 128 * (ci & 1), c->an[part], c->an_lo[part], m);
+            take_update(tMu, c->an[part], c->an_lo[part], m);
             tc_fence_before();
-            warp_arrive(&c->taken[ci & 1], lane);
+            warp_arrive(&c->taken, lane);
         }
         if (ok) store_state(dst, r, h, m);
     }
@@ -877,7 +962,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     __syncthreads();
     if (warp == 17) {
         tc_fence_after();
-        tmem_dealloc(tm, 256);
+        tmem_dealloc(tm, 512);
     }
 }
 
@@ -912,7 +997,7 @@ cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, boo
         }
     if (a.T > 0 && !states)
         for (int i = 0; i < nprob; ++i)
-            if (!a.pr[i].out_f32 && !tcg::map_kd(&k.out[i], a.pr[i].out, a.B * a.Hv * a.T, 32))
+            if (!a.pr[i].out_f32 && !tcg::map_kd(&k.out[i], a.pr[i].out, a.B * a.Hv * a.T))
                 return cudaErrorInvalidValue;
     cudaError_t e;
     if (states) {
