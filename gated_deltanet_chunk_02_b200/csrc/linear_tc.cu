@@ -6,15 +6,15 @@
 // all products 128 x 128 x 128, fp32 accumulators in TMEM):
 //   Sc = a b^T              -> P_ij = s lambda^|i-j| Sc_ij / d_i on the causal side, bf16
 //   O  = a M^T + P c        -> out_i = s_out d_i O_i,  d_i = lambda^(i+1)
-//   Mu = c^T (w b)          -> M <- lambda^n M + Mu,   w_j = lambda^(n-1-j)
+//   Mu = (w c)^T b          -> M <- lambda^n M + Mu,   w_j = lambda^(n-1-j)
 // Both terms of an output share one accumulator: the row's decay d_i is taken
 // out of its weights.  d_i stops at 2^-60, so that the weights stay in range;
 // the state then reaches rows it should reach with less than 2^-60 with 2^-60,
 // far below the rounding of anything it could matter to.
 //
-// The state lives in TMEM in fp32; only its copy as an operand of O is rounded
-// to bf16, and so is P (each term of an output passes one rounding).
-// c is exact in bf16 and w b is split into bf16 parts with a product each,
+// The state lives in fp32 registers; only its copy as an operand of O is
+// rounded to bf16, and so is P (each term of an output passes one rounding).
+// b is exact in bf16 and w c is split into bf16 parts with a product each,
 // smallest first: two parts (2^-16) where the state is only an operand later,
 // three (exact) where it is returned or starts other segments.  Mu is added to
 // the state in fp32 after every chunk: accumulation in TMEM rounds towards
@@ -23,19 +23,21 @@
 // Bound: five products (2600 cycles of the tensor pipe) and 128 KB in and out
 // per chunk (5600 cycles at 1/148 of the copy bandwidth), so the aim is to
 // stream.  One CTA per SM, 19 warps:
-//   warps 0-7   P from Sc; the last chunk's outputs (lane = row, half the columns)
-//   warps 8-15  the parts of w b; the state (lane = row, half the columns)
-//   warp 16     TMA: b, a, c of each chunk into a ring of five 32 KB tiles
-//   warp 17     MMA: Sc, a M^T, Mu, P c
+//   warps 0-7   P from Sc, the parts of w c, the last chunk's outputs
+//   warps 8-15  the state (lane = row, half the columns)
+//   warp 16     TMA: b, a, c of each chunk into a ring of two chunks' tiles
+//   warp 17     MMA: Sc, a M^T, P c, Mu
 //   warp 18     TMA: outputs, staged in the tile of a
-// hi overwrites b's tile (Sc has read it), mid has a tile, the bf16 state the
-// seventh; a third part, lo, takes the state's once a M^T has read it.  TMEM
-// holds Sc, O, Mu and M; P goes back over Sc (A operand).  Outputs leave while
-// Mu is formed.  Two things ruined first versions, both at 8600 to 11000 cycles
-// a chunk: unrolled loops (80 KB of code a chunk run at the rate it can be
-// fetched), and the state in registers (a spilled register's reload is an L2
-// access, as shared memory leaves L1 no room).  Every wait is bounded (2 s): on
-// expiry the status word is set and all roles leave.
+// P (over Sc) and the parts are A operands in TMEM, so shared memory holds the
+// ring and the bf16 state alone and is read for B only.  The parts are made by
+// ldmatrix, which transposes c on the way: a thread gets pairs of tokens of one
+// column of c, a 32-bit column of A's row in TMEM (16x128b stores).  A third
+// part lies in the columns of Sc that P leaves.
+// What ruined first versions, at 8600 to 11000 cycles a chunk: unrolled loops
+// (80 KB of code a chunk run at the rate it can be fetched), spilled registers
+// (a reload is an L2 access, as shared memory leaves L1 no room), and products
+// issued by a walk of one lane.  Every wait is bounded (2 s): on expiry the
+// status word is set and all roles leave.
 //
 // k_linear_state_tc is step 1: the state part alone, always with three parts.
 #include <cstddef>
@@ -48,7 +50,8 @@ namespace gdn {
 namespace tcg {
 
 constexpr int kLtTile = kRows * kD * 2;                // one bf16 [2][128][64] operand: 32 KB
-constexpr int kLtRing = 5;
+constexpr int kLtRing = 6;
+constexpr int kLtPart = 64;                            // TMEM columns of a part
 constexpr int kLtThreads = 19 * 32;
 
 struct LinTcArgs {
@@ -60,7 +63,7 @@ struct LinTcArgs {
 
 struct __align__(16) LtCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t sc, am, p, parts, o, drained, mu, state, staged[2], stored[2], drain;
+    uint64_t sc, p, parts, o, drained, mu, state, staged[2], stored[2], drain;
     __align__(16) float pw[kRows];                     // s lambda^n
     __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
     // by row, for whole chunks [0] and for the segment's last rows [1]: the
@@ -70,7 +73,7 @@ struct __align__(16) LtCtrl {
     uint32_t tmem;
     int abort;
 };
-constexpr int kLtSmem = 7 * kLtTile + (int)sizeof(LtCtrl);
+constexpr int kLtSmem = (kLtRing + 1) * kLtTile + (int)sizeof(LtCtrl);
 static_assert(kLtSmem <= 232448, "shared memory budget");
 static_assert(offsetof(LtCtrl, step) % 16 == 0, "step is read 16 bytes at a time");
 
@@ -132,41 +135,66 @@ __device__ __forceinline__ uint32_t take_upper(F2& x) {
     x = sub2(x, F2(__uint_as_float(ua & 0xffff0000u), __uint_as_float(ub & 0xffff0000u)));
     return __byte_perm(ua, ub, 0x7632);
 }
-// eight bf16 of one 16-byte group times w, as hi + mid (+ lo): truncation
-// leaves 16, then 8 bits, so that three parts are exact
-template <int PARTS>
-__device__ __forceinline__ void split8(const uint4& u, float w, uint4 (&part)[PARTS]) {
-    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-    uint32_t y[PARTS][4];
-    const F2 w2(w, w);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        F2 v = mul2(F2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), w2);
-#pragma unroll
-        for (int k = 0; k < PARTS - 1; ++k) y[k][i] = take_upper(v);
-        float a, b;
-        v.get(a, b);
-        y[PARTS - 1][i] = pack_b2(a, b);
-    }
-#pragma unroll
-    for (int k = 0; k < PARTS; ++k) part[k] = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
-// row r (columns 64 h ..) of b times w: hi in its place, mid (and lo) in their
-// tiles.  Rows that are not this segment's (off) may hold anything: zero.
+// 16 lanes x 8 columns; thread t: lanes t / 4 (a0, b0) and t / 4 + 8 (a1, b1),
+// columns t % 4 (a) and 4 + t % 4 (b)
+__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, uint32_t a0, uint32_t a1,
+                                                uint32_t b0, uint32_t b1) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+                 "r"(a0), "r"(a1), "r"(b0), "r"(b1)
+                 : "memory");
+}
+// One warp's share of the parts of w c: 32 columns of c (lanes of A) and the 64
+// tokens from tok0 (32 columns of each part).  Truncation leaves 16, then 8
+// bits, so that three parts are exact.  Tokens from n on are not the segment's
+// and may hold anything: zero.
 template <int PARTS>
-__device__ __forceinline__ void split_row(uint32_t b, uint32_t mid_tile, uint32_t lo_tile, int r,
-                                          int h, float w, bool off) {
-#pragma unroll 2
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t at = op_off(r, 8 * h + e);
-        uint4 u = lds128(b + at), part[PARTS];
-        if (off) u = make_uint4(0, 0, 0, 0);
-        split8<PARTS>(u, w, part);
-        sts128(b + at, part[0]);
-        sts128(mid_tile + at, part[1]);
-        if (PARTS == 3) sts128(lo_tile + at, part[PARTS - 1]);
+__device__ __forceinline__ void split_c(uint32_t tile, int quarter, int tok0, int n,
+                                        const float* w, uint32_t at_hi, uint32_t at_mid,
+                                        uint32_t at_lo) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int t = 0; t < 64; t += 16) {
+        uint32_t part[PARTS][2][4];                    // [part][eight tokens][eight columns of c]
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t x[4];
+            ldmatrix_x4_trans(
+                tile + op_off(tok0 + t + 8 * j + (lane & 7), 4 * quarter + (lane >> 3)), x);
+            const int tok = tok0 + t + 8 * j + 2 * (lane & 3);
+            if (n < kRows) {
+                const uint32_t keep = tok + 1 < n ? 0xffffffffu : (tok < n ? 0xffffu : 0u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] &= keep;
+            }
+            const float2 wt = *reinterpret_cast<const float2*>(w + tok);
+            const F2 w2(wt.x, wt.y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                F2 y = mul2(F2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)),
+                            w2);
+#pragma unroll
+                for (int e = 0; e < PARTS - 1; ++e) part[e][j][i] = take_upper(y);
+                float a, b;
+                y.get(a, b);
+                part[PARTS - 1][j][i] = pack_b2(a, b);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < PARTS; ++e) {
+            const uint32_t at = (e == 0 ? at_hi : (e == 1 ? at_mid : at_lo)) + t / 2;
+            tmem_st_16x128b(at, part[e][0][0], part[e][0][1], part[e][1][0], part[e][1][1]);
+            tmem_st_16x128b(at + (16u << 16), part[e][0][2], part[e][0][3], part[e][1][2],
+                            part[e][1][3]);
+        }
     }
 }
+// rows that are not the segment's, as an operand: zero (row r, columns 64 h ..)
 __device__ __forceinline__ void zero_row(uint32_t tile, int r, int h) {
 #pragma unroll 1
     for (int q = 0; q < 8; ++q) sts128(tile + op_off(r, 8 * h + q), make_uint4(0, 0, 0, 0));
@@ -200,7 +228,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* b, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(b);
 }
-// D (+)= A B over 128: both K-major, A in TMEM with B MN-major, both MN-major.
+// D (+)= A B over 128: both K-major in shared memory, or A in TMEM with B MN-major.
 // A step of 16 is 32 bytes on in a K-major operand (64 columns to a half) and
 // 2048 in an MN-major one.
 __device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b) {
@@ -211,17 +239,14 @@ __device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b) {
         mma_ss(d, da + o, db + o, idesc_f16(1, 0, 0, 128, 128), kk > 0);
     }
 }
-__device__ __forceinline__ void mma_pc(uint32_t d, uint32_t a, uint32_t b) {
+// D (+)= A B over 128 tokens, A in TMEM at a, its second half `half` columns on
+__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, uint32_t half, uint32_t b,
+                                       bool fresh) {
     const uint64_t db = sdesc(b, kRows * 128, 1024);
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-        mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128), 1);
-}
-__device__ __forceinline__ void mma_mm(uint32_t d, uint32_t a, uint32_t b, bool fresh) {
-    const uint64_t da = sdesc(a, kRows * 128, 1024), db = sdesc(b, kRows * 128, 1024);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_ss(d, da + kk * 128, db + kk * 128, idesc_f16(1, 1, 1, 128, 128), !fresh || kk > 0);
+        mma_ts(d, a + (kk >> 2) * half + (kk & 3) * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128),
+               !fresh || kk > 0);
 }
 
 __device__ __forceinline__ int lt_row0(const LinArgs& p, const LinSeg& g, int hv, int group) {
@@ -245,13 +270,7 @@ __device__ __forceinline__ void land(uint64_t* full, int t) {
     for (int i = t > N ? t - N : 0; i < t; ++i) mbar_wait(&full[i % N], (uint32_t)(i / N) & 1);
 }
 
-// 32 columns of this thread's lane -> TMEM, raw
-__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&w)[32]) {
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
-    tmem_st32(taddr, v);
-}
+// row r (columns 64 h ..) of a state
 __device__ __forceinline__ void store_state(float* dst, int r, int h, const float (&m)[64]) {
 #pragma unroll
     for (int i = 0; i < 64; i += 8) {
@@ -300,8 +319,8 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
     for (; t < tiles; ++t) {
         const int s = at.slot;
         if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, &c->abort, k.a.status)) break;
-        // b comes where the a of two chunks ago was, and after that chunk's outputs
-        if (m == 0 && t >= 6 &&
+        // a comes where the a of two chunks ago was, and after that chunk's outputs
+        if (m == 1 && t >= kLtRing &&
             !lt_wait(&c->stored[t / 3 & 1], ((t / 3 - 2) >> 1) & 1, &c->abort, k.a.status))
             break;
         const CUtensorMap* mp = m == 0 ? mb : (m == 1 ? ma : mc);
@@ -320,7 +339,7 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
 // register first, and the eight steps of a product took 1500 cycles to issue.
 __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* status) {
     const uint32_t tSc = __shfl_sync(0xffffffffu, c->tmem, 0), tO = tSc + 128, tMu = tSc + 256;
-    const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
+    const uint32_t tPart = tSc + 384, m_tile = tiles + kLtRing * kLtTile;
     int* const ab = &c->abort;
     const bool lead = elect_one();
     Ring<kLtRing> at;
@@ -336,7 +355,8 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
         const uint32_t sb = b.tile(tiles), sa = a.tile(tiles), sv = v.tile(tiles);
         if (!warp_wait(&c->full[b.slot], b.phase, ab, status) ||
             !warp_wait(&c->full[a.slot], a.phase, ab, status) ||
-            (ci > 0 && !warp_wait(&c->o, par ^ 1, ab, status)))    // P c of the last chunk is done
+            // P of the last chunk has been read, and the third part beside it
+            (ci > 0 && !warp_wait(wk.exact ? &c->mu : &c->o, par ^ 1, ab, status)))
             break;
         tc_fence_after();
         if (lead) {
@@ -350,27 +370,28 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
         tc_fence_after();
         if (lead) {
             mma_kk(tO, sa, m_tile);
-            mma_commit(&c->am);
             mma_commit(&c->empty[a.slot]);
         }
         __syncwarp();
+        // c's rows that are not the segment's are zero with the parts
         if (!warp_wait(&c->full[v.slot], v.phase, ab, status) ||
-            !warp_wait(&c->parts, par, ab, status))
+            !warp_wait(&c->p, par, ab, status) ||
+            (wk.rows(wk.first(ci)) < kRows && !warp_wait(&c->parts, par, ab, status)))
             break;
         tc_fence_after();
         if (lead) {
-            if (wk.exact) mma_mm(tMu, sv, m_tile, true);           // lo
-            mma_mm(tMu, sv, mid_tile, !wk.exact);
-            mma_mm(tMu, sv, sb, false);                            // hi
-            mma_commit(&c->mu);                        // first: the state is the longer chain
-            mma_commit(&c->empty[b.slot]);
+            mma_tm(tO, tSc, 64, sv, false);
+            mma_commit(&c->o);
         }
         __syncwarp();
-        if (!warp_wait(&c->p, par, ab, status)) break;
+        if (!warp_wait(&c->parts, par, ab, status)) break;
         tc_fence_after();
         if (lead) {
-            mma_pc(tO, tSc, sv);
-            mma_commit(&c->o);
+            if (wk.exact) mma_tm(tMu, tSc + 32, 64, sb, true);     // lo
+            mma_tm(tMu, tPart + kLtPart, 32, sb, !wk.exact);       // mid
+            mma_tm(tMu, tPart, 32, sb, false);                     // hi
+            mma_commit(&c->mu);
+            mma_commit(&c->empty[b.slot]);
             mma_commit(&c->empty[v.slot]);
         }
         __syncwarp();
@@ -459,15 +480,13 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
     const int64_t orow = (g.b * p.Hv + hv) * p.T + g.t0;
     const float lam = c->lambda;
     float d = 0.f;
+    const uint32_t tPart = c->tmem + ((uint32_t)(quarter * 32) << 16) + 384 + 32 * h;
     Ring<kLtRing> at;
+    uint32_t a_tile = 0;
 #pragma unroll 1
     for (int ci = 0; ci <= wk.nch; ++ci) {
         if (ci > 0) {                                  // the last chunk's outputs, while Mu is formed
             const int r0 = wk.first(ci - 1);
-            at.next();
-            const uint32_t a_tile = at.tile(tiles);
-            at.next();
-            at.next();
             if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) break;
             tc_fence_after();
             lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, a_tile, c, ci - 1);
@@ -539,6 +558,33 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&c->p, lane);
+            // the parts of w c, once the last chunk's have been read
+            const Ring<kLtRing> b = at;
+            at.next();
+            a_tile = at.tile(tiles);
+            at.next();
+            const Ring<kLtRing> v = at;
+            at.next();
+            if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status) ||
+                (ci > 0 && !warp_wait(&c->mu, (ci - 1) & 1, &c->abort, p.status)))
+                break;
+            tc_fence_after();
+            const float* w = c->w[n < kRows];
+            if (wk.exact)
+                split_c<3>(v.tile(tiles), quarter, 64 * h, n, w, tPart, tPart + kLtPart, tSc + 32);
+            else
+                split_c<2>(v.tile(tiles), quarter, 64 * h, n, w, tPart, tPart + kLtPart, 0);
+            if (n < kRows) {                           // rows of others may hold NaN
+                if (!warp_wait(&c->full[b.slot], b.phase, &c->abort, p.status)) break;
+                if (r >= n) {
+                    zero_row(b.tile(tiles), r, h);
+                    zero_row(v.tile(tiles), r, h);
+                }
+                fence_async_smem();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&c->parts, lane);
         }
     }
 }
@@ -548,37 +594,8 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, h = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t tMu = c->tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + 64 * h;
-    const uint32_t tM = tMu + 128;
-    const uint32_t mid_tile = tiles + 5 * kLtTile, m_tile = tiles + 6 * kLtTile;
-    float* const out = wk.exact && q.mout
-                           ? q.mout + (g.seq * p.Hv + hv) * kLinState + r * kD + 64 * h
-                           : nullptr;
-    // 32 columns of the state to where they are needed next: TMEM and, in bf16,
-    // the operand tile, or behind the last chunk the outgoing state
-    auto put = [&](int pc, const uint32_t(&m)[32], bool last) {
-        if (last) {
-            if (!out) return;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st_global32(out + 32 * pc + 8 * e, &m[8 * e]);
-            return;
-        }
-        tmem_st32u(tM + 32 * pc, m);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = pack_b2(__uint_as_float(m[8 * e + 2 * i]),
-                               __uint_as_float(m[8 * e + 2 * i + 1]));
-            sts128(m_tile + op_off(r, 8 * h + 4 * pc + e), make_uint4(w[0], w[1], w[2], w[3]));
-        }
-    };
-    auto ready = [&]() {
-        tmem_wait_st();
-        fence_async_smem();
-        tc_fence_before();
-        warp_arrive(&c->state, lane);
-    };
+    const uint32_t m_row = tiles + kLtRing * kLtTile + op_off(r, 8 * h);
+    float m[64];
     {   // the incoming state
         const bool first = wk.rev ? g.k == g.m - 1 : g.k == 0;
         const float* src = nullptr;
@@ -589,64 +606,28 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
             src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
             if (q.m0_t) { rs = 1; cs = kD; }
         }
-#pragma unroll 1
-        for (int pc = 0; pc < 2; ++pc) {
-            uint32_t m[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                m[i] = src ? __float_as_uint(src[r * rs + (64 * h + 32 * pc + i) * cs]) : 0u;
-            put(pc, m, wk.nch == 0);
-        }
-        ready();
+        for (int i = 0; i < 64; ++i) m[i] = src ? src[r * rs + (64 * h + i) * cs] : 0.f;
     }
-    Ring<kLtRing> at;
 #pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
-        const uint32_t par = ci & 1;
-        const int n = wk.rows(wk.first(ci)), part = n < kRows;
-        const float w = c->w[part][r];
-        const Ring<kLtRing> b = at;
-        at.next();
-        at.next();
-        const Ring<kLtRing> v = at;
-        at.next();
-        const uint32_t sb = b.tile(tiles);
-        if (!warp_wait(&c->full[b.slot], b.phase, &c->abort, p.status) ||
-            !warp_wait(wk.exact ? &c->am : &c->sc, par, &c->abort, p.status))
-            return;                                    // Sc has read b (a M^T the state)
-        if (wk.exact) split_row<3>(sb, mid_tile, m_tile, r, h, w, r >= n);
-        else split_row<2>(sb, mid_tile, m_tile, r, h, w, r >= n);
-        if (n < kRows) {
-            if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status)) return;
-            if (r >= n) zero_row(v.tile(tiles), r, h);
-        }
-        fence_async_smem();
-        warp_arrive(&c->parts, lane);
-        if (!warp_wait(&c->mu, par, &c->abort, p.status)) return;
-        tc_fence_after();
-        // M <- (an + an_lo) M + Mu: an's own rounding would add up over the
-        // chunks that a slow decay remembers
-        const float an = c->an[part], an_lo = c->an_lo[part];
-        const F2 a2(an, an), l2(an_lo, an_lo);
-#pragma unroll 1
-        for (int pc = 0; pc < 2; ++pc) {
-            uint32_t m[32], u[32];
-            tmem_ld32_async(tM + 32 * pc, m);
-            tmem_ld32_async(tMu + 32 * pc, u);
-            tmem_wait_ld();
+        // the state as an operand of chunk ci; the last one has been read
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const F2 x(__uint_as_float(m[i]), __uint_as_float(m[i + 1]));
-                float y, z;
-                fma2(a2, x, fma2(l2, x, F2(__uint_as_float(u[i]), __uint_as_float(u[i + 1]))))
-                    .get(y, z);
-                m[i] = __float_as_uint(y);
-                m[i + 1] = __float_as_uint(z);
-            }
-            put(pc, m, ci == wk.nch - 1);
-        }
-        if (ci < wk.nch - 1) ready();
+        for (int e = 0; e < 8; ++e)
+            sts128(m_row ^ (e << 4),
+                   make_uint4(pack_b2(m[8 * e], m[8 * e + 1]), pack_b2(m[8 * e + 2], m[8 * e + 3]),
+                              pack_b2(m[8 * e + 4], m[8 * e + 5]),
+                              pack_b2(m[8 * e + 6], m[8 * e + 7])));
+        fence_async_smem();
+        tc_fence_before();
+        warp_arrive(&c->state, lane);
+        if (!warp_wait(&c->mu, ci & 1, &c->abort, p.status)) return;
+        tc_fence_after();
+        const int part = wk.rows(wk.first(ci)) < kRows;
+        take_update(tMu, c->an[part], c->an_lo[part], m);
     }
+    if (wk.exact && q.mout)
+        store_state(q.mout + (g.seq * p.Hv + hv) * kLinState, r, h, m);
 }
 
 // grid: (segments, Hv, problems)
@@ -661,14 +642,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     const LinSeg g = lin_find(p, blockIdx.x, kAllSegments);
     if (!g.ok) return;
     const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + 7 * kLtTile);
+    LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + (kLtRing + 1) * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLtRing; ++i) {
             mbar_init(&c->full[i], 1);
             mbar_init(&c->empty[i], 1);
         }
         mbar_init(&c->sc, 1);
-        mbar_init(&c->am, 1);
         mbar_init(&c->p, 8);
         mbar_init(&c->parts, 8);
         mbar_init(&c->o, 1);
@@ -733,18 +713,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
 }
 
 // ---- step 1: what a segment adds to the state ----
-// Here the parts are c's: (w c)^T b, with A = (w c)^T in TMEM, so that a product
-// reads shared memory for b alone and all seven tiles are the ring's.  ldmatrix
-// transposes c on the way: a thread gets pairs of tokens of one column of c,
-// which is a 32-bit column of A's row in TMEM (16x128b stores).  With the parts
-// of b in shared memory, as in k_linear_tc, a chunk's parts had to wait for the
-// last chunk's products: 5000 cycles a chunk.
+// As in k_linear_tc without rows, so that all seven tiles are the ring's and the
+// parts have two buffers.  With the parts (of b) in shared memory a chunk's had
+// to wait for the last chunk's products: 5000 cycles a chunk.
 //   warps 0-7   the parts of c (32 rows of A, half the tokens), two buffers
 //   warps 8-15  the state, in registers
 //   warp 16     TMA: b, c of each chunk;   warp 17  MMA
 constexpr int kLsThreads = 18 * 32;
 constexpr int kLsRing = 7;
-constexpr int kLsPart = 64;                            // TMEM columns of a part
 struct __align__(16) LsCtrl {
     uint64_t full[kLsRing], empty[kLsRing];
     uint64_t parts[2], read[2], mu, taken, drain;
@@ -755,28 +731,6 @@ struct __align__(16) LsCtrl {
 };
 constexpr int kLsSmem = kLsRing * kLtTile + (int)sizeof(LsCtrl);
 static_assert(kLsSmem <= 232448, "shared memory budget");
-
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-// 16 lanes x 8 columns; thread t: lanes t / 4 (a0, b0) and t / 4 + 8 (a1, b1),
-// columns t % 4 (a) and 4 + t % 4 (b)
-__device__ __forceinline__ void tmem_st_16x128b(uint32_t taddr, uint32_t a0, uint32_t a1,
-                                                uint32_t b0, uint32_t b1) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-                 "r"(a0), "r"(a1), "r"(b0), "r"(b1)
-                 : "memory");
-}
-// D (+)= A B over 128 tokens, A in TMEM, B MN-major
-__device__ __forceinline__ void mma_tm(uint32_t d, uint32_t a, uint32_t b, bool fresh) {
-    const uint64_t db = sdesc(b, kRows * 128, 1024);
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-        mma_ts(d, a + kk * 8, db + kk * 128, idesc_f16(1, 0, 1, 128, 128), !fresh || kk > 0);
-}
 
 // grid: (segments of sequences that have several, Hv, problems)
 __global__ void __launch_bounds__(kLsThreads, 1)
@@ -860,11 +814,11 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
                 (ci > 0 && !warp_wait(&c->taken, (ci - 1) & 1, ab, p.status)))
                 break;
             tc_fence_after();
-            const uint32_t sb = b.tile(tiles), pt = td + 128 + (ci & 1) * 3 * kLsPart;
+            const uint32_t sb = b.tile(tiles), pt = td + 128 + (ci & 1) * 3 * kLtPart;
             if (lead) {
-                mma_tm(td, pt + 2 * kLsPart, sb, true);            // lo
-                mma_tm(td, pt + kLsPart, sb, false);
-                mma_tm(td, pt, sb, false);                         // hi
+                mma_tm(td, pt + 2 * kLtPart, 32, sb, true);        // lo
+                mma_tm(td, pt + kLtPart, 32, sb, false);
+                mma_tm(td, pt, 32, sb, false);                     // hi
                 mma_commit(&c->mu);
                 mma_commit(&c->read[ci & 1]);
                 mma_commit(&c->empty[v.slot]);
@@ -890,44 +844,10 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
                 (ci > 1 && !warp_wait(&c->read[ci & 1], ((ci >> 1) & 1) ^ 1, ab, p.status)))
                 break;
             tc_fence_after();
-            const uint32_t sv = v.tile(tiles);
-            const uint32_t pt = tPart + (ci & 1) * 3 * kLsPart + ((uint32_t)(quarter * 32) << 16);
-#pragma unroll 1
-            for (int t0 = tok0; t0 < tok0 + 64; t0 += 16) {
-                uint32_t part[3][2][4];                // [part][eight tokens][eight columns of c]
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t x[4];
-                    ldmatrix_x4_trans(
-                        sv + op_off(t0 + 8 * j + (lane & 7), 4 * quarter + (lane >> 3)), x);
-                    const int tok = t0 + 8 * j + 2 * (lane & 3);
-                    if (n < kRows) {                   // rows that are not the segment's
-                        const uint32_t keep = tok + 1 < n ? 0xffffffffu : (tok < n ? 0xffffu : 0u);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] &= keep;
-                    }
-                    const float2 w = *reinterpret_cast<const float2*>(&c->w[n < kRows][tok]);
-                    const F2 w2(w.x, w.y);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        F2 y = mul2(F2(__uint_as_float(x[i] << 16),
-                                       __uint_as_float(x[i] & 0xffff0000u)), w2);
-                        part[0][j][i] = take_upper(y);
-                        part[1][j][i] = take_upper(y);
-                        float lo, hi;
-                        y.get(lo, hi);
-                        part[2][j][i] = pack_b2(lo, hi);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    const uint32_t at2 = pt + e * kLsPart + t0 / 2;
-                    tmem_st_16x128b(at2, part[e][0][0], part[e][0][1], part[e][1][0],
-                                    part[e][1][1]);
-                    tmem_st_16x128b(at2 + (16u << 16), part[e][0][2], part[e][0][3],
-                                    part[e][1][2], part[e][1][3]);
-                }
-            }
+            const uint32_t pt = tPart + (ci & 1) * 3 * kLtPart + ((uint32_t)(quarter * 32) << 16) +
+                                tok0 / 2;
+            split_c<3>(v.tile(tiles), quarter, tok0, n, c->w[n < kRows], pt, pt + kLtPart,
+                       pt + 2 * kLtPart);
             if (n < kRows) {
                 const int r = (warp & 3) * 32 + lane;
                 if (!warp_wait(&c->full[b.slot], b.phase, ab, p.status)) break;
