@@ -579,7 +579,7 @@ int gdn_linear_forward(const void* Q, const void* K, const void* V, const float*
     if (pl.state_bytes > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
     const int group = (int)(s.Hv / s.Hk);
     gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
-    a.pr[0] = {Q, K, V, O, group, group, 1, 0, 0, S0, 0, S_final, scale, 1.f, 1.f, nullptr};
+    a.pr[0] = {Q, K, V, O, group, group, 1, 0, 0, S0, 0, S_final, 1, scale, 1.f, 1.f, 0, nullptr};
     int kernels = 0;
     return launched(gdn::launch_linear(a, 1, pl, dtype == GDN_BF16, workspace, &kernels,
                                        (cudaStream_t)stream),
@@ -591,7 +591,7 @@ int64_t gdn_linear_backward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype)
     if (check_linear(s, s.nseq > 0 ? &some : nullptr, dtype) != GDN_OK) return -1;
     if (s.B == 0 || s.Hv == 0) return 0;
     const int64_t part = s.Hv == s.Hk ? 0 : s.B * s.Hv * s.T * (int64_t)s.d * 4;
-    return 3 * gdn::linear_plan(s, 3, dtype == GDN_BF16).state_bytes + 2 * part;
+    return 2 * gdn::linear_plan(s, 3, dtype == GDN_BF16).state_bytes + 2 * part;
 }
 
 int gdn_linear_backward(const void* Q, const void* K, const void* V, const float* loggate,
@@ -617,15 +617,17 @@ int gdn_linear_backward(const void* Q, const void* K, const void* V, const float
     const gdn::LinPlan pl = gdn::linear_plan(s, 3, bf16);
     const int group = (int)(s.Hv / s.Hk);
     const int64_t part = group == 1 ? 0 : s.B * s.Hv * s.T * (int64_t)s.d;
-    float* pq = (float*)((uint8_t*)workspace + 3 * pl.state_bytes);
+    float* pq = (float*)((uint8_t*)workspace + 2 * pl.state_bytes);
     float* pk = pq + part;
     const int f32 = group > 1;
     gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
-    a.pr[0] = {dO, V, K, f32 ? (void*)pq : dQ, 1, 1, group, 0, f32, S0, 1, nullptr,
-               scale, 1.f, 1.f, nullptr};
-    a.pr[1] = {V, dO, Q, f32 ? (void*)pk : dK, 1, 1, group, 1, f32, dS_final, 1, nullptr,
-               1.f, scale, scale, nullptr};
-    a.pr[2] = {K, Q, dO, dV, group, group, 1, 1, 0, dS_final, 0, dS0, 1.f, scale, scale, nullptr};
+    a.pr[0] = {dO, V, K, f32 ? (void*)pq : dQ, 1, 1, group, 0, f32, S0, 1, nullptr, 0,
+               scale, 1.f, 1.f, 0, nullptr};
+    // dk's states are dv's, transposed
+    a.pr[1] = {V, dO, Q, f32 ? (void*)pk : dK, 1, 1, group, 1, f32, dS_final, 1, nullptr, 0,
+               1.f, scale, scale, 1, nullptr};
+    a.pr[2] = {K, Q, dO, dV, group, group, 1, 1, 0, dS_final, 0, dS0, 1, 1.f, scale, scale, 0,
+               nullptr};
     cudaStream_t st = (cudaStream_t)stream;
     int kernels = 0;
     GDN_TRY(launched(gdn::launch_linear(a, 3, pl, bf16, workspace, &kernels, st),

@@ -21,8 +21,10 @@ namespace {
 // ---- step 2: boundary states ----
 // Slot k of a sequence holds what segment k (k + 1 if reverse) adds from zero;
 // it is replaced by the state that crosses that boundary.
-__global__ void __launch_bounds__(256) k_lin_combine(const LinArgs p) {
+constexpr int kCombineThreads = 512;
+__global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p) {
     const LinProblem& q = p.pr[blockIdx.z];
+    if (q.ws_t) return;
     const int64_t seq = blockIdx.x / p.Hv;
     const int hv = (int)(blockIdx.x - seq * p.Hv);
     LinSeg g;
@@ -30,6 +32,8 @@ __global__ void __launch_bounds__(256) k_lin_combine(const LinArgs p) {
         // the sequence's first slot: boundaries of the sequences before it
         const int lane = threadIdx.x & 31;
         int64_t slots = 0, t0, n;
+        lin_bounds(p, seq, t0, n);
+        if (n <= p.seg_len) return;
         for (int64_t s = lane; s < seq; s += 32) {
             lin_bounds(p, s, t0, n);
             slots += lin_segments(n, p.seg_len) - 1;
@@ -49,7 +53,7 @@ __global__ void __launch_bounds__(256) k_lin_combine(const LinArgs p) {
     const double lg = lin_log2(p.loggate, hv);
     const float a_full = lin_pow(lg, p.seg_len);
     const float a_last = lin_pow(lg, g.seq_n - (g.m - 1) * p.seg_len);
-    const int e = 4 * (blockIdx.y * 256 + threadIdx.x);
+    const int e = 4 * (blockIdx.y * kCombineThreads + threadIdx.x);
     float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
     if (q.m0) {
         const float* s = q.m0 + (seq * p.Hv + hv) * kLinState;
@@ -150,7 +154,8 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
             const bool first = REV ? g.k == g.m - 1 : g.k == 0;
             if (!first) {
                 const int64_t slot = g.slot0 + (REV ? g.k : g.k - 1);
-                m = q.ws[(slot * p.Hv + hv) * kLinState + (v0 + r) * kLinD + c];
+                const float* src = q.ws + (slot * p.Hv + hv) * kLinState;
+                m = q.ws_t ? src[c * kLinD + v0 + r] : src[(v0 + r) * kLinD + c];
             } else if (q.m0) {
                 const float* src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
                 m = q.m0_t ? src[c * kLinD + v0 + r] : src[(v0 + r) * kLinD + c];
@@ -340,6 +345,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtSmem& s = *reinterpret_cast<SimtSmem*>(raw);
     const LinProblem& q = p.pr[blockIdx.z];
+    if (STATE_ONLY && q.ws_t) return;
     const LinSeg g = lin_find(p, blockIdx.x, STATE_ONLY ? kCutSegments : kAllSegments);
     if (!g.ok) return;
     const int hv = blockIdx.y >> 2, v0 = (blockIdx.y & 3) * kSimtDV;
@@ -367,11 +373,12 @@ cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t cut_segs
     return cudaGetLastError();
 }
 
-// Segment length (a multiple of 128): one segment per sequence when that fills
-// the GPU, else as many as bring the two passes' time down.  In units of half
-// an output step (a chunk of 128 rows on one SM): the state pass takes one per
-// chunk; a CTA's start two in step 3 and one in step 1; a boundary's state
-// moves 256 KB, as much as two output steps; two more launches cost eight.
+// Segment length (a multiple of 128).  Costs are in units of half an output
+// step (a chunk of 128 rows on one SM): a chunk of the state pass takes one, a
+// CTA's start two in step 3 and one in step 1, the state at a boundary moves as
+// much as two output steps, and two more launches cost eight.
+// Sequences of one length are taken in waves: one segment each when that fills
+// the GPU, else the cut with the least cost.
 int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int ctas_per_head) {
     const int64_t chunks = (rows + 127) / 128, sms = sm_count();
     const int64_t lines = nprob * nseq * Hv;
@@ -380,9 +387,27 @@ int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int 
         const int64_t len = (chunks + m - 1) / m;
         if ((chunks + len - 1) / len != m) continue;   // the same cut with fewer pieces is listed
         const int64_t waves = (lines * ctas_per_head * m + sms - 1) / sms;
-        const int64_t waves1 = (lines * ctas_per_head * (m - 1) + sms - 1) / sms;
+        const int64_t waves1 = (lines * ctas_per_head * m + sms - 1) / sms;
         const int64_t c = waves * (2 * len + 2) +
                           (m > 1 ? waves1 * (len + 1) + 4 * lines * (m - 1) / sms + 8 : 0);
+        if (c < cost) { cost = c; best = len; }
+    }
+    return best < 1 ? 128 : 128 * best;
+}
+// Packed sequences have lengths that the host does not know: all their chunks
+// spread over the SMs, the last segment to run alone behind them (cutting 73
+// chunks of 32 heads at 6 instead of 16 took the output pass from 122 to 80 us).
+int64_t pick_segment_packed(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows,
+                            int ctas_per_head) {
+    const int64_t chunks = (rows + 127) / 128, sms = sm_count();
+    const int64_t heads = nprob * Hv * ctas_per_head;
+    int64_t best = chunks, cost = INT64_MAX;
+    for (int64_t len = 1; len <= chunks; len += len < 16 ? 1 : len / 8) {
+        const int64_t m = len < chunks ? (chunks + len - 1) / len : 0;     // segments of cut ones
+        const int64_t c = 2 * heads * (chunks + nseq) / sms + 2 * len +
+                          2 * heads * (m + nseq) / sms +
+                          (m ? heads * (chunks + m) / sms + len +
+                                   4 * nprob * Hv * m / sms + 8 : 0);
         if (c < cost) { cost = c; best = len; }
     }
     return best < 1 ? 128 : 128 * best;
@@ -393,7 +418,9 @@ int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int 
 LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16) {
     LinPlan pl;
     const bool packed = s.nseq > 0;
-    pl.seg_len = pick_segment(nprob, packed ? 1 : s.B, s.Hv, s.T, bf16 ? 1 : 4);
+    // on CUDA cores four CTAs share a head, two to an SM
+    pl.seg_len = packed ? pick_segment_packed(nprob, s.nseq, s.Hv, s.T, bf16 ? 1 : 2)
+                        : pick_segment(nprob, s.B, s.Hv, s.T, bf16 ? 1 : 2);
     // boundaries: a sequence of n rows has at most n / seg_len
     const int64_t m = s.T <= pl.seg_len ? 1 : (s.T + pl.seg_len - 1) / pl.seg_len;
     pl.bounds = packed ? (s.T <= pl.seg_len ? 0 : s.T / pl.seg_len) : s.B * (m - 1);
@@ -410,13 +437,22 @@ cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool 
     a.seg_len = pl.seg_len;
     a.bounds = pl.bounds;
     a.status = status_ptr();
-    for (int i = 0; i < nprob; ++i) a.pr[i].ws = (float*)((uint8_t*)ws + i * pl.state_bytes);
+    uint8_t* at = (uint8_t*)ws;
+    for (int i = nprob - 1; i >= 0; --i) {             // a sharing problem uses the one behind it
+        if (a.pr[i].ws_t) {
+            a.pr[i].ws = a.pr[i + 1].ws;
+            continue;
+        }
+        a.pr[i].ws = (float*)at;
+        at += pl.state_bytes;
+    }
     cudaError_t e;
     if (pl.bounds > 0) {
         e = bf16 ? launch_linear_tc(a, nprob, pl, true, st)
                  : run_simt(a, nprob, pl.segs, pl.cut_segs, true, st);
         if (e != cudaSuccess) return e;
-        k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), kLinState / 1024, nprob), 256, 0, st>>>(a);
+        k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), kLinState / 4 / kCombineThreads, nprob),
+                        kCombineThreads, 0, st>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         *launches += 2;

@@ -28,7 +28,9 @@ struct LinProblem {
     int out_f32;               // out is float32 whatever the data type
     const float* m0; int m0_t; // incoming state of each sequence (or null); transposed
     float* mout;               // outgoing state of each sequence (or null)
+    int has_state;             // the call has an outgoing state here, wanted or not
     float s_out, s_weight, s_state;
+    int ws_t;                  // the boundary states are another problem's, transposed
     float* ws;                 // states at the segment boundaries [boundary][Hv][128][128]
 };
 constexpr int kLinProblems = 3;

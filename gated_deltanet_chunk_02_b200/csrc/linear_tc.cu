@@ -27,7 +27,7 @@
 //   warps 8-15  the state (lane = row, half the columns)
 //   warp 16     TMA: b, a, c of each chunk into a ring of two chunks' tiles
 //   warp 17     MMA: Sc, a M^T, P c, Mu
-//   warp 18     TMA: outputs, staged in the tile of a
+//   warp 18     TMA: outputs, staged in the tile of c
 // P (over Sc) and the parts are A operands in TMEM, so shared memory holds the
 // ring and the bf16 state alone and is read for B only.  The parts are made by
 // ldmatrix, which transposes c on the way: a thread gets pairs of tokens of one
@@ -94,6 +94,15 @@ __device__ __noinline__ bool lt_wait_long(uint64_t* b, uint32_t parity, int* abo
     atomicExch(abort, 1);
     raise_status(status, kStatusTimeout);
     return false;
+}
+// is the phase over? (mbar_try may hold the thread for a microsecond)
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
     return mbar_try(b, parity) || lt_wait_long(b, parity, abort, status);
@@ -319,8 +328,8 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
     for (; t < tiles; ++t) {
         const int s = at.slot;
         if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, &c->abort, k.a.status)) break;
-        // a comes where the a of two chunks ago was, and after that chunk's outputs
-        if (m == 1 && t >= kLtRing &&
+        // c comes where the c of two chunks ago was, and after that chunk's outputs
+        if (m == 2 && t >= kLtRing &&
             !lt_wait(&c->stored[t / 3 & 1], ((t / 3 - 2) >> 1) & 1, &c->abort, k.a.status))
             break;
         const CUtensorMap* mp = m == 0 ? mb : (m == 1 ? ma : mc);
@@ -342,6 +351,7 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
     const uint32_t tPart = tSc + 384, m_tile = tiles + kLtRing * kLtTile;
     int* const ab = &c->abort;
     const bool lead = elect_one();
+    bool ahead = false;
     Ring<kLtRing> at;
 #pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
@@ -353,17 +363,19 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
         const Ring<kLtRing> v = at;
         at.next();
         const uint32_t sb = b.tile(tiles), sa = a.tile(tiles), sv = v.tile(tiles);
-        if (!warp_wait(&c->full[b.slot], b.phase, ab, status) ||
-            !warp_wait(&c->full[a.slot], a.phase, ab, status) ||
-            // P of the last chunk has been read, and the third part beside it
-            (ci > 0 && !warp_wait(wk.exact ? &c->mu : &c->o, par ^ 1, ab, status)))
-            break;
-        tc_fence_after();
-        if (lead) {
-            mma_kk(tSc, sa, sb);
-            mma_commit(&c->sc);
+        if (!ahead) {
+            if (!warp_wait(&c->full[b.slot], b.phase, ab, status) ||
+                !warp_wait(&c->full[a.slot], a.phase, ab, status) ||
+                // P of the last chunk has been read, and the third part beside it
+                (ci > 0 && !warp_wait(wk.exact ? &c->mu : &c->o, par ^ 1, ab, status)))
+                break;
+            tc_fence_after();
+            if (lead) {
+                mma_kk(tSc, sa, sb);
+                mma_commit(&c->sc);
+            }
+            __syncwarp();
         }
-        __syncwarp();
         if (!warp_wait(&c->state, par, ab, status) ||
             (ci > 0 && !warp_wait(&c->drained, par ^ 1, ab, status)))
             break;
@@ -384,6 +396,22 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
             mma_commit(&c->o);
         }
         __syncwarp();
+        // the next Sc, if its tiles are there, while the parts are still made:
+        // the rows' next work then waits for them
+        Ring<kLtRing> a1 = at;
+        a1.next();
+        ahead = !wk.exact && ci + 1 < wk.nch &&
+                __all_sync(0xffffffffu, mbar_test(&c->full[at.slot], at.phase) &&
+                                            mbar_test(&c->full[a1.slot], a1.phase));
+        if (ahead) {
+            if (!warp_wait(&c->o, par, ab, status)) break;
+            tc_fence_after();
+            if (lead) {
+                mma_kk(tSc, a1.tile(tiles), at.tile(tiles));
+                mma_commit(&c->sc);
+            }
+            __syncwarp();
+        }
         if (!warp_wait(&c->parts, par, ab, status)) break;
         tc_fence_after();
         if (lead) {
@@ -403,12 +431,12 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
     __syncwarp();
 }
 
-// Half of one row's outputs from its accumulator: to the tile of a (its
-// products are done), for the store warp; straight to memory where rows of the
+// Half of one row's outputs from its accumulator: to the tile of c (which has
+// been read; a's and b's are needed sooner), for the store warp; straight to memory where rows of the
 // chunk are not the segment's, or in float32.  Direct stores of whole rows take
 // the shared-memory pipe for 1000 cycles a chunk.
 __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, int h, int64_t row,
-                                          const LinProblem& q, uint32_t a_tile, LtCtrl* c,
+                                          const LinProblem& q, uint32_t c_tile, LtCtrl* c,
                                           int chunk) {
     const int lane = threadIdx.x & 31;
     uint32_t x[2][32];
@@ -437,7 +465,7 @@ __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, in
         if (by_tma) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                sts128(a_tile + op_off(r, 8 * h + 4 * pc + e),
+                sts128(c_tile + op_off(r, 8 * h + 4 * pc + e),
                        make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
         } else if (r < n) {
             st_global32((__nv_bfloat16*)q.out + at + 32 * pc, w);
@@ -448,15 +476,15 @@ __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, in
     warp_arrive(&c->staged[chunk & 1], lane);
 }
 
-// The store warp's lane: a chunk's staged outputs to memory; then b may come
+// The store warp's lane: a chunk's staged outputs to memory; then c may come
 // into their tile.
 __device__ void lt_store(const LtWalk& wk, const LinProblem& q, const CUtensorMap* map, int row,
                          uint8_t* smem, LtCtrl* c, int* status) {
     Ring<kLtRing> at;
     for (int ci = 0; ci < wk.nch; ++ci) {
         at.next();
-        const uint8_t* tile = smem + at.slot * kLtTile;
         at.next();
+        const uint8_t* tile = smem + at.slot * kLtTile;
         at.next();
         const int r0 = wk.first(ci);
         if (!lt_wait(&c->staged[ci & 1], (ci >> 1) & 1, &c->abort, status)) break;
@@ -482,14 +510,17 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
     float d = 0.f;
     const uint32_t tPart = c->tmem + ((uint32_t)(quarter * 32) << 16) + 384 + 32 * h;
     Ring<kLtRing> at;
-    uint32_t a_tile = 0;
+    uint32_t c_tile = 0;
 #pragma unroll 1
     for (int ci = 0; ci <= wk.nch; ++ci) {
         if (ci > 0) {                                  // the last chunk's outputs, while Mu is formed
             const int r0 = wk.first(ci - 1);
-            if (!warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status)) break;
+            // parts: the other warps have read c too
+            if (!warp_wait(&c->parts, (ci - 1) & 1, &c->abort, p.status) ||
+                !warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status))
+                break;
             tc_fence_after();
-            lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, a_tile, c, ci - 1);
+            lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, c_tile, c, ci - 1);
         }
         if (ci < wk.nch) {
             const int n = wk.rows(wk.first(ci));
@@ -561,10 +592,10 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
             // the parts of w c, once the last chunk's have been read
             const Ring<kLtRing> b = at;
             at.next();
-            a_tile = at.tile(tiles);
             at.next();
             const Ring<kLtRing> v = at;
             at.next();
+            c_tile = v.tile(tiles);
             if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status) ||
                 (ci > 0 && !warp_wait(&c->mu, (ci - 1) & 1, &c->abort, p.status)))
                 break;
@@ -599,15 +630,27 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
     {   // the incoming state
         const bool first = wk.rev ? g.k == g.m - 1 : g.k == 0;
         const float* src = nullptr;
-        int rs = kD, cs = 1;
+        bool across = false;
         if (!first) {
             src = q.ws + ((g.slot0 + (wk.rev ? g.k : g.k - 1)) * p.Hv + hv) * kLinState;
+            across = q.ws_t != 0;
         } else if (q.m0) {
             src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
-            if (q.m0_t) { rs = 1; cs = kD; }
+            across = q.m0_t != 0;
         }
+        if (!src) {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) m[i] = src ? src[r * rs + (64 * h + i) * cs] : 0.f;
+            for (int i = 0; i < 64; ++i) m[i] = 0.f;
+        } else if (across) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) m[i] = src[(64 * h + i) * kD + r];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(src + r * kD + 64 * h + i);
+                m[i] = f.x; m[i + 1] = f.y; m[i + 2] = f.z; m[i + 3] = f.w;
+            }
+        }
     }
 #pragma unroll 1
     for (int ci = 0; ci < wk.nch; ++ci) {
@@ -666,8 +709,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     if (warp == 17) tmem_alloc(&c->tmem, 512);
     const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0,
                     // a sequence of several segments has its outgoing state from steps 1
-                    // and 2; whether it is asked for changes no output
-                    g.m == 1};
+                    // and 2; whether one is asked for changes no output
+                    g.m == 1 && q.has_state};
     {
         const double lg = lin_log2(p.loggate, hv);
         const int t = threadIdx.x, i = t % kRows, n1 = wk.n - (wk.nch - 1) * kRows;
@@ -742,6 +785,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         return;
     }
     const LinProblem& q = p.pr[blockIdx.z];
+    if (q.ws_t) return;
     const LinSeg g = lin_find(p, blockIdx.x, kCutSegments);
     if (!g.ok) return;
     const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
