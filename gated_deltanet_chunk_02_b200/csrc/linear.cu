@@ -21,7 +21,7 @@ namespace {
 // ---- step 2: boundary states ----
 // Slot k of a sequence holds what segment k (k + 1 if reverse) adds from zero;
 // it is replaced by the state that crosses that boundary.
-constexpr int kCombineThreads = 512;
+constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p) {
     const LinProblem& q = p.pr[blockIdx.z];
     if (q.ws_t) return;
@@ -53,45 +53,49 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
     const double lg = lin_log2(p.loggate, hv);
     const float a_full = lin_pow(lg, p.seg_len);
     const float a_last = lin_pow(lg, g.seq_n - (g.m - 1) * p.seg_len);
-    const int e = 4 * (blockIdx.y * kCombineThreads + threadIdx.x);
-    float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (q.m0) {
-        const float* s = q.m0 + (seq * p.Hv + hv) * kLinState;
-        if (!q.m0_t) {
-            m = *reinterpret_cast<const float4*>(s + e);
-        } else {
-            const int r = e / kLinD, c = e % kLinD;
-            m = make_float4(s[c * kLinD + r], s[(c + 1) * kLinD + r], s[(c + 2) * kLinD + r],
-                            s[(c + 3) * kLinD + r]);
+    // a share of the state's elements, four to a thread at a time
+    const int share = kLinState / gridDim.y;
+    for (int e = blockIdx.y * share + 4 * threadIdx.x; e < (blockIdx.y + 1) * share;
+         e += 4 * kCombineThreads) {
+        float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (q.m0) {
+            const float* s = q.m0 + (seq * p.Hv + hv) * kLinState;
+            if (!q.m0_t) {
+                m = *reinterpret_cast<const float4*>(s + e);
+            } else {
+                const int r = e / kLinD, c = e % kLinD;
+                m = make_float4(s[c * kLinD + r], s[(c + 1) * kLinD + r], s[(c + 2) * kLinD + r],
+                                s[(c + 3) * kLinD + r]);
+            }
         }
-    }
-    float4* const base = reinterpret_cast<float4*>(q.ws + (g.slot0 * p.Hv + hv) * kLinState + e);
-    const int64_t step = p.Hv * kLinState / 4;
-    constexpr int kAhead = 8;                          // loads in flight
-    for (int i0 = 0; i0 < g.m - 1; i0 += kAhead) {
-        float4 u[kAhead];
+        float4* const base = reinterpret_cast<float4*>(q.ws + (g.slot0 * p.Hv + hv) * kLinState + e);
+        const int64_t step = p.Hv * kLinState / 4;
+        constexpr int kAhead = 8;                      // loads in flight
+        for (int i0 = 0; i0 < g.m - 1; i0 += kAhead) {
+            float4 u[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j;
-            if (i < g.m - 1) u[j] = base[(q.reverse ? g.m - 2 - i : i) * step];
-        }
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + j;
+                if (i < g.m - 1) u[j] = base[(q.reverse ? g.m - 2 - i : i) * step];
+            }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const int i = i0 + j;
-            if (i >= g.m - 1) break;
-            const float a = q.reverse && i == 0 ? a_last : a_full;
-            m = make_float4(fmaf(a, m.x, u[j].x), fmaf(a, m.y, u[j].y), fmaf(a, m.z, u[j].z),
-                            fmaf(a, m.w, u[j].w));
-            base[(q.reverse ? g.m - 2 - i : i) * step] = m;
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = i0 + j;
+                if (i >= g.m - 1) break;
+                const float a = q.reverse && i == 0 ? a_last : a_full;
+                m = make_float4(fmaf(a, m.x, u[j].x), fmaf(a, m.y, u[j].y), fmaf(a, m.z, u[j].z),
+                                fmaf(a, m.w, u[j].w));
+                base[(q.reverse ? g.m - 2 - i : i) * step] = m;
+            }
         }
-    }
-    if (q.mout) {                                      // the walk's last segment left its part here
-        float4* const out =
-            reinterpret_cast<float4*>(q.mout + (seq * p.Hv + hv) * kLinState + e);
-        const float a = q.reverse ? a_full : a_last;
-        const float4 u = *out;
-        *out = make_float4(fmaf(a, m.x, u.x), fmaf(a, m.y, u.y), fmaf(a, m.z, u.z),
-                           fmaf(a, m.w, u.w));
+        if (q.mout) {                                  // the walk's last segment left its part here
+            float4* const out =
+                reinterpret_cast<float4*>(q.mout + (seq * p.Hv + hv) * kLinState + e);
+            const float a = q.reverse ? a_full : a_last;
+            const float4 u = *out;
+            *out = make_float4(fmaf(a, m.x, u.x), fmaf(a, m.y, u.y), fmaf(a, m.z, u.z),
+                               fmaf(a, m.w, u.w));
+        }
     }
 }
 
@@ -394,20 +398,23 @@ int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int 
     }
     return best < 1 ? 128 : 128 * best;
 }
-// Packed sequences have lengths that the host does not know: all their chunks
-// spread over the SMs, the last segment to run alone behind them (cutting 73
-// chunks of 32 heads at 6 instead of 16 took the output pass from 122 to 80 us).
+// Packed sequences have lengths that the host does not know.  Cut: all chunks
+// spread over the SMs, half of a last segment behind them.  Not cut: that, or
+// the longest sequence, taken to be half of the rows if there are several (73
+// chunks of 32 heads, the longest 32: 153 us not cut, and 153 to 163 us cut at
+// 6 to 16, 195 us at 3).
 int64_t pick_segment_packed(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows,
                             int ctas_per_head) {
     const int64_t chunks = (rows + 127) / 128, sms = sm_count();
     const int64_t heads = nprob * Hv * ctas_per_head;
-    int64_t best = chunks, cost = INT64_MAX;
-    for (int64_t len = 1; len <= chunks; len += len < 16 ? 1 : len / 8) {
-        const int64_t m = len < chunks ? (chunks + len - 1) / len : 0;     // segments of cut ones
-        const int64_t c = 2 * heads * (chunks + nseq) / sms + 2 * len +
-                          2 * heads * (m + nseq) / sms +
-                          (m ? heads * (chunks + m) / sms + len +
-                                   4 * nprob * Hv * m / sms + 8 : 0);
+    const int64_t longest = nseq > 1 ? (chunks + 1) / 2 : chunks;
+    const int64_t work = 2 * heads * (chunks + nseq) / sms;
+    int64_t best = chunks;
+    int64_t cost = (work > 2 * longest ? work : 2 * longest) * 5 / 4 + 2 * heads * nseq / sms;
+    for (int64_t len = 1; len < longest; len += len < 16 ? 1 : len / 8) {
+        const int64_t m = (chunks + len - 1) / len;    // segments of the cut ones
+        const int64_t c = work + len + 2 * heads * (m + nseq) / sms + heads * (chunks + m) / sms +
+                          len / 2 + 4 * nprob * Hv * m / sms + 8;
         if (c < cost) { cost = c; best = len; }
     }
     return best < 1 ? 128 : 128 * best;
@@ -451,8 +458,10 @@ cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool 
         e = bf16 ? launch_linear_tc(a, nprob, pl, true, st)
                  : run_simt(a, nprob, pl.segs, pl.cut_segs, true, st);
         if (e != cudaSuccess) return e;
-        k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), kLinState / 4 / kCombineThreads, nprob),
-                        kCombineThreads, 0, st>>>(a);
+        // blocks for four to an SM: of packed sequences many have nothing to do here
+        int parts = 16;
+        while (parts > 1 && a.nseq * a.Hv * parts > 4LL * sm_count()) parts /= 2;
+        k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), parts, nprob), kCombineThreads, 0, st>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         *launches += 2;

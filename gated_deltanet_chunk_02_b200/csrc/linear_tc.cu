@@ -396,19 +396,24 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
             mma_commit(&c->o);
         }
         __syncwarp();
-        // the next Sc, if its tiles are there, while the parts are still made:
-        // the rows' next work then waits for them
-        Ring<kLtRing> a1 = at;
-        a1.next();
-        ahead = !wk.exact && ci + 1 < wk.nch &&
-                __all_sync(0xffffffffu, mbar_test(&c->full[at.slot], at.phase) &&
-                                            mbar_test(&c->full[a1.slot], a1.phase));
-        if (ahead) {
-            if (!warp_wait(&c->o, par, ab, status)) break;
-            tc_fence_after();
-            if (lead) {
-                mma_kk(tSc, a1.tile(tiles), at.tile(tiles));
-                mma_commit(&c->sc);
+        // the next Sc, if its tiles come while the parts are still made: the rows'
+        // next work waits for it
+        ahead = false;
+        if (!wk.exact && ci + 1 < wk.nch) {
+            Ring<kLtRing> a1 = at;
+            a1.next();
+            while (!ahead && !__all_sync(0xffffffffu, mbar_test(&c->parts, par))) {
+                ahead = __all_sync(0xffffffffu, mbar_test(&c->full[at.slot], at.phase) &&
+                                                    mbar_test(&c->full[a1.slot], a1.phase) &&
+                                                    mbar_test(&c->o, par));
+                if (*(volatile int*)ab) break;         // the rows' own wait ran out
+            }
+            if (ahead) {
+                tc_fence_after();
+                if (lead) {
+                    mma_kk(tSc, a1.tile(tiles), at.tile(tiles));
+                    mma_commit(&c->sc);
+                }
             }
             __syncwarp();
         }
