@@ -112,30 +112,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* abo
     return __all_sync(0xffffffffu, lt_wait(b, parity, abort, status));
 }
 
-// two floats in one register pair
-struct F2 {
-    uint64_t v;
-    F2() = default;
-    __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
-    __device__ void get(float& a, float& b) const {
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-    }
-};
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
-    F2 r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 // The upper 16 bits of both (truncated to bf16) as a pair, and what is left.
 __device__ __forceinline__ uint32_t take_upper(F2& x) {
     float a, b;

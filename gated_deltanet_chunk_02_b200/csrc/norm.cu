@@ -13,69 +13,125 @@
 // The row is recomputed from y, z, r in float32, so nothing is saved in the
 // forward pass and dx does not see X's rounding.
 //
-// GPU mapping.  Bound by moving the rows.  A row lives in the registers of
-// TPR threads, 8 channels per 16-byte (bf16) load and V such vectors per
-// thread, so every input crosses once; CTAs are persistent, keep the weights
-// in registers and load the next row while the current one is reduced.  A
-// row's sums go by shuffle inside a warp and through shared memory across
-// warps, in a fixed order.  Weight gradients stay in registers over all rows
-// of a CTA; the CTAs' partial sums (float32) are added by a second kernel in
-// CTA order, so results do not depend on scheduling.
+// GPU mapping.  Bound by moving the rows, so bytes in flight decide.  A row
+// lives in the registers of `tpr` threads as V 16-byte vectors per thread and
+// input, all loaded before anything is reduced: with many rows V is 8 (4
+// backward), so that a row of 2048 bf16 channels is one warp's (two warps') and
+// needs no (one) barrier; with rows too few to fill the GPU V is small, for the
+// latency of one row.  Weights are read again for each row (from L1).  A row's
+// sums go by shuffle inside a warp and through shared memory across warps, in a
+// fixed order.  Backward, CTAs stay and keep the weight gradients of their rows
+// in registers; the CTAs' sums (float32) are added by a second kernel in CTA
+// order, so results do not depend on scheduling.
 #include "common.cuh"
 #include "kernels.h"
 
 namespace gdn {
 namespace {
 
-constexpr int kNormThreads = 256;                      // threads of a CTA with several rows
-constexpr int kNormMaxRow = 512;                       // most threads on one row
+template <typename T>
+constexpr int kE = 16 / (int)sizeof(T);                // channels of a vector
 
-// 8 consecutive channels
-__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+// Channels are handled in pairs (F2): one at a time the instructions, not the
+// bytes, were the bound (forward 110 us, backward 243 us at 16384 x 2048 bf16).
+__device__ __forceinline__ void unpack(const uint4& u, F2 (&x)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+        x[i] = F2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void ld8(const float* p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    const float4 b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void unpack(const uint4& u, F2 (&x)[2]) {
+    x[0] = F2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = F2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-__device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack(const F2 (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        float a, b;
+        x[i].get(a, b);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void st8(float* p, const float (&x)[8]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ uint4 pack(const F2 (&x)[2]) {
+    float a, b, c, d;
+    x[0].get(a, b);
+    x[1].get(c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c),
+                      __float_as_uint(d));
+}
+__device__ __forceinline__ F2 both(float x) { return F2(x, x); }
+__device__ __forceinline__ float sum2(F2 x) {
+    float a, b;
+    x.get(a, b);
+    return a + b;
+}
+// weights of the channels from `at` on (ones without any)
+template <int P>
+__device__ __forceinline__ void weights(const float* w, int at, F2 (&x)[P]) {
+    if (w) {
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(w + at + 2 * i));
+            x[i] = F2(f.x, f.y);
+            x[i + 1] = F2(f.z, f.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) x[i] = both(1.f);
+    }
 }
 
-// act(z) and its derivative.  Both tails of the logistic function come from
-// e^-|z|, so 1 - s keeps its digits where s is near one.
-__device__ __forceinline__ float gate_of(float z, int act, float& slope) {
-    const float t = expf(-fabsf(z)), near1 = 1.f / (1.f + t), near0 = t * near1;
-    const float s = z >= 0.f ? near1 : near0, s1 = z >= 0.f ? near0 : near1;
+// t = e^-z and s = 1 / (1 + t), two at a time.  The exponent -z log2(e) is held
+// as a sum of two floats, h + l, so that the base-2 exponential of h and
+// 1 + l ln 2 keep the digits that a single product would lose for large |z|.
+// z stops at -87, where t is still finite (1 - s = t s then keeps its digits
+// too), and at 126, where h is; a NaN stays one.
+__device__ __forceinline__ float between(float z) {
+    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(z));  // -87
+    asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(z));  // 126
+    return z;
+}
+__device__ __forceinline__ void logistic2(F2 z, F2& t, F2& s) {
+    float x, y;
+    z.get(x, y);
+    z = F2(between(x), between(y));
+    const F2 h = mul2(z, both(-1.442695041f));
+    // -log2(e) = -1.442695041 (as a float) - 1.925963e-8
+    const F2 l = fma2(z, both(-1.925963033e-8f), fma2(z, both(-1.442695041f), mul2(h, both(-1.f))));
+    h.get(x, y);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
+    const F2 e(x, y);
+    t = fma2(e, mul2(l, both(0.6931471806f)), e);
+    add2(t, both(1.f)).get(x, y);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
+    s = F2(x, y);
+}
+// act(z)
+__device__ __forceinline__ F2 gate_of(F2 z, int act) {
+    F2 t, s;
+    logistic2(z, t, s);
+    return act == GDN_ACT_SILU ? mul2(z, s) : s;
+}
+// act(z) and its derivative
+__device__ __forceinline__ F2 gate_of(F2 z, int act, F2& slope) {
+    F2 t, s;
+    logistic2(z, t, s);
+    const F2 s1 = mul2(t, s);                          // 1 - s
     if (act == GDN_ACT_SILU) {
-        slope = s * fmaf(z, s1, 1.f);
-        return z * s;
+        slope = mul2(s, fma2(z, s1, both(1.f)));
+        return mul2(z, s);
     }
-    slope = s * s1;
+    slope = mul2(s, s1);
     return s;
 }
 
-// Sum of N values over the threads of a row (TPR of them, a multiple of 32),
-// the same for all of them.  `red` holds [rows of the CTA][TPR / 32][N] floats
-// and is free again after the next call's first barrier: callers alternate two.
+// Sum of N values over the threads of a row (tpr of them, a multiple of 32),
+// the same for all of them; `red` is used once per barrier-free stretch.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int tpr) {
 #pragma unroll
@@ -84,11 +140,10 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int tpr) {
         for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     const int warps = tpr >> 5;
     if (warps == 1) return;
-    const int w = threadIdx.x >> 5;
     float* mine = red + threadIdx.y * warps * N;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int i = 0; i < N; ++i) mine[w * N + i] = v[i];
+        for (int i = 0; i < N; ++i) mine[(threadIdx.x >> 5) * N + i] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.f;
@@ -96,18 +151,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* red, int tpr) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += mine[k * N + i];
 }
-// the same over the 16 lanes that hold one head of 128 channels
+// the same over the lanes that hold one head of 128 channels (16 of bf16, 32)
+template <int E>
 __device__ __forceinline__ float head_sum(float x) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 64 / E; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-
-// One row's inputs for this thread: V vectors of 8 channels each.
-template <typename T, int V>
-struct RowIn {
-    float y[V][8], z[V][8], r[V][8];
-};
 
 // offset of channel e of a row of y (rows are below 2^31)
 __device__ __forceinline__ int64_t y_at(const NormArgs& p, const gdn_strides& s, int64_t row,
@@ -117,331 +167,365 @@ __device__ __forceinline__ int64_t y_at(const NormArgs& p, const gdn_strides& s,
     return b * s.b + h * s.h + t * s.t + c;
 }
 
-// ---- the row up to x: yh, 1/rms(y) per vector, act, act', x ----
-template <typename T, int V>
-struct RowState {
-    float y[V][8];        // yh (y itself without a post norm)
-    float ry[V];          // 1 / rms of the vector's head
-    float x[V][8];
-    float g[V][8], dg[V][8];  // act(z), act'(z) (1, 0 without a gate)
-};
-
-template <typename T, int V, bool GRAD>
-__device__ __forceinline__ void row_x(const NormArgs& p, const RowIn<T, V>& in,
-                                      const float (&wo)[V][8], RowState<T, V>& s, float* red,
-                                      int tpr, const bool (&has)[V]) {
+// 1 / rms_d of y, by vector (H > 1) or for the row; 1 without a post norm
+template <int V, int E>
+__device__ __forceinline__ void post_scale(const NormArgs& p, const uint4 (&y)[V], float (&ry)[V],
+                                           float* red, int tpr) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) ry[k] = 1.f;
+    if (!p.w_post) return;
+    float q[V], all[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        s.ry[k] = 1.f;
+        F2 v[E / 2], a = both(0.f);
+        unpack(y[k], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s.y[k][i] = in.y[k][i];
+        for (int i = 0; i < E / 2; ++i) a = fma2(v[i], v[i], a);
+        q[k] = sum2(a);
+        all[0] += q[k];
     }
-    if (p.w_post) {
-        if (p.H == 1) {
-            float q[1] = {0.f};
+    if (p.H == 1) {
+        row_sums<1>(all, red, tpr);
+        const float r = 1.f / sqrtf(all[0] / (float)p.d + p.eps);
 #pragma unroll
-            for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V; ++k) ry[k] = r;
+    } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) q[0] = fmaf(s.y[k][i], s.y[k][i], q[0]);
-            row_sums<1>(q, red, tpr);
-            const float ri = 1.f / sqrtf(q[0] / (float)p.d + p.eps);
-#pragma unroll
-            for (int k = 0; k < V; ++k) s.ry[k] = ri;
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                float q = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) q = fmaf(s.y[k][i], s.y[k][i], q);
-                s.ry[k] = 1.f / sqrtf(head_sum(q) * (1.f / 128.f) + p.eps);
-            }
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        if (!has[k]) s.ry[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            s.y[k][i] *= s.ry[k];
-            float n = s.y[k][i] * wo[k][i], sl = 0.f, g = 1.f;
-            if (p.Z) g = gate_of(in.z[k][i], p.act, sl);
-            if (GRAD) { s.g[k][i] = g; s.dg[k][i] = sl; }
-            s.x[k][i] = fmaf(p.scale, n * g, in.r[k][i]);
-            if (!has[k]) s.x[k][i] = 0.f;
-        }
+        for (int k = 0; k < V; ++k) ry[k] = 1.f / sqrtf(head_sum<E>(q[k]) * (1.f / 128.f) + p.eps);
     }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kNormMaxRow)
-k_block_norm(const NormArgs p) {
+template <typename T, int V, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_block_norm(const NormArgs p) {
+    constexpr int E = kE<T>;
     extern __shared__ float red[];
     const int tpr = blockDim.x, W = (int)(p.H * p.d);
-    const int64_t rows = p.B * p.T, step = (int64_t)gridDim.x * blockDim.y;
-    int at[V];
-    bool has[V];
-    float wo[V][8], wi[V][8];
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, rows = p.B * p.T;
+    uint4 y[V], z[V], r[V];
+    bool ok[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        at[k] = 8 * (threadIdx.x + k * tpr);
-        has[k] = at[k] < W;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            wo[k][i] = has[k] && p.w_post ? p.w_post[at[k] + i] : 1.f;
-            wi[k][i] = has[k] && p.w_pre ? p.w_pre[at[k] + i] : 0.f;
-        }
+        const int at = E * (threadIdx.x + k * tpr);
+        ok[k] = at < W && row < rows;
+        y[k] = z[k] = r[k] = make_uint4(0, 0, 0, 0);
+        if (!ok[k]) continue;
+        y[k] = *reinterpret_cast<const uint4*>((const T*)p.Y + y_at(p, p.ys, row, at));
+        if (p.Z) z[k] = *reinterpret_cast<const uint4*>((const T*)p.Z + row * W + at);
+        if (p.R) r[k] = *reinterpret_cast<const uint4*>((const T*)p.R + row * W + at);
     }
-    const int span = blockDim.y * (tpr >> 5);          // floats of one reduction buffer
-    auto load = [&](int64_t row, RowIn<T, V>& in) {
+    float ry[V];
+    post_scale<V, E>(p, y, ry, red, tpr);
+    constexpr int P = E / 2;                           // pairs of a vector
+    F2 x[V][P], xx = both(0.f);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const bool ok = has[k] && row < rows;
-            const int64_t e = row * W + at[k];
+    for (int k = 0; k < V; ++k) {
+        const int at = E * (threadIdx.x + k * tpr);
+        F2 w[P], yv[P], zv[P];
+        weights(p.w_post, min(at, W - E), w);
+        unpack(y[k], yv);
+        unpack(r[k], x[k]);
+        const F2 a = both(p.scale * ry[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) in.y[k][i] = in.z[k][i] = in.r[k][i] = 0.f;
-            if (!ok) continue;
-            ld8((const T*)p.Y + y_at(p, p.ys, row, at[k]), in.y[k]);
-            if (p.Z) ld8((const T*)p.Z + e, in.z[k]);
-            if (p.R) ld8((const T*)p.R + e, in.r[k]);
+        for (int i = 0; i < P; ++i) yv[i] = mul2(mul2(yv[i], a), w[i]);
+        if (p.Z) {
+            unpack(z[k], zv);
+#pragma unroll
+            for (int i = 0; i < P; ++i) yv[i] = mul2(yv[i], gate_of(zv[i], p.act));
         }
-    };
-    for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < rows; base += step) {
-        const int64_t row = base + threadIdx.y;        // every thread takes every barrier
-        RowIn<T, V> in;
-        load(row, in);
-        RowState<T, V> s;
-        row_x<T, V, false>(p, in, wo, s, red, tpr, has);
-        float q[1] = {0.f};
-        if (p.w_pre) {
 #pragma unroll
-            for (int k = 0; k < V; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) q[0] = fmaf(s.x[k][i], s.x[k][i], q[0]);
-            row_sums<1>(q, red + span, tpr);
+        for (int i = 0; i < P; ++i) {
+            x[k][i] = add2(x[k][i], yv[i]);
+            xx = fma2(x[k][i], x[k][i], xx);
         }
-        const float ri = 1.f / sqrtf(q[0] / (float)W + p.eps);
+        if (p.X && ok[k])
+            *reinterpret_cast<uint4*>((T*)p.X + row * W + at) = pack(x[k]);
+    }
+    if (!p.w_pre) return;
+    float q[1] = {sum2(xx)};
+    row_sums<1>(q, red + (tpr >> 5) * blockDim.y, tpr);
+    const F2 ri = both(1.f / sqrtf(q[0] / (float)W + p.eps));
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            if (!has[k] || row >= rows) continue;
-            const int64_t e = row * W + at[k];
-            if (p.X) st8((T*)p.X + e, s.x[k]);
-            if (p.w_pre) {
+    for (int k = 0; k < V; ++k) {
+        if (!ok[k]) continue;
+        const int at = E * (threadIdx.x + k * tpr);
+        F2 w[P];
+        weights(p.w_pre, at, w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s.x[k][i] = s.x[k][i] * ri * wi[k][i];
-                st8((T*)p.N + e, s.x[k]);
-            }
-        }
-        // red's two buffers are written in turn; with only one of the two
-        // sums present the next row's would overtake its readers
-        if (tpr > 32 && !(p.w_pre && p.w_post && p.H == 1)) __syncthreads();
+        for (int i = 0; i < P; ++i) x[k][i] = mul2(mul2(x[k][i], ri), w[i]);
+        *reinterpret_cast<uint4*>((T*)p.N + row * W + at) = pack(x[k]);
     }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kNormMaxRow)
-k_block_norm_backward(const NormArgs p) {
-    extern __shared__ float red[];
-    const int tpr = blockDim.x, W = (int)(p.H * p.d);
+template <typename T, int V, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) {
+    constexpr int E = kE<T>;
+    extern __shared__ __align__(16) float red[];
+    const int tpr = blockDim.x, W = (int)(p.H * p.d), span = blockDim.y * (tpr >> 5) * 2;
     const int64_t rows = p.B * p.T, step = (int64_t)gridDim.x * blockDim.y;
-    int at[V];
-    bool has[V];
-    float wo[V][8], wi[V][8], dwo[V][8], dwi[V][8];
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-        at[k] = 8 * (threadIdx.x + k * tpr);
-        has[k] = at[k] < W;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            wo[k][i] = has[k] && p.w_post ? p.w_post[at[k] + i] : 1.f;
-            wi[k][i] = has[k] && p.w_pre ? p.w_pre[at[k] + i] : 0.f;
-            dwo[k][i] = dwi[k][i] = 0.f;
-        }
-    }
-    const int span = blockDim.y * (tpr >> 5) * 2;
-    for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < rows; base += step) {
-        const int64_t row = base + threadIdx.y;
-        RowIn<T, V> in;
-        float dx[V][8], dn[V][8];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const bool ok = has[k] && row < rows;
-            const int64_t e = row * W + at[k];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                in.y[k][i] = in.z[k][i] = in.r[k][i] = dx[k][i] = dn[k][i] = 0.f;
-            if (!ok) continue;
-            ld8((const T*)p.Y + y_at(p, p.ys, row, at[k]), in.y[k]);
-            if (p.Z) ld8((const T*)p.Z + e, in.z[k]);
-            if (p.R) ld8((const T*)p.R + e, in.r[k]);
-            if (p.dX) ld8((const T*)p.dX + e, dx[k]);
-            if (p.dN) ld8((const T*)p.dN + e, dn[k]);
-        }
-        RowState<T, V> s;
-        row_x<T, V, true>(p, in, wo, s, red, tpr, has);
-        if (p.w_pre) {
-            // sum x^2 and sum w_pre dN x together: mean(g xh) = ri sum(g x) / W
-            float q[2] = {0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    q[0] = fmaf(s.x[k][i], s.x[k][i], q[0]);
-                    q[1] = fmaf(wi[k][i] * dn[k][i], s.x[k][i], q[1]);
-                }
-            row_sums<2>(q, red + span, tpr);
-            const float ri = 1.f / sqrtf(q[0] / (float)W + p.eps);
-            const float m = ri * q[1] / (float)W;
-#pragma unroll
-            for (int k = 0; k < V; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float xh = s.x[k][i] * ri;
-                    dwi[k][i] = fmaf(dn[k][i], xh, dwi[k][i]);
-                    dx[k][i] = fmaf(ri, fmaf(-xh, m, wi[k][i] * dn[k][i]), dx[k][i]);
-                }
-        }
-        float e1[1] = {0.f}, eh[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int64_t e = row * W + at[k];
-            const bool ok = has[k] && row < rows;
-            if (p.dR && ok) st8((T*)p.dR + e, dx[k]);
-            eh[k] = 0.f;
-            float dz[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float du = p.scale * dx[k][i];
-                dz[i] = du * (s.y[k][i] * wo[k][i]) * s.dg[k][i];
-                const float d1 = du * s.g[k][i];       // dn
-                dwo[k][i] = fmaf(d1, s.y[k][i], dwo[k][i]);
-                dx[k][i] = d1 * wo[k][i];              // e
-                eh[k] = fmaf(dx[k][i], s.y[k][i], eh[k]);
-            }
-            if (p.dZ && ok) st8((T*)p.dZ + e, dz);
-            e1[0] += eh[k];
-        }
-        if (p.w_post) {
-            float m = 0.f;
-            if (p.H == 1) {
-                row_sums<1>(e1, red + 2 * span, tpr);
-                m = e1[0] / (float)p.d;
-            }
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-                const float mk = p.H == 1 ? m : head_sum(eh[k]) * (1.f / 128.f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dx[k][i] = s.ry[k] * fmaf(-s.y[k][i], mk, dx[k][i]);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-            if (has[k] && row < rows)
-                st8((T*)p.dY + y_at(p, p.dys, row, at[k]), dx[k]);
-        // a sum's buffer is next written after at least one barrier of
-        // another sum when two or three are present; with one, add one
-        if (tpr > 32 && !(p.w_post && p.H == 1)) __syncthreads();
-    }
-    // partial sums of this CTA's row group: [group][2][W]
-    const int64_t group = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    constexpr int P = E / 2;                           // pairs of a vector
+    F2 dwo[V][P], dwi[V][P];
 #pragma unroll
     for (int k = 0; k < V; ++k)
-        if (has[k]) {
-            if (p.dw_post) st8(p.ws + (group * 2) * W + at[k], dwo[k]);
-            if (p.dw_pre) st8(p.ws + (group * 2 + 1) * W + at[k], dwi[k]);
+#pragma unroll
+        for (int i = 0; i < P; ++i) dwo[k][i] = dwi[k][i] = both(0.f);
+    for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < rows; base += step) {
+        const int64_t row = base + threadIdx.y;        // every thread takes every barrier
+        uint4 y[V], z[V], r[V], gx[V], gn[V];
+        bool ok[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = E * (threadIdx.x + k * tpr);
+            const int64_t e = row * W + at;
+            ok[k] = at < W && row < rows;
+            y[k] = z[k] = r[k] = gx[k] = gn[k] = make_uint4(0, 0, 0, 0);
+            if (!ok[k]) continue;
+            y[k] = *reinterpret_cast<const uint4*>((const T*)p.Y + y_at(p, p.ys, row, at));
+            if (p.Z) z[k] = *reinterpret_cast<const uint4*>((const T*)p.Z + e);
+            if (p.R) r[k] = *reinterpret_cast<const uint4*>((const T*)p.R + e);
+            if (p.dX) gx[k] = *reinterpret_cast<const uint4*>((const T*)p.dX + e);
+            if (p.dN) gn[k] = *reinterpret_cast<const uint4*>((const T*)p.dN + e);
         }
+        float ry[V];
+        post_scale<V, E>(p, y, ry, red, tpr);
+        F2 x[V][P];                                    // x, then e
+        float ri = 0.f, m = 0.f;
+        // x, and its two sums: sum x^2, sum w_pre dN x (mean(g xh) = ri sum(g x) / W)
+        F2 xx = both(0.f), gg = both(0.f);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = min(E * (int)(threadIdx.x + k * tpr), W - E);
+            F2 w[P], yv[P], zv[P], gv[P];
+            weights(p.w_post, at, w);
+            unpack(y[k], yv);
+            unpack(r[k], x[k]);
+            const F2 a = both(p.scale * ry[k]);
+#pragma unroll
+            for (int i = 0; i < P; ++i) yv[i] = mul2(mul2(yv[i], a), w[i]);
+            if (p.Z) {
+                unpack(z[k], zv);
+#pragma unroll
+                for (int i = 0; i < P; ++i) yv[i] = mul2(yv[i], gate_of(zv[i], p.act));
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) x[k][i] = add2(x[k][i], yv[i]);
+            if (p.w_pre) {
+                weights(p.w_pre, at, w);
+                unpack(gn[k], gv);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    xx = fma2(x[k][i], x[k][i], xx);
+                    gg = fma2(mul2(w[i], gv[i]), x[k][i], gg);
+                }
+            }
+        }
+        if (p.w_pre) {
+            float q[2] = {sum2(xx), sum2(gg)};
+            row_sums<2>(q, red + span, tpr);
+            ri = 1.f / sqrtf(q[0] / (float)W + p.eps);
+            m = ri * q[1] / (float)W;
+        }
+        float all[1] = {0.f}, eh[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = E * (threadIdx.x + k * tpr), aw = min(at, W - E);
+            const int64_t e = row * W + at;
+            F2 w[P], yv[P], dx[P], gv[P];
+            unpack(gx[k], dx);
+            if (p.w_pre) {
+                weights(p.w_pre, aw, w);
+                unpack(gn[k], gv);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const F2 xh = mul2(x[k][i], both(ri));
+                    dwi[k][i] = fma2(gv[i], xh, dwi[k][i]);
+                    dx[i] = fma2(both(ri), fma2(xh, both(-m), mul2(w[i], gv[i])), dx[i]);
+                }
+            }
+            if (p.dR && ok[k]) *reinterpret_cast<uint4*>((T*)p.dR + e) = pack(dx);
+            weights(p.w_post, aw, w);
+            unpack(y[k], yv);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                yv[i] = mul2(yv[i], both(ry[k]));      // yh
+                dx[i] = mul2(dx[i], both(p.scale));    // du
+            }
+            if (p.Z) {
+                F2 zv[P];
+                unpack(z[k], zv);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    F2 slope;
+                    const F2 g = gate_of(zv[i], p.act, slope);
+                    zv[i] = mul2(mul2(dx[i], mul2(yv[i], w[i])), slope);   // dz
+                    dx[i] = mul2(dx[i], g);            // dn
+                }
+                if (ok[k]) *reinterpret_cast<uint4*>((T*)p.dZ + e) = pack(zv);
+            }
+            F2 s = both(0.f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                dwo[k][i] = fma2(dx[i], yv[i], dwo[k][i]);
+                x[k][i] = mul2(dx[i], w[i]);
+                s = fma2(x[k][i], yv[i], s);
+            }
+            eh[k] = sum2(s);
+            all[0] += eh[k];
+        }
+        if (p.w_post && p.H == 1) row_sums<1>(all, red + 2 * span, tpr);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = E * (threadIdx.x + k * tpr);
+            if (p.w_post) {
+                F2 yv[P];
+                unpack(y[k], yv);
+                const float mk = p.H == 1 ? all[0] / (float)p.d : head_sum<E>(eh[k]) * (1.f / 128.f);
+                const F2 a = both(ry[k]), b = both(-ry[k] * mk);
+#pragma unroll
+                for (int i = 0; i < P; ++i) x[k][i] = mul2(a, fma2(yv[i], b, x[k][i]));
+            }
+            if (ok[k])
+                *reinterpret_cast<uint4*>((T*)p.dY + y_at(p, p.dys, row, at)) = pack(x[k]);
+        }
+        // a sum's buffer is next written behind another sum's barrier when two
+        // or three are present, else behind this one
+        if (tpr > 32 && !(p.w_post && p.H == 1)) __syncthreads();
+    }
+    // the CTA's sums: its row groups in order, then to ws [CTA][2][W]
+    F2* part = reinterpret_cast<F2*>(red + 3 * span);  // [blockDim.y - 1][2][W / 2]
+    const int W2 = W / 2;
+    if (blockDim.y > 1) {
+        __syncthreads();
+        if (threadIdx.y > 0)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int at = P * (threadIdx.x + k * tpr);
+                if (at < W2)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        part[(threadIdx.y - 1) * 2 * W2 + at + i] = dwo[k][i];
+                        part[((threadIdx.y - 1) * 2 + 1) * W2 + at + i] = dwi[k][i];
+                    }
+            }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+    }
+    F2* const to = reinterpret_cast<F2*>(p.ws) + (int64_t)blockIdx.x * 2 * W2;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int at = P * (threadIdx.x + k * tpr);
+        if (at >= W2) continue;
+        for (int g = 0; g + 1 < blockDim.y; ++g)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                dwo[k][i] = add2(dwo[k][i], part[g * 2 * W2 + at + i]);
+                dwi[k][i] = add2(dwi[k][i], part[(g * 2 + 1) * W2 + at + i]);
+            }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (p.dw_post) to[at + i] = dwo[k][i];
+            if (p.dw_pre) to[W2 + at + i] = dwi[k][i];
+        }
+    }
 }
 
-// dw[c] = sum over the groups in order, four strands; blockIdx.y: post, pre
-__global__ void __launch_bounds__(256) k_norm_dw(const float* ws, float* dw_post, float* dw_pre,
-                                                 int W, int groups) {
-    __shared__ float part[8][32];
+// dw[c] = sum over the CTAs, 32 strands each in order; blockIdx.y: post, pre
+__global__ void __launch_bounds__(1024) k_norm_dw(const float* ws, float* dw_post, float* dw_pre,
+                                                  int W, int ctas) {
+    __shared__ float part[32][33];
     float* out = blockIdx.y ? dw_pre : dw_post;
     if (!out) return;
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float a = 0.f;
     if (c < W)
-        for (int g = w; g < groups; g += 8) a += ws[((int64_t)g * 2 + blockIdx.y) * W + c];
-    part[w][threadIdx.x & 31] = a;
+#pragma unroll 8
+        for (int g = w; g < ctas; g += 32) a += ws[((int64_t)g * 2 + blockIdx.y) * W + c];
+    part[w][lane] = a;
     __syncthreads();
     if (w == 0 && c < W) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+        for (int i = 0; i < 32; ++i) s += part[i][lane];
         out[c] = s;
     }
 }
 
-// threads per row, vectors per thread and rows per CTA for a width
+// vectors per thread, threads per row, rows per CTA
 struct NormShape {
-    int tpr, v, rpc;
+    int v, tpr, rpc;
 };
-NormShape norm_shape(int64_t W) {
-    const int vecs = (int)(W / 8);
+// As many vectors a thread, `most` at the top, as leave 16 warps for every SM
+// and the row a warp of its own; more where a row would take over 512 threads.
+NormShape norm_shape(int64_t rows, int64_t W, int e, int most, int wide) {
+    const int vecs = (int)(W / e);
     NormShape s;
-    s.v = vecs <= kNormMaxRow ? 1 : (vecs <= 2 * kNormMaxRow ? 2 : 4);
-    s.tpr = ((vecs + s.v - 1) / s.v + 31) / 32 * 32;
-    s.rpc = s.tpr >= kNormThreads ? 1 : kNormThreads / s.tpr;
+    auto warps = [&](int v) { return (vecs + 32 * v - 1) / (32 * v); };
+    s.v = 1;
+    while ((warps(s.v) > 16 && s.v < wide) ||
+           (s.v < most && vecs >= 64 * s.v && rows * warps(2 * s.v) >= 16LL * sm_count()))
+        s.v *= 2;
+    s.tpr = 32 * warps(s.v);
+    s.rpc = s.tpr >= 128 ? 1 : 128 / s.tpr;
     return s;
 }
+constexpr int kForwardV = 4, kBackwardV = 2;           // where rows are many
+constexpr int kForwardWide = 8, kBackwardWide = 4;     // where rows are wide
 
-constexpr int kNormCtas = 4;                           // CTAs per SM of the backward pass
-
-int backward_ctas(int64_t rows, const NormShape& s) {
-    const int64_t need = (rows + s.rpc - 1) / s.rpc, most = (int64_t)kNormCtas * sm_count();
-    return (int)(need < most ? need : most);
+// CTAs of the backward pass, whatever the data type (the workspace's size goes by it)
+int backward_ctas(int64_t rows) {
+    const int64_t most = 4LL * sm_count();
+    return (int)(rows < most ? rows : most);
 }
 
-template <typename T, int V>
+template <typename T, int V, int MAXT>
 void run_norm(const NormArgs& a, const NormShape& s, cudaStream_t st) {
-    const int64_t need = (a.B * a.T + s.rpc - 1) / s.rpc, most = 8LL * sm_count();
+    const int64_t ctas = (a.B * a.T + s.rpc - 1) / s.rpc;
     const int smem = 2 * s.rpc * (s.tpr / 32) * (int)sizeof(float);
-    k_block_norm<T, V><<<(unsigned)(need < most ? need : most), dim3(s.tpr, s.rpc), smem, st>>>(a);
+    k_block_norm<T, V, MAXT><<<(unsigned)ctas, dim3(s.tpr, s.rpc), smem, st>>>(a);
 }
-template <typename T, int V>
+template <typename T, int V, int MAXT>
 void run_norm_backward(const NormArgs& a, const NormShape& s, cudaStream_t st) {
-    const int smem = 3 * 2 * s.rpc * (s.tpr / 32) * (int)sizeof(float);
-    k_block_norm_backward<T, V>
-        <<<(unsigned)backward_ctas(a.B * a.T, s), dim3(s.tpr, s.rpc), smem, st>>>(a);
+    const int W = (int)(a.H * a.d);
+    const int smem = (3 * 2 * s.rpc * (s.tpr / 32) + (s.rpc - 1) * 2 * W) * (int)sizeof(float);
+    k_block_norm_backward<T, V, MAXT>
+        <<<(unsigned)backward_ctas(a.B * a.T), dim3(s.tpr, s.rpc), smem, st>>>(a);
+}
+template <typename T>
+void norm_forward(const NormArgs& a, cudaStream_t st) {
+    const NormShape s = norm_shape(a.B * a.T, a.H * a.d, kE<T>, kForwardV, kForwardWide);
+    if (s.v == 1) run_norm<T, 1, 512>(a, s, st);
+    else if (s.v == 2) run_norm<T, 2, 512>(a, s, st);
+    else if (s.v == 4) run_norm<T, 4, 512>(a, s, st);
+    else run_norm<T, 8, 512>(a, s, st);
+}
+template <typename T>
+void norm_backward(const NormArgs& a, cudaStream_t st) {
+    const NormShape s = norm_shape(a.B * a.T, a.H * a.d, kE<T>, kBackwardV, kBackwardWide);
+    if (s.v == 1) run_norm_backward<T, 1, 512>(a, s, st);
+    else if (s.v == 2) run_norm_backward<T, 2, 512>(a, s, st);
+    else if (s.tpr <= 256) run_norm_backward<T, 4, 256>(a, s, st);
+    else run_norm_backward<T, 4, 1024>(a, s, st);
 }
 
 }  // namespace
 
 int64_t block_norm_ws_bytes(int64_t rows, int64_t width) {
-    const NormShape s = norm_shape(width);
-    return (int64_t)backward_ctas(rows, s) * s.rpc * 2 * width * 4;
+    return (int64_t)backward_ctas(rows) * 2 * width * 4;
 }
 
 cudaError_t launch_block_norm(const NormArgs& a, bool bf16, cudaStream_t st) {
-    const NormShape s = norm_shape(a.H * a.d);
-    if (bf16) {
-        if (s.v == 1) run_norm<__nv_bfloat16, 1>(a, s, st);
-        else if (s.v == 2) run_norm<__nv_bfloat16, 2>(a, s, st);
-        else run_norm<__nv_bfloat16, 4>(a, s, st);
-    } else {
-        if (s.v == 1) run_norm<float, 1>(a, s, st);
-        else if (s.v == 2) run_norm<float, 2>(a, s, st);
-        else run_norm<float, 4>(a, s, st);
-    }
+    if (bf16) norm_forward<__nv_bfloat16>(a, st);
+    else norm_forward<float>(a, st);
     return cudaGetLastError();
 }
 
 cudaError_t launch_block_norm_backward(const NormArgs& a, bool bf16, cudaStream_t st) {
-    const NormShape s = norm_shape(a.H * a.d);
-    if (bf16) {
-        if (s.v == 1) run_norm_backward<__nv_bfloat16, 1>(a, s, st);
-        else if (s.v == 2) run_norm_backward<__nv_bfloat16, 2>(a, s, st);
-        else run_norm_backward<__nv_bfloat16, 4>(a, s, st);
-    } else {
-        if (s.v == 1) run_norm_backward<float, 1>(a, s, st);
-        else if (s.v == 2) run_norm_backward<float, 2>(a, s, st);
-        else run_norm_backward<float, 4>(a, s, st);
-    }
+    if (bf16) norm_backward<__nv_bfloat16>(a, st);
+    else norm_backward<float>(a, st);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !(a.dw_post || a.dw_pre)) return e;
     const int W = (int)(a.H * a.d);
-    k_norm_dw<<<dim3((W + 31) / 32, 2), 256, 0, st>>>(
-        a.ws, a.dw_post, a.dw_pre, W, backward_ctas(a.B * a.T, s) * s.rpc);
+    k_norm_dw<<<dim3((W + 31) / 32, 2), 1024, 0, st>>>(a.ws, a.dw_post, a.dw_pre, W,
+                                                       backward_ctas(a.B * a.T));
     return cudaGetLastError();
 }
 

@@ -317,12 +317,14 @@ def gdn_decode(Q, K, V, beta, loggate, S, O, stream=None):
 
 class _Call:
     """Checks of one call's tensors: shapes, types, one CUDA device (made
-    current for the launch) and the stream on it."""
+    current for the launch) and the stream on it.  Kept short: a call on a few
+    rows costs the host more than the GPU."""
+    __slots__ = ("index", "stream")
 
     def __init__(self, stream, first):
         if not isinstance(first, torch.Tensor):
             raise TypeError("expected a torch tensor")
-        self.device, self.stream = first.device, stream
+        self.index, self.stream = first.get_device(), stream
 
     def check(self, t, name, shape=None, dtype=None, strided=False):
         """The data pointer of ``t`` (None passes as NULL)."""
@@ -330,46 +332,62 @@ class _Call:
             return None
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch tensor")
-        if shape is not None and tuple(t.shape) != tuple(shape):
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, expected {self.device}")
-        if not t.is_cuda:
+        index = t.get_device()
+        if index < 0:
             raise ValueError(f"{name}: libgdn takes CUDA tensors")
+        if index != self.index:
+            raise ValueError(f"{name} is on cuda:{index}, expected cuda:{self.index}")
         if strided:
-            if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+            if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
                 raise ValueError(f"{name}: the last dimension is not contiguous")
         elif not t.is_contiguous():
             raise ValueError(f"{name}: libgdn takes contiguous tensors")
-        return ctypes.c_void_p(t.data_ptr())
+        return t.data_ptr()
 
     def run(self, name, *args):
         """The C call on the tensors' device and its current (or the given) stream."""
-        if self.stream is not None and self.stream.device != self.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-        with torch.cuda.device(self.device):
-            _check(getattr(load(), name)(*args, _stream(self.stream)))
+        f, index = getattr(_lib or load(), name), self.index
+        if self.stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(index)
+        elif self.stream.device.index != index:
+            raise ValueError(f"the stream is on {self.stream.device}, the tensors on cuda:{index}")
+        else:
+            stream = self.stream.cuda_stream
+        if torch.cuda.current_device() == index:
+            rc = f(*args, stream)
+        else:
+            with torch.cuda.device(index):
+                rc = f(*args, stream)
+        if rc != GDN_OK:
+            _check(rc)
 
 
 def _strides(t, b, h, tok):
     """Element strides of the named dimensions (0 where nothing is walked)."""
-    at = [t.stride(i) if t.shape[i] > 1 else 0 for i in (b, h, tok)]
-    return GdnStrides(*at)
+    n, st = t.shape, t.stride()
+    return GdnStrides(st[b] if n[b] > 1 else 0, st[h] if n[h] > 1 else 0,
+                      st[tok] if n[tok] > 1 else 0)
 
 
 def _apart(outs, ins):
     """Outputs share no memory with inputs or one another (contiguous tensors)."""
-    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
-    outs = [(n, t) for n, t in outs if t is not None and t.numel()]
-    rest = [(n, t) for n, t in ins if t is not None and t.numel()]
-    for i, (n, t) in enumerate(outs):
-        a0, a1 = span(t)
-        for m, u in outs[i + 1:] + rest:
-            b0, b1 = span(u)
-            if a0 < b1 and b0 < a1:
-                raise ValueError(f"{n} shares memory with {m}")
+    spans = [(t.data_ptr(), t.nbytes, True, n) for n, t in outs if t is not None]
+    spans += [(t.data_ptr(), t.nbytes, False, n) for n, t in ins if t is not None]
+    spans.sort()
+    end_out, end_all, last_out, last = 0, 0, "", ""
+    for at, size, out, name in spans:
+        if not size:
+            continue
+        if at < (end_all if out else end_out):
+            raise ValueError(f"{name} shares memory with {last if out else last_out}")
+        if out and at + size > end_out:
+            end_out, last_out = at + size, name
+        if at + size > end_all:
+            end_all, last = at + size, name
 
 
 def gdn_rotary_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, original_length=0):
@@ -377,7 +395,7 @@ def gdn_rotary_frequencies(rot, base=10000.0, scaling="plain", factor=1.0, origi
     factor on sines and cosines; ``scaling``: plain, linear, ntk or yarn."""
     inv = torch.empty(max(0, rot // 2), dtype=torch.float32)
     m = ctypes.c_float()
-    _check(load().gdn_rotary_frequencies(ctypes.c_void_p(inv.data_ptr()), ctypes.byref(m), rot,
+    _check(load().gdn_rotary_frequencies(inv.data_ptr(), ctypes.byref(m), rot,
                                          float(base), GDN_ROTARY[scaling], float(factor),
                                          int(original_length)))
     return inv, m.value
