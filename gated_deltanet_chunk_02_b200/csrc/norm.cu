@@ -20,8 +20,8 @@
 // needs no (one) barrier; with rows too few to fill the GPU V is small, for the
 // latency of one row.  Weights are read again for each row (from L1).  A row's
 // sums go by shuffle inside a warp and through shared memory across warps, in a
-// fixed order.  Backward, CTAs stay and keep the weight gradients of their rows
-// in registers; the CTAs' sums (float32) are added by a second kernel in CTA
+// fixed order.  Backward, CTAs stay, fetch a row ahead into shared memory and
+// keep the weight gradients of their rows in registers; the CTAs' sums (float32) are added by a second kernel in CTA
 // order, so results do not depend on scheduling.
 #include "common.cuh"
 #include "kernels.h"
@@ -84,50 +84,61 @@ __device__ __forceinline__ void weights(const float* w, int at, F2 (&x)[P]) {
     }
 }
 
-// t = e^-z and s = 1 / (1 + t), two at a time.  The exponent -z log2(e) is held
-// as a sum of two floats, h + l, so that the base-2 exponential of h and
-// 1 + l ln 2 keep the digits that a single product would lose for large |z|.
-// z stops at -87, where t is still finite (1 - s = t s then keeps its digits
-// too), and at 126, where h is; a NaN stays one.
-__device__ __forceinline__ float between(float z) {
-    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(z));  // -87
-    asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(z));  // 126
-    return z;
-}
+// t = e^-z and s = 1 / (1 + t), two at a time, by the base-2 exponential (the
+// product -z log2(e) costs |z| 2^-24).  z stops at -87, where t is still finite:
+// 1 - s = t s then keeps its digits where s is near one.  A NaN stays one.
 __device__ __forceinline__ void logistic2(F2 z, F2& t, F2& s) {
     float x, y;
     z.get(x, y);
-    z = F2(between(x), between(y));
-    const F2 h = mul2(z, both(-1.442695041f));
-    // -log2(e) = -1.442695041 (as a float) - 1.925963e-8
-    const F2 l = fma2(z, both(-1.925963033e-8f), fma2(z, both(-1.442695041f), mul2(h, both(-1.f))));
-    h.get(x, y);
+    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(x));  // -87
+    asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(y));
+    mul2(F2(x, y), both(-1.442695041f)).get(x, y);
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
-    const F2 e(x, y);
-    t = fma2(e, mul2(l, both(0.6931471806f)), e);
+    t = F2(x, y);
     add2(t, both(1.f)).get(x, y);
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
     s = F2(x, y);
 }
-// act(z)
-__device__ __forceinline__ F2 gate_of(F2 z, int act) {
+// x *= act(z), a vector's channels
+template <int P>
+__device__ __forceinline__ void apply_gate(const F2 (&z)[P], int act, F2 (&x)[P]) {
     F2 t, s;
-    logistic2(z, t, s);
-    return act == GDN_ACT_SILU ? mul2(z, s) : s;
-}
-// act(z) and its derivative
-__device__ __forceinline__ F2 gate_of(F2 z, int act, F2& slope) {
-    F2 t, s;
-    logistic2(z, t, s);
-    const F2 s1 = mul2(t, s);                          // 1 - s
     if (act == GDN_ACT_SILU) {
-        slope = mul2(s, fma2(z, s1, both(1.f)));
-        return mul2(z, s);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            logistic2(z[i], t, s);
+            x[i] = mul2(x[i], mul2(z[i], s));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            logistic2(z[i], t, s);
+            x[i] = mul2(x[i], s);
+        }
     }
-    slope = mul2(s, s1);
-    return s;
+}
+// du, n -> dn = du act(z) (in du) and dz = du n act'(z) (in z)
+template <int P>
+__device__ __forceinline__ void gate_gradient(F2 (&z)[P], int act, const F2 (&n)[P], F2 (&du)[P]) {
+    F2 t, s;
+    if (act == GDN_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            logistic2(z[i], t, s);
+            const F2 a = mul2(du[i], s);               // act' = s (1 + z (1 - s))
+            du[i] = mul2(a, z[i]);
+            z[i] = mul2(mul2(a, n[i]), fma2(z[i], mul2(t, s), both(1.f)));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            logistic2(z[i], t, s);
+            du[i] = mul2(du[i], s);                    // act' = s (1 - s)
+            z[i] = mul2(mul2(du[i], n[i]), mul2(t, s));
+        }
+    }
 }
 
 // Sum of N values over the threads of a row (tpr of them, a multiple of 32),
@@ -159,12 +170,13 @@ __device__ __forceinline__ float head_sum(float x) {
     return x;
 }
 
-// offset of channel e of a row of y (rows are below 2^31)
-__device__ __forceinline__ int64_t y_at(const NormArgs& p, const gdn_strides& s, int64_t row,
-                                        int e) {
+// offset of a row of y (rows are below 2^31), and of its channel e in the row
+__device__ __forceinline__ int64_t y_row(const NormArgs& p, const gdn_strides& s, int64_t row) {
     const uint32_t T32 = (uint32_t)p.T, b = (uint32_t)row / T32, t = (uint32_t)row - b * T32;
-    const int h = p.H == 1 ? 0 : e >> 7, c = p.H == 1 ? e : e & 127;
-    return b * s.b + h * s.h + t * s.t + c;
+    return b * s.b + t * s.t;
+}
+__device__ __forceinline__ int64_t y_in(const NormArgs& p, const gdn_strides& s, int e) {
+    return p.H == 1 ? e : (e >> 7) * s.h + (e & 127);
 }
 
 // 1 / rms_d of y, by vector (H > 1) or for the row; 1 without a post norm
@@ -203,13 +215,14 @@ __global__ void __launch_bounds__(MAXT) k_block_norm(const NormArgs p) {
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y, rows = p.B * p.T;
     uint4 y[V], z[V], r[V];
     bool ok[V];
+    const T* const yr = (const T*)p.Y + y_row(p, p.ys, row);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int at = E * (threadIdx.x + k * tpr);
         ok[k] = at < W && row < rows;
         y[k] = z[k] = r[k] = make_uint4(0, 0, 0, 0);
         if (!ok[k]) continue;
-        y[k] = *reinterpret_cast<const uint4*>((const T*)p.Y + y_at(p, p.ys, row, at));
+        y[k] = *reinterpret_cast<const uint4*>(yr + y_in(p, p.ys, at));
         if (p.Z) z[k] = *reinterpret_cast<const uint4*>((const T*)p.Z + row * W + at);
         if (p.R) r[k] = *reinterpret_cast<const uint4*>((const T*)p.R + row * W + at);
     }
@@ -229,8 +242,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm(const NormArgs p) {
         for (int i = 0; i < P; ++i) yv[i] = mul2(mul2(yv[i], a), w[i]);
         if (p.Z) {
             unpack(z[k], zv);
-#pragma unroll
-            for (int i = 0; i < P; ++i) yv[i] = mul2(yv[i], gate_of(zv[i], p.act));
+            apply_gate(zv, p.act, yv);
         }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -256,7 +268,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm(const NormArgs p) {
     }
 }
 
-template <typename T, int V, int MAXT>
+template <typename T, int V, int MAXT, bool AHEAD>
 __global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) {
     constexpr int E = kE<T>;
     extern __shared__ __align__(16) float red[];
@@ -268,23 +280,65 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) 
     for (int k = 0; k < V; ++k)
 #pragma unroll
         for (int i = 0; i < P; ++i) dwo[k][i] = dwi[k][i] = both(0.f);
+    // The next row's vectors come into shared memory (a thread's own places, so
+    // no barrier) while a row is reduced; two sets in turn.
+    uint4* const ahead =
+        reinterpret_cast<uint4*>(red + ((3 * span + (blockDim.y - 1) * 2 * W + 3) & ~3));
+    const int threads = tpr * blockDim.y, me = threadIdx.y * tpr + threadIdx.x;
+    auto fetch = [&](int64_t row, int set) {
+        const T* const yr = (const T*)p.Y + y_row(p, p.ys, row);
+        const void* const src[5] = {p.Y, p.Z, p.R, p.dX, p.dN};
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int at = E * (threadIdx.x + k * tpr);
+            const bool ok = at < W && row < rows;
+#pragma unroll
+            for (int j = 0; j < 5; ++j)
+                if (src[j]) {
+                    const T* g = (const T*)src[j];
+                    if (ok) g = j == 0 ? yr + y_in(p, p.ys, at) : g + row * W + at;
+                    const uint32_t to = (uint32_t)__cvta_generic_to_shared(
+                        ahead + ((set * 5 + j) * V + k) * threads + me);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(g),
+                                 "r"(ok ? 16 : 0)
+                                 : "memory");          // zeros where there is no channel
+                }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int set = 0;
+    if (AHEAD) fetch((int64_t)blockIdx.x * blockDim.y + threadIdx.y, 0);
     for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < rows; base += step) {
         const int64_t row = base + threadIdx.y;        // every thread takes every barrier
         uint4 y[V], z[V], r[V], gx[V], gn[V];
         bool ok[V];
+        if (AHEAD) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            fetch(row + step, set ^ 1);
+        }
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int at = E * (threadIdx.x + k * tpr);
             const int64_t e = row * W + at;
             ok[k] = at < W && row < rows;
             y[k] = z[k] = r[k] = gx[k] = gn[k] = make_uint4(0, 0, 0, 0);
-            if (!ok[k]) continue;
-            y[k] = *reinterpret_cast<const uint4*>((const T*)p.Y + y_at(p, p.ys, row, at));
-            if (p.Z) z[k] = *reinterpret_cast<const uint4*>((const T*)p.Z + e);
-            if (p.R) r[k] = *reinterpret_cast<const uint4*>((const T*)p.R + e);
-            if (p.dX) gx[k] = *reinterpret_cast<const uint4*>((const T*)p.dX + e);
-            if (p.dN) gn[k] = *reinterpret_cast<const uint4*>((const T*)p.dN + e);
+            if (AHEAD) {
+                const uint4* a = ahead + (set * 5 * V + k) * threads + me;
+                y[k] = a[0];
+                if (p.Z) z[k] = a[V * threads];
+                if (p.R) r[k] = a[2 * V * threads];
+                if (p.dX) gx[k] = a[3 * V * threads];
+                if (p.dN) gn[k] = a[4 * V * threads];
+            } else if (ok[k]) {
+                y[k] = *reinterpret_cast<const uint4*>((const T*)p.Y + y_row(p, p.ys, row) +
+                                                       y_in(p, p.ys, at));
+                if (p.Z) z[k] = *reinterpret_cast<const uint4*>((const T*)p.Z + e);
+                if (p.R) r[k] = *reinterpret_cast<const uint4*>((const T*)p.R + e);
+                if (p.dX) gx[k] = *reinterpret_cast<const uint4*>((const T*)p.dX + e);
+                if (p.dN) gn[k] = *reinterpret_cast<const uint4*>((const T*)p.dN + e);
+            }
         }
+        set ^= 1;
         float ry[V];
         post_scale<V, E>(p, y, ry, red, tpr);
         F2 x[V][P];                                    // x, then e
@@ -303,8 +357,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) 
             for (int i = 0; i < P; ++i) yv[i] = mul2(mul2(yv[i], a), w[i]);
             if (p.Z) {
                 unpack(z[k], zv);
-#pragma unroll
-                for (int i = 0; i < P; ++i) yv[i] = mul2(yv[i], gate_of(zv[i], p.act));
+                apply_gate(zv, p.act, yv);
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) x[k][i] = add2(x[k][i], yv[i]);
@@ -350,15 +403,11 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) 
                 dx[i] = mul2(dx[i], both(p.scale));    // du
             }
             if (p.Z) {
-                F2 zv[P];
+                F2 zv[P], n[P];
                 unpack(z[k], zv);
 #pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    F2 slope;
-                    const F2 g = gate_of(zv[i], p.act, slope);
-                    zv[i] = mul2(mul2(dx[i], mul2(yv[i], w[i])), slope);   // dz
-                    dx[i] = mul2(dx[i], g);            // dn
-                }
+                for (int i = 0; i < P; ++i) n[i] = mul2(yv[i], w[i]);
+                gate_gradient(zv, p.act, n, dx);       // dn
                 if (ok[k]) *reinterpret_cast<uint4*>((T*)p.dZ + e) = pack(zv);
             }
             F2 s = both(0.f);
@@ -372,6 +421,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) 
             all[0] += eh[k];
         }
         if (p.w_post && p.H == 1) row_sums<1>(all, red + 2 * span, tpr);
+        T* const dyr = (T*)p.dY + y_row(p, p.dys, row);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int at = E * (threadIdx.x + k * tpr);
@@ -383,8 +433,7 @@ __global__ void __launch_bounds__(MAXT) k_block_norm_backward(const NormArgs p) 
 #pragma unroll
                 for (int i = 0; i < P; ++i) x[k][i] = mul2(a, fma2(yv[i], b, x[k][i]));
             }
-            if (ok[k])
-                *reinterpret_cast<uint4*>((T*)p.dY + y_at(p, p.dys, row, at)) = pack(x[k]);
+            if (ok[k]) *reinterpret_cast<uint4*>(dyr + y_in(p, p.dys, at)) = pack(x[k]);
         }
         // a sum's buffer is next written behind another sum's barrier when two
         // or three are present, else behind this one
@@ -467,7 +516,7 @@ NormShape norm_shape(int64_t rows, int64_t W, int e, int most, int wide) {
     s.rpc = s.tpr >= 128 ? 1 : 128 / s.tpr;
     return s;
 }
-constexpr int kForwardV = 4, kBackwardV = 2;           // where rows are many
+constexpr int kForwardV = 2, kBackwardV = 2;           // where rows are many
 constexpr int kForwardWide = 8, kBackwardWide = 4;     // where rows are wide
 
 // CTAs of the backward pass, whatever the data type (the workspace's size goes by it)
@@ -483,11 +532,22 @@ void run_norm(const NormArgs& a, const NormShape& s, cudaStream_t st) {
     k_block_norm<T, V, MAXT><<<(unsigned)ctas, dim3(s.tpr, s.rpc), smem, st>>>(a);
 }
 template <typename T, int V, int MAXT>
-void run_norm_backward(const NormArgs& a, const NormShape& s, cudaStream_t st) {
-    const int W = (int)(a.H * a.d);
-    const int smem = (3 * 2 * s.rpc * (s.tpr / 32) + (s.rpc - 1) * 2 * W) * (int)sizeof(float);
-    k_block_norm_backward<T, V, MAXT>
-        <<<(unsigned)backward_ctas(a.B * a.T), dim3(s.tpr, s.rpc), smem, st>>>(a);
+cudaError_t run_norm_backward(const NormArgs& a, const NormShape& s, cudaStream_t st) {
+    const int W = (int)(a.H * a.d), threads = s.tpr * s.rpc;
+    int smem = (3 * 2 * s.rpc * (s.tpr / 32) + (s.rpc - 1) * 2 * W) * (int)sizeof(float);
+    // rows ahead where three CTAs still share an SM's 227 KB (16384 x 2048 bf16:
+    // 40 KB each); with wider rows those in registers are enough to load
+    const int ahead = ((smem + 15) & ~15) + 2 * 5 * V * threads * 16;
+    const dim3 grid((unsigned)backward_ctas(a.B * a.T)), block(s.tpr, s.rpc);
+    if (ahead > 75 * 1024) {
+        k_block_norm_backward<T, V, MAXT, false><<<grid, block, smem, st>>>(a);
+        return cudaGetLastError();
+    }
+    cudaError_t e = cudaFuncSetAttribute(k_block_norm_backward<T, V, MAXT, true>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 75 * 1024);
+    if (e != cudaSuccess) return e;
+    k_block_norm_backward<T, V, MAXT, true><<<grid, block, ahead, st>>>(a);
+    return cudaGetLastError();
 }
 template <typename T>
 void norm_forward(const NormArgs& a, cudaStream_t st) {
@@ -498,12 +558,12 @@ void norm_forward(const NormArgs& a, cudaStream_t st) {
     else run_norm<T, 8, 512>(a, s, st);
 }
 template <typename T>
-void norm_backward(const NormArgs& a, cudaStream_t st) {
+cudaError_t norm_backward(const NormArgs& a, cudaStream_t st) {
     const NormShape s = norm_shape(a.B * a.T, a.H * a.d, kE<T>, kBackwardV, kBackwardWide);
-    if (s.v == 1) run_norm_backward<T, 1, 512>(a, s, st);
-    else if (s.v == 2) run_norm_backward<T, 2, 512>(a, s, st);
-    else if (s.tpr <= 256) run_norm_backward<T, 4, 256>(a, s, st);
-    else run_norm_backward<T, 4, 1024>(a, s, st);
+    if (s.v == 1) return run_norm_backward<T, 1, 512>(a, s, st);
+    if (s.v == 2) return run_norm_backward<T, 2, 512>(a, s, st);
+    if (s.tpr <= 256) return run_norm_backward<T, 4, 256>(a, s, st);
+    return run_norm_backward<T, 4, 1024>(a, s, st);
 }
 
 }  // namespace
@@ -519,9 +579,7 @@ cudaError_t launch_block_norm(const NormArgs& a, bool bf16, cudaStream_t st) {
 }
 
 cudaError_t launch_block_norm_backward(const NormArgs& a, bool bf16, cudaStream_t st) {
-    if (bf16) norm_backward<__nv_bfloat16>(a, st);
-    else norm_backward<float>(a, st);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = bf16 ? norm_backward<__nv_bfloat16>(a, st) : norm_backward<float>(a, st);
     if (e != cudaSuccess || !(a.dw_post || a.dw_pre)) return e;
     const int W = (int)(a.H * a.d);
     k_norm_dw<<<dim3((W + 31) / 32, 2), 1024, 0, st>>>(a.ws, a.dw_post, a.dw_pre, W,
