@@ -14,7 +14,8 @@
 // GPU mapping.  Bound by moving the rows: 16 lanes hold one row of 128 columns
 // (8 each), a CTA 16 tokens.  The angles of a token are the same for every
 // head, so a lane forms its 8 (4 if interleaved) sines and cosines once and
-// walks the heads with them, four rows in flight; heads are split over CTAs
+// walks the heads with them, four rows in flight (64 registers, so that four
+// CTAs share an SM: 1 GB of bf16 in 192 us, 202 at three); heads are split over CTAs
 // only when the tokens alone do not fill the GPU (one token per request).
 // The partner columns of the half layout come by shuffle from the lane that
 // holds them when rot is a multiple of 16, else by loads of the elements.
@@ -24,7 +25,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kRotCols = 128;
 constexpr int kRotTokens = 16;                         // tokens per CTA
 constexpr int kRotAhead = 4;                           // rows in flight per lane
 
@@ -94,7 +94,7 @@ struct Row8<float> {
 };
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kRotTokens * 16)
+__global__ void __launch_bounds__(kRotTokens * 16, sizeof(T) == 2 && MODE != kHalfOdd ? 4 : 1)
 k_rotary(const RotaryArgs p) {
     const int lane = threadIdx.x & 15;
     const int64_t n = (int64_t)blockIdx.x * kRotTokens + (threadIdx.x >> 4);
