@@ -149,6 +149,19 @@ int check_linear(const gdn_linear_shape& s, const int32_t* cu, gdn_dtype dtype) 
     return GDN_OK;
 }
 
+// Outputs that are an input (or one another) by pointer.
+int check_apart(std::initializer_list<std::pair<const void*, const char*>> outs,
+                std::initializer_list<std::pair<const void*, const char*>> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->first) continue;
+        for (auto& i : ins)
+            if (o->first == i.first) return fail(GDN_ERR_ARG, "%s is %s", o->second, i.second);
+        for (auto p = o + 1; p != outs.end(); ++p)
+            if (o->first == p->first) return fail(GDN_ERR_ARG, "%s is %s", p->second, o->second);
+    }
+    return GDN_OK;
+}
+
 // the packed or padded sequences of a call
 gdn::LinArgs linear_args(const gdn_linear_shape& s, const float* loggate, const int32_t* cu) {
     gdn::LinArgs a;
@@ -572,6 +585,9 @@ int gdn_linear_forward(const void* Q, const void* K, const void* V, const float*
     GDN_TRY(check_vec(loggate, 4, "loggate"));
     GDN_TRY(check_opt_ptr(S0, "S0"));
     GDN_TRY(check_opt_ptr(S_final, "S_final"));
+    if (s.T > 0)
+        GDN_TRY(check_apart({{O, "O"}, {S_final, "S_final"}},
+                            {{Q, "Q"}, {K, "K"}, {V, "V"}, {S0, "S0"}}));
     const gdn::LinPlan pl = gdn::linear_plan(s, 1, dtype == GDN_BF16);
     if (workspace_bytes < pl.state_bytes)
         return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
@@ -608,6 +624,10 @@ int gdn_linear_backward(const void* Q, const void* K, const void* V, const float
     GDN_TRY(check_opt_ptr(S0, "S0"));
     GDN_TRY(check_opt_ptr(dS_final, "dS_final"));
     GDN_TRY(check_opt_ptr(dS0, "dS0"));
+    if (s.T > 0)
+        GDN_TRY(check_apart({{dQ, "dQ"}, {dK, "dK"}, {dV, "dV"}, {dS0, "dS0"}},
+                            {{Q, "Q"}, {K, "K"}, {V, "V"}, {S0, "S0"}, {dO, "dO"},
+                             {dS_final, "dS_final"}}));
     const int64_t need = gdn_linear_backward_workspace_bytes(s, dtype);
     if (workspace_bytes < need)
         return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
@@ -658,6 +678,7 @@ int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* 
     GDN_TRY(check_ptrs({{Q, "Q"}, {K, "K"}, {V, "V"}, {S, "S"}, {O, "O"}}));
     GDN_TRY(check_vec(loggate, 4, "loggate"));
     GDN_TRY(check_vec(slots, 4, "slots", true));
+    GDN_TRY(check_apart({{O, "O"}, {S, "S"}}, {{Q, "Q"}, {K, "K"}, {V, "V"}}));
     return launched(gdn::launch_linear_decode(Q, K, V, loggate, S, slots, nslots, scale, O, B, Hk,
                                               Hv, n, dtype == GDN_BF16, (cudaStream_t)stream),
                     "linear decode");

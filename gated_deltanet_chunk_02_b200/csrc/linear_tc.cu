@@ -40,6 +40,10 @@
 // status word is set and all roles leave.
 //
 // k_linear_state_tc is step 1: the state part alone, always with three parts.
+//
+// One B200, bf16, graph replay: 65536 tokens of 16 heads in 9 segments a head:
+// state pass 110 us (4.9 TB/s), outputs 195 us (5.5 TB/s), 306 us together;
+// batch 4 of 16 heads x 4096 tokens backward 217 us.
 #include <cstddef>
 #include <cstring>
 
@@ -67,7 +71,7 @@ struct __align__(16) LtCtrl {
     __align__(16) float pw[kRows];                     // s lambda^n
     __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
     // by row, for whole chunks [0] and for the segment's last rows [1]: the
-    // weight of b, d; and lambda^n as a sum of two floats
+    // weight of c, d; and lambda^n as a sum of two floats
     float w[2][kRows], d[2][kRows];
     float an[2], an_lo[2], lambda;
     uint32_t tmem;
@@ -382,7 +386,8 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
                 ahead = __all_sync(0xffffffffu, mbar_test(&c->full[at.slot], at.phase) &&
                                                     mbar_test(&c->full[a1.slot], a1.phase) &&
                                                     mbar_test(&c->o, par));
-                if (*(volatile int*)ab) break;         // the rows' own wait ran out
+                // the rows' own wait ran out
+                if (__any_sync(0xffffffffu, *(volatile int*)ab)) break;
             }
             if (ahead) {
                 tc_fence_after();

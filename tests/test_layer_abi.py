@@ -9,7 +9,7 @@ from gated_deltanet_chunk_02_b200 import build as B
 from gated_deltanet_chunk_02_b200 import gdn
 from oracle import layer_oracle as L
 
-FAKE, ODD = 0x10000, 0x10008       # never dereferenced: every call fails its checks first
+FAKE, OUT, ODD = 0x10000, 0x20000, 0x10008     # never dereferenced: every call fails its checks first
 BF16, F32 = gdn.GDN_BF16, gdn.GDN_F32
 
 
@@ -85,16 +85,17 @@ def shape(B=1, Hk=2, Hv=4, T=100, nseq=0, d=128):
     return gdn.GdnLinearShape(B, Hk, Hv, T, nseq, d)
 
 
-def forward(lib, q=FAKE, lg=FAKE, s0=None, cu=None, sf=FAKE, ws=None, wsb=1 << 40, s=None,
-            dtype=BF16):
-    return lib.gdn_linear_forward(P(q), P(FAKE), P(FAKE), P(lg), P(s0), P(cu), 1.0, P(FAKE), P(sf),
+def forward(lib, q=FAKE, lg=FAKE, s0=None, cu=None, out=OUT, sf=OUT + 64, ws=None, wsb=1 << 40,
+            s=None, dtype=BF16):
+    return lib.gdn_linear_forward(P(q), P(FAKE), P(FAKE), P(lg), P(s0), P(cu), 1.0, P(out), P(sf),
                                   P(ws), wsb, s or shape(), dtype, None)
 
 
-def backward(lib, dq=FAKE, cu=None, ws=None, wsb=1 << 40, s=None, ds0=None, dtype=BF16):
-    return lib.gdn_linear_backward(P(FAKE), P(FAKE), P(FAKE), P(FAKE), None, P(FAKE), None, P(cu),
-                                   1.0, P(dq), P(FAKE), P(FAKE), P(ds0), P(ws), wsb, s or shape(),
-                                   dtype, None)
+def backward(lib, dq=OUT, dk=OUT + 16, cu=None, ws=None, wsb=1 << 40, s=None, ds=None, ds0=None,
+             dtype=BF16):
+    return lib.gdn_linear_backward(P(FAKE), P(FAKE), P(FAKE), P(FAKE), None, P(FAKE), P(ds), P(cu),
+                                   1.0, P(dq), P(dk), P(OUT + 32), P(ds0), P(ws), wsb,
+                                   s or shape(), dtype, None)
 
 
 def test_linear_refusals(lib):
@@ -114,6 +115,11 @@ def test_linear_refusals(lib):
     for kw in [dict(q=ODD), dict(lg=FAKE + 2), dict(s0=ODD), dict(sf=ODD), dict(s=long, ws=ODD)]:
         assert forward(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
     assert backward(lib, dq=None) == gdn.GDN_ERR_ARG
+    # an output that is an input, or another output
+    for kw in [dict(out=FAKE), dict(sf=FAKE), dict(s0=OUT + 64), dict(sf=OUT)]:
+        assert forward(lib, **kw) == gdn.GDN_ERR_ARG and " is " in last(lib), kw
+    for kw in [dict(dq=FAKE), dict(dk=OUT), dict(ds=OUT + 64, ds0=OUT + 64)]:
+        assert backward(lib, **kw) == gdn.GDN_ERR_ARG and " is " in last(lib), kw
     assert backward(lib, ds0=ODD) == gdn.GDN_ERR_ALIGN
 
 
@@ -128,12 +134,13 @@ def test_linear_workspace_sizes(lib):
 
 
 def test_linear_decode_refusals(lib):
-    def call(q=FAKE, lg=FAKE, S=FAKE, slots=None, nslots=8, B=2, Hk=2, Hv=4, n=1, d=128,
+    def call(q=FAKE, lg=FAKE, S=OUT + 64, slots=None, nslots=8, B=2, Hk=2, Hv=4, n=1, d=128,
              dtype=BF16):
         return lib.gdn_linear_decode(P(q), P(FAKE), P(FAKE), P(lg), P(S), P(slots), nslots, 1.0,
-                                     P(FAKE), B, Hk, Hv, n, d, dtype, None)
+                                     P(OUT), B, Hk, Hv, n, d, dtype, None)
     for kw in [dict(q=None), dict(lg=None), dict(S=None), dict(nslots=1), dict(Hk=3), dict(Hk=0),
-               dict(n=-1), dict(B=65536), dict(dtype=9), dict(slots=FAKE, nslots=-1)]:
+               dict(n=-1), dict(B=65536), dict(dtype=9), dict(slots=FAKE, nslots=-1), dict(S=OUT),
+               dict(S=FAKE)]:
         assert call(**kw) == gdn.GDN_ERR_ARG, kw
     for kw in [dict(q=ODD), dict(S=ODD), dict(slots=FAKE + 2), dict(lg=FAKE + 2)]:
         assert call(**kw) == gdn.GDN_ERR_ALIGN, kw

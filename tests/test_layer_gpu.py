@@ -324,6 +324,43 @@ def test_linear_bad_bounds_are_reported(lib, cu):
     assert gdn.gdn_get_status() == gdn.GDN_ERR_ARG
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_packed_rows_start_late(lib, dtype):
+    """The first sequence need not start at row 0; the rows before it stay."""
+    T, at = 400, [130, 131, 131, 300]
+    c = linear_case(13, dtype, 1, 2, 4, T, [1, 0, 169], True)
+    c["cu"] = torch.tensor(at, dtype=torch.int32).cuda()
+    c["rows"] = [(0, 130, 1), (0, 131, 0), (0, 131, 169)]
+    O, S = run_forward(c, 0.7)
+    o, s = oracle_linear(c, 0.7)
+    om, sm = oracle_linear(c, 0.7, absolute=True)
+    near(S, s, state_tol(sm, dtype, T), "S")
+    used = slice(130, 300)
+    near(O[:, :, used], o[:, :, used], out_tol(o, om, dtype, T)[:, :, used], "O")
+    got = run_backward(c, 0.7)
+    want, mag = oracle_linear_grad(c, 0.7), oracle_linear_grad(c, 0.7, absolute=True)
+    for x, y, m, name in zip(got, want[:3], mag, ("dQ", "dK", "dV")):
+        near(x[:, :, used], y[:, :, used], out_tol(y, m, dtype, T)[:, :, used], name)
+    for x in (O, *got[:3]):
+        assert (x[:, :, :130] == 77.0).all() and (x[:, :, 300:] == 77.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_two_calls_at_once(lib, dtype):
+    """Two streams, a workspace each: the bits of the calls one after the other."""
+    cases = [linear_case(40 + i, dtype, 1, 1, 2, 2600, None, True) for i in range(2)]
+    want = [(*run_forward(c, 1.0), *run_backward(c, 1.0)) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for c, st in zip(cases, streams):
+        with torch.cuda.stream(st):
+            got.append((*run_forward(c, 1.0), *run_backward(c, 1.0)))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 # --------------------------------------------------------------------------- #
 # single tokens
 # --------------------------------------------------------------------------- #
@@ -506,6 +543,27 @@ def test_block_norm_backward(lib, dtype, act, parts, B, T, H, d, hm):
         assert torch.equal(c["dX"], dR)
         assert all(torch.equal(a, b) for a, b in zip(keep, [t for t in (dY, dZ, dwo, dwi)
                                                             if t is not None]))
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_block_norm_gate_at_its_ends(lib, act):
+    """Gates far out on both sides: one, or nothing, and slopes that vanish."""
+    z = torch.tensor([-1e30, -200.0, -88.0, -60.0, 60.0, 88.0, 200.0, 1e30]).cuda()[None, None]
+    y = torch.full((1, 1, 1, 8), 2.0, device="cuda")
+    g, X = torch.ones_like(z), torch.empty_like(z)
+    gdn.gdn_block_norm(y, z, None, None, None, X, None, act=act)
+    want, _ = L.block_norm(f64(y)[0], f64(z)[0], None, None, None, act=act)
+    assert np.allclose(f64(X)[0], want, rtol=1e-5, atol=1e-6)
+    dY, dZ = torch.empty_like(y), torch.empty_like(z)
+    gdn.gdn_block_norm_backward(y, z, None, None, None, g, None, dY, dZ, None, None, None, None,
+                                act=act)
+    dy, dz, *_ = L.block_norm_backward(f64(y)[0], f64(z)[0], None, None, None, f64(g)[0], None,
+                                       act=act)
+    assert np.allclose(f64(dY)[0, 0], dy, rtol=1e-5, atol=1e-6)
+    assert np.allclose(f64(dZ)[0], dz, rtol=1e-5, atol=1e-6)
+    z[...] = float("nan")
+    gdn.gdn_block_norm(y, z, None, None, None, X, None, act=act)
+    assert X.isnan().all()
 
 
 def test_block_norm_without_rows(lib):
