@@ -396,9 +396,10 @@ int gdn_rotary(const void* Q, gdn_strides qs, void* Q_out, gdn_strides qos, cons
  * bytes (it may be 0; of the current device, fixed by shape and dtype); calls
  * that may overlap need one each.  A bound outside the rule sets the status
  * word (gdn_get_status returns GDN_ERR_ARG) and that sequence is left out.
- * bf16 data: products of bf16 on the tensor cores with fp32 accumulation, the
- * state fp32 with its updates split into two bf16 parts (2^-17); weights and the
- * state as an operand of o are rounded to bf16.  f32 data: fp32 on CUDA cores.
+ * bf16 data: products of bf16 on the tensor cores with fp32 accumulation; the
+ * state is fp32 and returned to fp32 accuracy (its updates split into bf16
+ * parts); weights and the state as an operand of o are rounded to bf16.
+ * Sequences of up to 8 rows run in fp32.  f32 data: fp32 on CUDA cores.
  */
 int gdn_linear_forward(const void* Q, const void* K, const void* V, const float* loggate,
                        const float* S0, const int32_t* cu_seqlens, float scale, void* O,
