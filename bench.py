@@ -58,13 +58,13 @@ def load_peaks() -> tuple[dict, str]:
 
 
 KERNEL_SOURCES = {
-    "fused": ["tc.cu", "tc.h", "common.cuh"],
-    "neumann": ["tc.cu", "tc.h", "common.cuh"],
-    "int8": ["tc.cu", "tc.h", "common.cuh"],
-    "build_A": ["tc.cu", "tc.h", "common.cuh"],
-    "wy": ["tc.cu", "tc.h", "common.cuh"],
+    "fused": ["tc.cu", "tc.h", "tc_ptx.cuh", "common.cuh"],
+    "neumann": ["tc.cu", "tc.h", "tc_ptx.cuh", "common.cuh"],
+    "int8": ["tc.cu", "tc.h", "tc_ptx.cuh", "common.cuh"],
+    "build_A": ["tc.cu", "tc.h", "tc_ptx.cuh", "common.cuh"],
+    "wy": ["tc.cu", "tc.h", "tc_ptx.cuh", "common.cuh"],
     "fwdsub": ["simt.cu", "kernels.h", "common.cuh"],
-    "forward": ["tc.cu", "scan.cu", "simt.cu", "common.cuh"],
+    "forward": ["tc.cu", "tc_ptx.cuh", "scan.cu", "simt.cu", "common.cuh"],
 }
 
 
