@@ -141,7 +141,8 @@ int check_linear(const gdn_linear_shape& s, const int32_t* cu, gdn_dtype dtype) 
     if (s.Hv > 8192) return fail(GDN_ERR_ARG, "Hv=%lld above 8192", (long long)s.Hv);
     if (s.nseq > 0 && s.B != 1) return fail(GDN_ERR_ARG, "packed sequences need B=1");
     if (s.T > kMaxRows || s.B > kMaxRows || s.nseq > kMaxRows ||
-        s.B * s.Hv > kMaxRows || s.nseq * s.Hv > kMaxRows || s.T * 32 > kMaxRows * 8 / s.Hv / s.B)
+        s.B * s.Hv > kMaxRows / 16 || s.nseq * s.Hv > kMaxRows / 16 ||   // 12 blocks each
+        s.T * 32 > kMaxRows * 8 / s.Hv / s.B)
         return fail(GDN_ERR_ARG, "too many rows (B=%lld, Hv=%lld, T=%lld, nseq=%lld)",
                     (long long)s.B, (long long)s.Hv, (long long)s.T, (long long)s.nseq);
     if (s.nseq > 0) return check_vec(cu, 4, "cu_seqlens");

@@ -25,11 +25,12 @@ constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p) {
     const LinProblem& q = p.pr[blockIdx.z];
     if (q.ws_t) return;
-    const int64_t seq = blockIdx.x / p.Hv;
-    const int hv = (int)(blockIdx.x - seq * p.Hv);
+    // blockIdx.x: (sequence, head), past those that are whole
+    const int64_t seq = (p.whole + blockIdx.x) / p.Hv;
+    const int hv = (int)(p.whole + blockIdx.x - seq * p.Hv);
     LinSeg g;
     if (p.cu) {
-        // the sequence's first slot: boundaries of the sequences before it
+        // the sequence's first boundary: those of the sequences before it
         const int lane = threadIdx.x & 31;
         int64_t slots = 0, t0, n;
         lin_bounds(p, seq, t0, n);
@@ -41,15 +42,19 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) slots += __shfl_xor_sync(0xffffffffu, slots, o);
         lin_bounds(p, seq, t0, n);
-        g.slot0 = slots;
+        g.st0 = slots * p.Hv + hv;
+        g.st_step = p.Hv;
         g.seq_n = n;
         g.m = (int)lin_segments(n, p.seg_len);
+        if ((slots + g.m - 1) * p.Hv > p.bounds) return;
     } else {
         g.seq_n = p.T;
         g.m = (int)lin_segments(p.T, p.seg_len);
-        g.slot0 = seq * (g.m - 1);
+        g.st0 = blockIdx.x * (int64_t)(g.m - 1);
+        g.st_step = 1;
+        if (g.st0 + g.m - 1 > p.bounds) return;
     }
-    if (g.m < 2 || g.slot0 + g.m - 1 > p.bounds) return;
+    if (g.m < 2) return;
     const double lg = lin_log2(p.loggate, hv);
     const float a_full = lin_pow(lg, p.seg_len);
     const float a_last = lin_pow(lg, g.seq_n - (g.m - 1) * p.seg_len);
@@ -68,8 +73,8 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
                                 s[(c + 3) * kLinD + r]);
             }
         }
-        float4* const base = reinterpret_cast<float4*>(q.ws + (g.slot0 * p.Hv + hv) * kLinState + e);
-        const int64_t step = p.Hv * kLinState / 4;
+        float4* const base = reinterpret_cast<float4*>(lin_boundary(q, g, 0) + e);
+        const int64_t step = g.st_step * kLinState / 4;
         constexpr int kAhead = 8;                      // loads in flight
         for (int i0 = 0; i0 < g.m - 1; i0 += kAhead) {
             float4 u[kAhead];
@@ -157,8 +162,7 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
         if (!STATE_ONLY) {
             const bool first = REV ? g.k == g.m - 1 : g.k == 0;
             if (!first) {
-                const int64_t slot = g.slot0 + (REV ? g.k : g.k - 1);
-                const float* src = q.ws + (slot * p.Hv + hv) * kLinState;
+                const float* src = lin_boundary(q, g, REV ? g.k : g.k - 1);
                 m = q.ws_t ? src[c * kLinD + v0 + r] : src[(v0 + r) * kLinD + c];
             } else if (q.m0) {
                 const float* src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
@@ -336,44 +340,33 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
     __syncthreads();
     // a sequence of several segments has its outgoing state from steps 1 and 2
     float* dst = nullptr;
-    if (STATE_ONLY) dst = lin_added(p, q, g, hv);
+    if (STATE_ONLY) dst = lin_added(p, q, g);
     else if (q.mout && g.m == 1) dst = q.mout + (g.seq * p.Hv + hv) * kLinState;
     if (dst)
         for (int e = tid; e < kSimtDV * kLinD; e += kSimtThreads)
             dst[v0 * kLinD + e] = s.m[e / kLinD][e % kLinD];
 }
 
-// grid: (segments (of sequences that have several), 4 Hv, problems)
+// four blocks, of 32 state rows each, for every one of lin_find's
 template <bool STATE_ONLY>
 __global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtSmem& s = *reinterpret_cast<SimtSmem*>(raw);
-    const LinProblem& q = p.pr[blockIdx.z];
-    if (STATE_ONLY && q.ws_t) return;
-    const LinSeg g = lin_find(p, blockIdx.x, STATE_ONLY ? kCutSegments : kAllSegments);
+    const LinSeg g = lin_find(p, blockIdx.x >> 2, STATE_ONLY ? kCutSegments : kAllSegments);
     if (!g.ok) return;
-    const int hv = blockIdx.y >> 2, v0 = (blockIdx.y & 3) * kSimtDV;
-    if (STATE_ONLY && !lin_added(p, q, g, hv)) return;
+    const LinProblem& q = p.pr[g.z];
+    if (STATE_ONLY && (q.ws_t || !lin_added(p, q, g))) return;
+    const int hv = g.hv, v0 = (blockIdx.x & 3) * kSimtDV;
     if (q.reverse) simt_segment<STATE_ONLY, true>(p, q, g, hv, v0, s);
     else simt_segment<STATE_ONLY, false>(p, q, g, hv, v0, s);
 }
 
-cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t cut_segs, bool states,
-                     cudaStream_t st) {
+cudaError_t run_simt(const LinArgs& a, int64_t blocks, bool states, cudaStream_t st) {
     const int smem = (int)sizeof(SimtSmem);
-    if (states) {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<true>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        k_linear_simt<true><<<dim3((unsigned)cut_segs, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
-                                 smem, st>>>(a);
-    } else {
-        cudaError_t e = cudaFuncSetAttribute(k_linear_simt<false>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        k_linear_simt<false><<<dim3((unsigned)segs, (unsigned)(4 * a.Hv), nprob), kSimtThreads,
-                                  smem, st>>>(a);
-    }
+    const auto kernel = states ? k_linear_simt<true> : k_linear_simt<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(4 * blocks), kSimtThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -381,28 +374,39 @@ cudaError_t run_simt(const LinArgs& a, int nprob, int64_t segs, int64_t cut_segs
 // step (a chunk of 128 rows on one SM): a chunk of the state pass takes one, a
 // CTA's start two in step 3 and one in step 1, the state at a boundary moves as
 // much as two output steps, and two more launches cost eight.
-// Sequences of one length are taken in waves: one segment each when that fills
-// the GPU, else the cut with the least cost.
-int64_t pick_segment(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows, int ctas_per_head) {
-    const int64_t chunks = (rows + 127) / 128, sms = sm_count();
-    const int64_t lines = nprob * nseq * Hv;
-    int64_t best = chunks, cost = INT64_MAX;
-    for (int64_t m = 1; m <= chunks && m <= 128; ++m) {
-        const int64_t len = (chunks + m - 1) / m;
-        if ((chunks + len - 1) / len != m) continue;   // the same cut with fewer pieces is listed
-        const int64_t waves = (lines * ctas_per_head * m + sms - 1) / sms;
-        const int64_t waves1 = (lines * ctas_per_head * m + sms - 1) / sms;
-        const int64_t c = waves * (2 * len + 2) +
-                          (m > 1 ? waves1 * (len + 1) + 4 * lines * (m - 1) / sms + 8 : 0);
-        if (c < cost) { cost = c; best = len; }
+// Sequences of one length are taken in waves: either all are cut alike (or not
+// at all), or as many as fill whole waves stay whole, and the others' pieces
+// follow as SMs come free.  64 heads x 4096 tokens backward (bf16) are 192
+// lines on 148 SMs: 223 us in two waves, 198 us with 45 of them cut at 8 chunks,
+// 215 us with all of them cut at 16.
+struct LinCut {
+    int64_t len, whole;
+};
+LinCut pick_segment(int64_t nprob, int64_t units, int64_t rows, int ctas_per_head) {
+    const int64_t chunks = (rows + 127) / 128, sms = sm_count(), unit = nprob * ctas_per_head;
+    const int64_t full = units * unit / sms;
+    LinCut best{chunks, units};
+    int64_t cost = (units * unit + sms - 1) / sms * (2 * chunks + 2);
+    for (int64_t w = 0; w <= full; w += full > 0 ? full : 1) {
+        const int64_t whole = w * sms / unit, cut = units - whole;
+        for (int64_t m = 2; m <= chunks && m <= 128 && cut > 0; ++m) {
+            const int64_t len = (chunks + m - 1) / m;
+            if ((chunks + len - 1) / len != m) continue;   // the same cut with fewer pieces is listed
+            const int64_t pieces = cut * unit * m, each = 3 * len + 3;
+            const int64_t run = w > 0 ? w * (2 * chunks + 2) + pieces * each / sms + 3 * len / 2
+                                      : (pieces + sms - 1) / sms * each;
+            const int64_t c = run + 4 * cut * unit * (m - 1) / sms + 8;
+            if (c < cost) { cost = c; best = {len, whole}; }
+        }
     }
-    return best < 1 ? 128 : 128 * best;
+    return {best.len < 1 ? 128 : 128 * best.len, best.whole};
 }
 // Packed sequences have lengths that the host does not know.  Cut: all chunks
 // spread over the SMs, half of a last segment behind them.  Not cut: that, or
-// the longest sequence, taken to be half of the rows if there are several (73
-// chunks of 32 heads, the longest 32: 153 us not cut, and 153 to 163 us cut at
-// 6 to 16, 195 us at 3).
+// the longest sequence, taken to be half of the rows if there are several; its
+// one piece returns a state, which takes a product more per chunk, hence 9/8 (73
+// chunks of 32 heads, the longest 32: 125 us not cut, 127 to 141 us cut at 16
+// to 8, 173 us at 4).
 int64_t pick_segment_packed(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows,
                             int ctas_per_head) {
     const int64_t chunks = (rows + 127) / 128, sms = sm_count();
@@ -410,7 +414,7 @@ int64_t pick_segment_packed(int64_t nprob, int64_t nseq, int64_t Hv, int64_t row
     const int64_t longest = nseq > 1 ? (chunks + 1) / 2 : chunks;
     const int64_t work = 2 * heads * (chunks + nseq) / sms;
     int64_t best = chunks;
-    int64_t cost = (work > 2 * longest ? work : 2 * longest) * 5 / 4 + 2 * heads * nseq / sms;
+    int64_t cost = (work > 2 * longest ? work : 2 * longest) * 9 / 8 + 2 * heads * nseq / sms;
     for (int64_t len = 1; len < longest; len += len < 16 ? 1 : len / 8) {
         const int64_t m = (chunks + len - 1) / len;    // segments of the cut ones
         const int64_t c = work + len + 2 * heads * (m + nseq) / sms + heads * (chunks + m) / sms +
@@ -424,24 +428,37 @@ int64_t pick_segment_packed(int64_t nprob, int64_t nseq, int64_t Hv, int64_t row
 
 LinPlan linear_plan(const gdn_linear_shape& s, int nprob, bool bf16) {
     LinPlan pl;
-    const bool packed = s.nseq > 0;
     // on CUDA cores four CTAs share a head, two to an SM
-    pl.seg_len = packed ? pick_segment_packed(nprob, s.nseq, s.Hv, s.T, bf16 ? 1 : 2)
-                        : pick_segment(nprob, s.B, s.Hv, s.T, bf16 ? 1 : 2);
-    // boundaries: a sequence of n rows has at most n / seg_len
-    const int64_t m = s.T <= pl.seg_len ? 1 : (s.T + pl.seg_len - 1) / pl.seg_len;
-    pl.bounds = packed ? (s.T <= pl.seg_len ? 0 : s.T / pl.seg_len) : s.B * (m - 1);
-    pl.segs = packed ? s.nseq + pl.bounds : s.B * m;
-    const int64_t cut = packed ? (s.nseq < pl.bounds ? s.nseq : pl.bounds) : s.B;
-    pl.cut_segs = m > 1 ? pl.bounds + cut : 0;         // each cut sequence has one more segment
-    pl.state_bytes = pl.bounds * s.Hv * kLinState * 4;
+    const int per = bf16 ? 1 : 2;
+    if (s.nseq > 0) {
+        pl.seg_len = pick_segment_packed(nprob, s.nseq, s.Hv, s.T, per);
+        // a sequence of n rows has at most n / seg_len boundaries, and a segment more
+        const int64_t m = s.T <= pl.seg_len ? 0 : s.T / pl.seg_len;
+        pl.whole = 0;
+        pl.units = s.nseq * s.Hv;
+        pl.bounds = m * s.Hv;
+        pl.blocks = (s.nseq + m) * s.Hv * nprob;
+        pl.cut_blocks = (m + (s.nseq < m ? s.nseq : m)) * s.Hv * nprob;
+    } else {
+        const LinCut cut = pick_segment(nprob, s.B * s.Hv, s.T, per);
+        pl.seg_len = cut.len;
+        pl.whole = cut.whole;
+        pl.units = s.B * s.Hv - cut.whole;
+        const int64_t m = s.T <= pl.seg_len ? 1 : (s.T + pl.seg_len - 1) / pl.seg_len;
+        pl.bounds = pl.units * (m - 1);
+        pl.cut_blocks = m > 1 ? pl.units * m * nprob : 0;
+        pl.blocks = (pl.whole + pl.units * m) * nprob;
+    }
+    pl.state_bytes = pl.bounds * kLinState * 4;
     return pl;
 }
 
 cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool bf16, void* ws,
                           int* launches, cudaStream_t st) {
     LinArgs a = a0;
+    a.nprob = nprob;
     a.seg_len = pl.seg_len;
+    a.whole = pl.whole;
     a.bounds = pl.bounds;
     a.status = status_ptr();
     uint8_t* at = (uint8_t*)ws;
@@ -456,18 +473,18 @@ cudaError_t launch_linear(const LinArgs& a0, int nprob, const LinPlan& pl, bool 
     cudaError_t e;
     if (pl.bounds > 0) {
         e = bf16 ? launch_linear_tc(a, nprob, pl, true, st)
-                 : run_simt(a, nprob, pl.segs, pl.cut_segs, true, st);
+                 : run_simt(a, pl.cut_blocks, true, st);
         if (e != cudaSuccess) return e;
         // blocks for four to an SM: of packed sequences many have nothing to do here
         int parts = 16;
-        while (parts > 1 && a.nseq * a.Hv * parts > 4LL * sm_count()) parts /= 2;
-        k_lin_combine<<<dim3((unsigned)(a.nseq * a.Hv), parts, nprob), kCombineThreads, 0, st>>>(a);
+        while (parts > 1 && pl.units * parts > 4LL * sm_count()) parts /= 2;
+        k_lin_combine<<<dim3((unsigned)pl.units, parts, nprob), kCombineThreads, 0, st>>>(a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         *launches += 2;
     }
     e = bf16 ? launch_linear_tc(a, nprob, pl, false, st)
-             : run_simt(a, nprob, pl.segs, pl.cut_segs, false, st);
+             : run_simt(a, pl.blocks, false, st);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -298,7 +298,7 @@ struct LtWalk {                                        // chunks of a segment, i
 
 __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g, int hv,
                         const LtWalk& wk, uint8_t* smem, LtCtrl* c) {
-    const int z = blockIdx.z;
+    const int z = g.z;
     const CUtensorMap *mb = &k.map[k.ib[z]], *ma = &k.map[k.ia[z]], *mc = &k.map[k.ic[z]];
     const int yb = lt_row0(k.a, g, hv, q.gb), ya = lt_row0(k.a, g, hv, q.ga),
               yc = lt_row0(k.a, g, hv, q.gc);
@@ -618,7 +618,7 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
         const float* src = nullptr;
         bool across = false;
         if (!first) {
-            src = q.ws + ((g.slot0 + (wk.rev ? g.k : g.k - 1)) * p.Hv + hv) * kLinState;
+            src = lin_boundary(q, g, wk.rev ? g.k : g.k - 1);
             across = q.ws_t != 0;
         } else if (q.m0) {
             src = q.m0 + (g.seq * p.Hv + hv) * kLinState;
@@ -733,7 +733,7 @@ __device__ void lt_short(const LinArgs& p, const LinProblem& q, const LinSeg& g,
     }
 }
 
-// grid: (segments, Hv, problems)
+// one block for each of lin_find's
 __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_constant__ LinTcArgs k) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const LinArgs& p = k.a;
@@ -741,14 +741,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         if (threadIdx.x == 0) raise_status(p.status, kStatusSmemAlign);
         return;
     }
-    const LinProblem& q = p.pr[blockIdx.z];
     const LinSeg g = lin_find(p, blockIdx.x, kAllSegments);
     if (!g.ok) return;
+    const LinProblem& q = p.pr[g.z];
     if (g.m == 1 && g.n <= kLtShort) {
-        lt_short(p, q, g, blockIdx.y);
+        lt_short(p, q, g, g.hv);
         return;
     }
-    const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + (kLtRing + 1) * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLtRing; ++i) {
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     } else if (warp == 17) {
         lt_multiply(wk, tiles, c, p.status);
     } else if (lane == 0) {
-        lt_store(wk, q, &k.out[blockIdx.z], (int)((g.b * p.Hv + hv) * p.T + g.t0), smem, c,
+        lt_store(wk, q, &k.out[g.z], (int)((g.b * p.Hv + hv) * p.T + g.t0), smem, c,
                  p.status);
     }
     __syncwarp();
@@ -839,7 +839,7 @@ struct __align__(16) LsCtrl {
 constexpr int kLsSmem = kLsRing * kLtTile + (int)sizeof(LsCtrl);
 static_assert(kLsSmem <= 232448, "shared memory budget");
 
-// grid: (segments of sequences that have several, Hv, problems)
+// one block for each of lin_find's, of the sequences that are cut
 __global__ void __launch_bounds__(kLsThreads, 1)
 k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -848,12 +848,12 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         if (threadIdx.x == 0) raise_status(p.status, kStatusSmemAlign);
         return;
     }
-    const LinProblem& q = p.pr[blockIdx.z];
-    if (q.ws_t) return;
     const LinSeg g = lin_find(p, blockIdx.x, kCutSegments);
     if (!g.ok) return;
-    const int hv = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* const dst = lin_added(p, q, g, hv);
+    const LinProblem& q = p.pr[g.z];
+    if (q.ws_t) return;
+    const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* const dst = lin_added(p, q, g);
     if (!dst) return;
     LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + kLsRing * kLtTile);
     if (threadIdx.x == 0) {
@@ -891,7 +891,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     int* const ab = &c->abort;
     if (warp == 16) {
         if (lane == 0) {
-            const int z = blockIdx.z;
+            const int z = g.z;
             const CUtensorMap *mb = &k.map[k.ib[z]], *mc = &k.map[k.ic[z]];
             const int yb = lt_row0(p, g, hv, q.gb), yc = lt_row0(p, g, hv, q.gc);
             Ring<kLsRing> at;
@@ -1032,13 +1032,13 @@ cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, boo
         e = cudaFuncSetAttribute(tcg::k_linear_state_tc,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, tcg::kLsSmem);
         if (e != cudaSuccess) return e;
-        tcg::k_linear_state_tc<<<dim3((unsigned)pl.cut_segs, (unsigned)a.Hv, nprob),
+        tcg::k_linear_state_tc<<<(unsigned)pl.cut_blocks,
                                  tcg::kLsThreads, tcg::kLsSmem, st>>>(k);
     } else {
         e = cudaFuncSetAttribute(tcg::k_linear_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  tcg::kLtSmem);
         if (e != cudaSuccess) return e;
-        tcg::k_linear_tc<<<dim3((unsigned)pl.segs, (unsigned)a.Hv, nprob), tcg::kLtThreads,
+        tcg::k_linear_tc<<<(unsigned)pl.blocks, tcg::kLtThreads,
                            tcg::kLtSmem, st>>>(k);
     }
     return cudaGetLastError();

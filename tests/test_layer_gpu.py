@@ -279,6 +279,42 @@ def test_linear_long_is_cut_into_segments(lib, dtype):
     near(state, s, state_tol(sm, dtype, T), "state handed over")
 
 
+def check_both_ways(c, dtype, T, forward=True, backward=True):
+    if forward:
+        O, S = run_forward(c, 0.7)
+        o, s = oracle_linear(c, 0.7)
+        om, sm = oracle_linear(c, 0.7, absolute=True)
+        near(S, s, state_tol(sm, dtype, T), "S")
+        near(O, o, out_tol(o, om, dtype, T), "O")
+    if backward:
+        got = run_backward(c, 0.7)
+        want, mag = oracle_linear_grad(c, 0.7), oracle_linear_grad(c, 0.7, absolute=True)
+        near(got[3], want[3], state_tol(mag[3], dtype, T), "dS0")
+        for x, y, m, name in zip(got, want, mag, ("dQ", "dK", "dV")):
+            near(x, y, out_tol(y, m, dtype, T), name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,backward", [(15, False), (5, True)])
+def test_linear_some_are_cut(lib, dtype, B, backward):
+    """Two lines more than one wave of 148 SMs takes: all but those stay whole."""
+    Hk, Hv, T = 5, 10, 1300
+    c = linear_case(7, dtype, B, Hk, Hv, T, None, True)
+    size = (gdn.gdn_linear_backward_workspace_bytes if backward
+            else gdn.gdn_linear_forward_workspace_bytes)(c["K"], c["V"])
+    parts = 2 * (B * Hv * T * 128) * 4 if backward else 0          # of shared heads' gradients
+    assert 0 < size - parts < B * Hv * 128 * 128 * 4
+    check_both_ways(c, dtype, T, forward=not backward, backward=backward)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[2] * 40 + [1400, 0, 257], [130] * 3 + [9] * 33 + [900, 450, 260, 1],
+                                  [0] * 35 + [1700]])
+def test_linear_packed_long_behind_short(lib, dtype, lens):
+    c = linear_case(8, dtype, 1, 1, 2, sum(lens), lens, True)
+    check_both_ways(c, dtype, sum(lens))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_linear_no_rows_and_no_memory(lib, dtype):
     c = linear_case(6, dtype, 2, 1, 2, 0, None, True)
