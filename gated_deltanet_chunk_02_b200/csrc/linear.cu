@@ -391,7 +391,7 @@ LinCut pick_segment(int64_t nprob, int64_t units, int64_t rows, int ctas_per_hea
         const int64_t whole = w * sms / unit, cut = units - whole;
         for (int64_t m = 2; m <= chunks && m <= 128 && cut > 0; ++m) {
             const int64_t len = (chunks + m - 1) / m;
-            if ((chunks + len - 1) / len != m) continue;   // the same cut with fewer pieces is listed
+            if ((chunks + len - 1) / len != m) continue;  // as with fewer pieces
             const int64_t pieces = cut * unit * m, each = 3 * len + 3;
             const int64_t run = w > 0 ? w * (2 * chunks + 2) + pieces * each / sms + 3 * len / 2
                                       : (pieces + sms - 1) / sms * each;

@@ -13,16 +13,21 @@
 // The row is recomputed from y, z, r in float32, so nothing is saved in the
 // forward pass and dx does not see X's rounding.
 //
-// GPU mapping.  Bound by moving the rows, so bytes in flight decide.  A row
-// lives in the registers of `tpr` threads as V 16-byte vectors per thread and
-// input, all loaded before anything is reduced: with many rows V is 8 (4
-// backward), so that a row of 2048 bf16 channels is one warp's (two warps') and
-// needs no (one) barrier; with rows too few to fill the GPU V is small, for the
-// latency of one row.  Weights are read again for each row (from L1).  A row's
-// sums go by shuffle inside a warp and through shared memory across warps, in a
-// fixed order.  Backward, CTAs stay, fetch a row ahead into shared memory and
-// keep the weight gradients of their rows in registers; the CTAs' sums (float32) are added by a second kernel in CTA
+// GPU mapping.  Bound by moving the rows and, close behind, by instructions.  A
+// row lives in the registers of `tpr` threads as V 16-byte vectors per thread
+// and input, all loaded before anything is reduced.  V is 2 where rows are many
+// (16384 x 2048 bf16, forward: 61 us, V = 4 69, V = 8 88; backward: 156 us, 204
+// at V = 4 and 197 at V = 1), 1 where they are too few to fill the GPU, and more
+// only where a row would take over 512 threads.  Weights are read again for
+// each row (from L1).  A row's sums go by shuffle inside a warp and through
+// shared memory across warps, in a fixed order.  Backward, CTAs stay, fetch a
+// row ahead into shared memory and keep the weight gradients of their rows in
+// registers; the CTAs' sums (float32) are added by a second kernel in CTA
 // order, so results do not depend on scheduling.
+//
+// One B200, 16384 rows of 2048 bf16 channels with everything present: forward
+// 61 us (336 MB in and out, 5.5 TB/s; instruction issue 74 %), backward 156 us
+// (537 MB, 3.4 TB/s; issue 58 %, one row's chain of sums the rest).
 #include "common.cuh"
 #include "kernels.h"
 

@@ -6,8 +6,8 @@ Tolerances count roundings (half a step: bf16 2^-8, fp32 2^-24 of the value):
 * linear attention: with A the same sums over absolute values, every term of an
   output passes at most one rounding to bf16 (its weight, or its state) besides
   the output's own, and fp32 sums of at most 256 terms a chunk; state updates
-  carry two bf16 parts (2^-17) on the tensor cores, and one more fp32 rounding
-  per chunk;
+  carry two bf16 parts (2^-17; three, and nothing lost, where the state is
+  returned) on the tensor cores, and one more fp32 rounding per chunk;
 * norms: sums over a row in fp32 (a tree, counted as 64 roundings with the
   exponential and divisions), weight gradients over the rows in fp32.
 """
