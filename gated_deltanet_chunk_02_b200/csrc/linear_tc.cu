@@ -68,7 +68,7 @@ struct LinTcArgs {
 
 struct __align__(16) LtCtrl {
     uint64_t full[kLtRing], empty[kLtRing];
-    uint64_t sc, p, parts, o, drained, mu, state, staged[2], stored[2], drain;
+    uint64_t sc, p, parts, o, drained, mu, lo, state, staged[2], stored[2], drain;
     __align__(16) float pw[kRows];                     // s lambda^n
     __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
     // by row, for whole chunks [0] and for the segment's last rows [1]: the
@@ -401,8 +401,31 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
         }
         if (!warp_wait(&c->parts, par, ab, status)) break;
         tc_fence_after();
+        if (wk.exact) {
+            if (lead) {
+                mma_tm(tMu, tSc + 32, 64, sb, true);   // lo
+                mma_commit(&c->lo);
+            }
+            __syncwarp();
+        }
+        if (wk.exact && ci + 1 < wk.nch) {
+            // the next Sc behind lo, which lies in its columns, if its tiles have
+            // come (a sequence of 32 chunks: 114 us; behind hi 119, behind Mu 124)
+            Ring<kLtRing> a1 = at;
+            a1.next();
+            ahead = __all_sync(0xffffffffu, mbar_test(&c->full[at.slot], at.phase) &&
+                                                mbar_test(&c->full[a1.slot], a1.phase));
+            if (ahead) {
+                if (!warp_wait(&c->lo, par, ab, status)) break;
+                tc_fence_after();
+                if (lead) {
+                    mma_kk(tSc, a1.tile(tiles), at.tile(tiles));
+                    mma_commit(&c->sc);
+                }
+            }
+            __syncwarp();
+        }
         if (lead) {
-            if (wk.exact) mma_tm(tMu, tSc + 32, 64, sb, true);     // lo
             mma_tm(tMu, tPart + kLtPart, 32, sb, !wk.exact);       // mid
             mma_tm(tMu, tPart, 32, sb, false);                     // hi
             mma_commit(&c->mu);
@@ -762,6 +785,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         mbar_init(&c->o, 1);
         mbar_init(&c->drained, 8);
         mbar_init(&c->mu, 1);
+        mbar_init(&c->lo, 1);
         mbar_init(&c->state, 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->staged[i], 8);
