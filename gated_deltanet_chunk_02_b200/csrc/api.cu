@@ -559,6 +559,19 @@ int gdn_rotary(const void* Q, gdn_strides qs, void* Q_out, gdn_strides qos, cons
         GDN_TRY(check_strides(kos, dtype, "K_out"));
         GDN_TRY(check_out_strides(kos, B, Hk, T, d, "K_out"));
     }
+    // in place: the same rows; else apart
+    const auto in_place = [&](const gdn_strides& i, const gdn_strides& o, int64_t H) {
+        return (B == 1 || i.b == o.b) && (H == 1 || i.h == o.h) && (T == 1 || i.t == o.t);
+    };
+    if (Hq > 0 && Q == Q_out && !in_place(qs, qos, Hq))
+        return fail(GDN_ERR_ARG, "Q_out is Q with other strides");
+    if (Hk > 0 && K == K_out && !in_place(ks, kos, Hk))
+        return fail(GDN_ERR_ARG, "K_out is K with other strides");
+    if (Hq > 0 && Hk > 0) {
+        GDN_TRY(check_apart({{Q_out, "Q_out"}, {K_out, "K_out"}}, {}));
+        GDN_TRY(check_apart({{Q_out, "Q_out"}}, {{K, "K"}}));
+        GDN_TRY(check_apart({{K_out, "K_out"}}, {{Q, "Q"}}));
+    }
     gdn::RotaryArgs a;
     memset(&a, 0, sizeof a);
     a.Q = Q; a.qs = qs; a.Qo = Q_out; a.qos = qos;
@@ -719,6 +732,9 @@ int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_
     if (!w_pre != !N) return fail(GDN_ERR_ARG, "w_pre and N go together");
     GDN_TRY(check_opt_ptr(X, "X"));
     GDN_TRY(check_opt_ptr(N, "N"));
+    GDN_TRY(check_apart({{X, "X"}, {N, "N"}},
+                        {{Y, "Y"}, {Z, "Z"}, {w_post, "w_post"}, {w_pre, "w_pre"}}));
+    GDN_TRY(check_apart({{N, "N"}}, {{R, "R"}}));
     gdn::NormArgs a;
     memset(&a, 0, sizeof a);
     a.Y = Y; a.ys = ys; a.Z = Z; a.w_post = w_post; a.R = R; a.w_pre = w_pre;
@@ -773,6 +789,11 @@ int gdn_block_norm_backward(const void* Y, gdn_strides ys, const void* Z, const 
         return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
                     (long long)workspace_bytes, (long long)need);
     if (need > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
+    GDN_TRY(check_apart({{dY, "dY"}, {dZ, "dZ"}, {dR, "dR"}, {dw_post, "dw_post"},
+                         {dw_pre, "dw_pre"}},
+                        {{Y, "Y"}, {Z, "Z"}, {w_post, "w_post"}, {R, "R"}, {w_pre, "w_pre"},
+                         {dN, "dN"}}));
+    GDN_TRY(check_apart({{dY, "dY"}, {dZ, "dZ"}}, {{dX, "dX"}}));
     gdn::NormArgs a;
     memset(&a, 0, sizeof a);
     a.Y = Y; a.ys = ys; a.Z = Z; a.w_post = w_post; a.R = R; a.w_pre = w_pre;

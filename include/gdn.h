@@ -447,7 +447,7 @@ int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* 
  * act(z) n), w_pre with N.  In: Y [B,H,T,d] (dtype, strided: the head-major
  * output of the attention calls, or H = 1 and [B,T,d]), Z, R [B,T,W] (dtype),
  * w_post, w_pre [W] f32.  Out: X [B,T,W] (dtype; NULL to skip if N is given; may
- * be R), N [B,T,W] (dtype).  N is the norm of x before X's rounding.  d = 128,
+ * be R, no other argument), N [B,T,W] (dtype).  N is the norm of x before X's rounding.  d = 128,
  * or H = 1 and d a multiple of 8; W <= 16384; eps > 0.
  */
 int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
@@ -462,7 +462,8 @@ int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_
  * device.  Inputs are those of the forward call; each weight, Z and their
  * gradients are given or left out together.  `workspace` holds
  * gdn_block_norm_backward_workspace_bytes(B, T, H, d) bytes (unused without
- * weights).  Without rows the weights' gradients are set to zero.
+ * weights).  Without rows the weights' gradients are set to zero.  Outputs share
+ * no memory with inputs, but for dR and dX.
  */
 int gdn_block_norm_backward(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
                             const void* R, const float* w_pre, const void* dX, const void* dN,

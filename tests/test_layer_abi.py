@@ -75,6 +75,10 @@ def test_rotary_refusals(lib):
     # output rows on one another: broadcast, and a token stride below a row
     assert rotary(lib, qos=st(0, 1024, 128)) == gdn.GDN_ERR_ARG and "overlap" in last(lib)
     assert rotary(lib, qos=st(4096, 1024, 64)) == gdn.GDN_ERR_ARG
+    # in place with other strides, and one tensor's output on the other
+    assert rotary(lib, qos=st(8192, 1024, 128)) == gdn.GDN_ERR_ARG and "strides" in last(lib)
+    for kw in [dict(k=FAKE), dict(k=OUT, qo=OUT)]:
+        assert rotary(lib, Hk=4, **kw) == gdn.GDN_ERR_ARG and " is " in last(lib), kw
     # nothing to do
     for kw in [dict(B=0), dict(T=0), dict(Hq=0)]:
         assert rotary(lib, q=None, qo=None, pos=None, inv=None, **kw) == gdn.GDN_OK
@@ -172,6 +176,10 @@ def test_norm_refusals(lib):
     for kw in [dict(y=ODD), dict(z=ODD), dict(wo=ODD), dict(r=ODD), dict(X=ODD),
                dict(ys=st(4096, 512, 4))]:
         assert norm(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
+    # an output that is an input (but for X and R), or the other output
+    for kw in [dict(), dict(X=OUT, z=OUT), dict(X=OUT, N=OUT, wi=FAKE),
+               dict(X=OUT, N=OUT + 64, wi=FAKE, r=OUT + 64)]:
+        assert norm(lib, **kw) == gdn.GDN_ERR_ARG and " is " in last(lib), kw
     for kw in [dict(B=0), dict(T=0), dict(H=0)]:
         assert norm(lib, y=None, **kw) == gdn.GDN_OK
 
@@ -183,6 +191,9 @@ def test_norm_backward_refusals(lib):
         assert norm_back(lib, **kw) == gdn.GDN_ERR_ARG, kw
     for kw in [dict(dy=ODD), dict(dwo=ODD), dict(ws=ODD), dict(dX=ODD), dict(dys=st(4096, 512, 4))]:
         assert norm_back(lib, **kw) == gdn.GDN_ERR_ALIGN, kw
+    for kw in [dict(), dict(dy=OUT), dict(dy=OUT, dwo=OUT), dict(dy=OUT, dwo=OUT + 64, dX=OUT),
+               dict(dy=OUT, dwo=OUT + 64, r=OUT + 128, dr=OUT + 128)]:
+        assert norm_back(lib, **kw) == gdn.GDN_ERR_ARG and " is " in last(lib), kw
     assert norm_back(lib, wo=None, dwo=None, B=0) == gdn.GDN_OK
     f = lib.gdn_block_norm_backward_workspace_bytes
     assert f(2, 4, 3, 128) > 0 and f(0, 4, 3, 128) == 0 and f(1, 1, 1, 12) == -1
