@@ -143,6 +143,7 @@ struct SimtSmem {
     float m[kSimtDV][kPitchD];                         // the state slice
     float pm[kSimtC][kPitchC];                         // weights of the chunk
     float dec[kSimtC + 1];                             // lambda^0 .. lambda^64
+    LinFound found;
 };
 
 // The rows of a chunk split over 16 x 16 threads (scores) and 32 x 8 (outputs);
@@ -352,7 +353,8 @@ template <bool STATE_ONLY>
 __global__ void __launch_bounds__(kSimtThreads) k_linear_simt(const LinArgs p) {
     extern __shared__ __align__(16) uint8_t raw[];
     SimtSmem& s = *reinterpret_cast<SimtSmem*>(raw);
-    const LinSeg g = lin_find(p, blockIdx.x >> 2, STATE_ONLY ? kCutSegments : kAllSegments);
+    const LinSeg g = lin_find(p, blockIdx.x >> 2,
+                              STATE_ONLY ? kCutSegments : kAllSegments, s.found);
     if (!g.ok) return;
     const LinProblem& q = p.pr[g.z];
     if (STATE_ONLY && (q.ws_t || !lin_added(p, q, g))) return;
@@ -405,7 +407,7 @@ LinCut pick_segment(int64_t nprob, int64_t units, int64_t rows, int ctas_per_hea
 // spread over the SMs, half of a last segment behind them.  Not cut: that, or
 // the longest sequence, taken to be half of the rows if there are several; its
 // one piece returns a state, which takes a product more per chunk, hence 9/8 (73
-// chunks of 32 heads, the longest 32: 125 us not cut, 127 to 141 us cut at 16
+// chunks of 32 heads, the longest 32: 114 us not cut, 127 to 141 us cut at 16
 // to 8, 173 us at 4).
 int64_t pick_segment_packed(int64_t nprob, int64_t nseq, int64_t Hv, int64_t rows,
                             int ctas_per_head) {

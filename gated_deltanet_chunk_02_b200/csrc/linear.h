@@ -79,10 +79,18 @@ __device__ __forceinline__ void lin_bounds(const LinArgs& p, int64_t s, int64_t&
 // Packed sequences come in classes by their share of all rows, so that the long
 // ones start first whatever their places: class 0 has above a half, class 4 up
 // to a 16th.  32 heads, 73 chunks, 32 of them one sequence's: 153 us in the
-// order of the sequences, 125 us so; backward in float32 231 and 172 us.
+// order of the sequences, 125 us so (114 with the next chunk's scores early);
+// backward in float32 231 and 172 us.
 constexpr int kLinClasses = 5;
 __device__ __forceinline__ int lin_class(int64_t n, int64_t rows) {
     return (2 * n <= rows) + (4 * n <= rows) + (8 * n <= rows) + (16 * n <= rows);
+}
+// g's own rows, from its sequence's
+__device__ __forceinline__ void lin_rows(const LinArgs& p, LinSeg& g) {
+    g.t0 = g.seq_t0 + g.k * p.seg_len;
+    g.n = g.seq_n - g.k * p.seg_len;                   // one of one may be longer than a segment
+    if (g.m > 1 && g.n > p.seg_len) g.n = p.seg_len;
+    g.ok = true;
 }
 // What lin_find counts: every segment (one at least per sequence), or the
 // segments of the sequences that have several.
@@ -90,11 +98,18 @@ enum : int { kAllSegments = 0, kCutSegments = 1 };
 __device__ __forceinline__ int lin_counted(int m, int which) {
     return which == kCutSegments && m < 2 ? 0 : m;
 }
-// The work of a block.  Problems and heads come first, as those of one segment
-// share inputs.  Called by whole warps; packed sequences are counted 32 at a time.
-__device__ __forceinline__ LinSeg lin_find(const LinArgs& p, uint32_t block, int which) {
+struct LinFound {                                      // of a block, in shared memory
+    LinSeg seg;
+    uint32_t count[32][kLinClasses + 1];               // by warp: of each class; boundaries
+};
+// The work of a block, by the first `warps` of its warps.  Problems and heads
+// come first, as those of one segment share inputs.  Each warp counts a stretch
+// of the packed sequences, 32 at a time.
+__device__ __forceinline__ void lin_search(const LinArgs& p, uint32_t block, int which, int warps,
+                                           LinFound& f) {
     LinSeg g;
     g.ok = false;
+    if (threadIdx.x == 0) f.seg = g;
     g.z = (int)(block % (uint32_t)p.nprob);
     uint32_t idx = block / (uint32_t)p.nprob;
     if (!p.cu) {
@@ -108,7 +123,7 @@ __device__ __forceinline__ LinSeg lin_find(const LinArgs& p, uint32_t block, int
             if (which == kAllSegments) idx -= whole;
             const uint32_t cut = units - whole;
             g.m = (int)lin_segments(p.T, p.seg_len);
-            if (cut == 0 || idx >= cut * (uint64_t)g.m) return g;
+            if (cut == 0 || idx >= cut * (uint64_t)g.m) return;
             g.k = (int)(idx / cut);
             u = idx - g.k * cut;
             g.st0 = (int64_t)u * (g.m - 1);
@@ -120,82 +135,105 @@ __device__ __forceinline__ LinSeg lin_find(const LinArgs& p, uint32_t block, int
         g.b = g.seq;
         g.seq_t0 = 0;
         g.seq_n = p.T;
-        if (g.m > 1 && g.st0 + g.m - 1 > p.bounds) return g;
-    } else {
-        g.hv = (int)(idx % (uint32_t)p.Hv);
-        idx /= (uint32_t)p.Hv;
-        const int lane = threadIdx.x & 31;
-        // up to 32 sequences are read once
-        int64_t t0 = 0, n = 0;
-        int m = 0, cls = -1;
-        auto read = [&](int64_t s) {
-            t0 = n = 0;
-            m = 0;
-            cls = -1;
-            if (s >= p.nseq) return;
-            lin_bounds(p, s, t0, n);
-            m = (int)lin_segments(n, p.seg_len);
-            cls = lin_class(n, p.T);
-        };
-        uint32_t total[kLinClasses] = {};
-        for (int64_t s0 = 0; s0 < p.nseq; s0 += 32) {
-            read(s0 + lane);
-#pragma unroll
-            for (int c = 0; c < kLinClasses; ++c)
-                total[c] += __reduce_add_sync(0xffffffffu, cls == c ? lin_counted(m, which) : 0);
-        }
-        int want = 0;
+        if (g.m > 1 && g.st0 + g.m - 1 > p.bounds) return;
+        lin_rows(p, g);
+        if (threadIdx.x == 0) f.seg = g;
+        return;
+    }
+    g.hv = (int)(idx % (uint32_t)p.Hv);
+    idx /= (uint32_t)p.Hv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t per = (p.nseq + 32 * warps - 1) / (32 * warps) * 32;
+    const int64_t lo = warp * per, hi = lo + per < p.nseq ? lo + per : p.nseq;
+    int64_t t0 = 0, n = 0;
+    int m = 0, cls = -1;
+    auto read = [&](int64_t s) {
+        t0 = n = 0;
+        m = 0;
+        cls = -1;
+        if (s >= hi) return;
+        lin_bounds(p, s, t0, n);
+        m = (int)lin_segments(n, p.seg_len);
+        cls = lin_class(n, p.T);
+    };
+    uint32_t count[kLinClasses + 1] = {};
+    for (int64_t s0 = lo; s0 < hi; s0 += 32) {
+        read(s0 + lane);
 #pragma unroll
         for (int c = 0; c < kLinClasses; ++c)
-            if (want == c && idx >= total[c]) {
-                idx -= total[c];
-                ++want;
-            }
-        if (want == kLinClasses) return g;
-        uint32_t before = 0;
-        int64_t slots = 0;
-        bool found = false;
-        for (int64_t s0 = 0; s0 < p.nseq && !found; s0 += 32) {
-            if (p.nseq > 32) read(s0 + lane);
-            const int mine = cls == want ? lin_counted(m, which) : 0;
-            int inc = mine, sinc = m ? m - 1 : 0;      // inclusive sums over the lanes
+            count[c] += __reduce_add_sync(0xffffffffu, cls == c ? lin_counted(m, which) : 0);
+        count[kLinClasses] += __reduce_add_sync(0xffffffffu, m > 1 ? m - 1 : 0);
+    }
+    if (lane == 0)
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, inc, o);
-                const int b = __shfl_up_sync(0xffffffffu, sinc, o);
-                if (lane >= o) { inc += a; sinc += b; }
-            }
-            const unsigned hit = __ballot_sync(
-                0xffffffffu, mine > 0 && idx < before + inc && idx >= before + inc - mine);
-            if (hit) {
-                const int w = __ffs(hit) - 1;
-                g.seq = s0 + w;
-                g.k = (int)(idx - before) - __shfl_sync(0xffffffffu, inc - mine, w);
-                g.m = __shfl_sync(0xffffffffu, m, w);
-                g.seq_t0 = __shfl_sync(0xffffffffu, t0, w);
-                g.seq_n = __shfl_sync(0xffffffffu, n, w);
-                slots += __shfl_sync(0xffffffffu, sinc - (m ? m - 1 : 0), w);
-                found = true;
-            } else {
-                slots += __shfl_sync(0xffffffffu, sinc, 31);
-            }
-            before += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (!found) return g;
-        g.b = 0;
-        g.st0 = slots * p.Hv + g.hv;
-        g.st_step = p.Hv;
-        if ((slots + g.m - 1) * p.Hv > p.bounds) {     // only sequences that overlap need more
-            raise_status(p.status, kStatusIndex);
-            return g;
+        for (int c = 0; c <= kLinClasses; ++c) f.count[warp][c] = count[c];
+    if (warps > 1) __syncthreads();
+    else __syncwarp();
+    // the class, and the warp whose stretch has it
+    int want = 0;
+#pragma unroll
+    for (int c = 0; c < kLinClasses; ++c) {
+        const uint32_t all =
+            __reduce_add_sync(0xffffffffu, lane < warps ? f.count[lane][c] : 0);
+        if (want == c && idx >= all) {
+            idx -= all;
+            ++want;
         }
     }
-    g.t0 = g.seq_t0 + g.k * p.seg_len;
-    g.n = g.seq_n - g.k * p.seg_len;
-    if (g.m == 1) g.n = g.seq_n;                       // a whole one may be longer than a segment
-    else if (g.n > p.seg_len) g.n = p.seg_len;
-    g.ok = true;
-    return g;
+    if (want == kLinClasses) return;
+    uint32_t inc = lane < warps ? f.count[lane][want] : 0;
+    const uint32_t own = inc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t a = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += a;
+    }
+    const int owner = __ffs(__ballot_sync(0xffffffffu, idx >= inc - own && idx < inc)) - 1;
+    uint32_t before = __shfl_sync(0xffffffffu, inc - own, owner);
+    int64_t slots = __reduce_add_sync(0xffffffffu, lane < owner ? f.count[lane][kLinClasses] : 0);
+    if (warp != owner) return;
+    bool found = false;
+    for (int64_t s0 = lo; s0 < hi && !found; s0 += 32) {
+        if (per > 32) read(s0 + lane);
+        const int mine = cls == want ? lin_counted(m, which) : 0;
+        int sum = mine, sinc = m ? m - 1 : 0;          // inclusive sums over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int a = __shfl_up_sync(0xffffffffu, sum, o);
+            const int b = __shfl_up_sync(0xffffffffu, sinc, o);
+            if (lane >= o) { sum += a; sinc += b; }
+        }
+        found = mine > 0 && idx < before + sum && idx >= before + sum - mine;
+        if (found) {                                   // one lane
+            g.seq = s0 + lane;
+            g.k = (int)(idx - before) - (sum - mine);
+            g.m = m;
+            g.seq_t0 = t0;
+            g.seq_n = n;
+            slots += sinc - (m - 1);
+            g.b = 0;
+            g.st0 = slots * p.Hv + g.hv;
+            g.st_step = p.Hv;
+            if ((slots + m - 1) * p.Hv > p.bounds)     // only sequences that overlap need more
+                raise_status(p.status, kStatusIndex);
+            else
+                lin_rows(p, g);
+            f.seg = g;
+        }
+        found = __any_sync(0xffffffffu, found);
+        slots += __shfl_sync(0xffffffffu, sinc, 31);
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+// The same, for all threads of a block.  One warp finds it where one count of 32
+// will do: with all warps at it the start of every block was 5 us later.  Of
+// 1000 sequences of 4 rows and 8 heads: one warp 1650 us, all of them 830 us.
+__device__ __forceinline__ LinSeg lin_find(const LinArgs& p, uint32_t block, int which,
+                                           LinFound& f) {
+    const int warps = p.cu && p.nseq > 32 ? (int)(blockDim.x >> 5) : 1;
+    if ((int)(threadIdx.x >> 5) < warps) lin_search(p, block, which, warps, f);
+    __syncthreads();
+    return f.seg;
 }
 
 // How a call is cut: the same for its workspace size and its launches.

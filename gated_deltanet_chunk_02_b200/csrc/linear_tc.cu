@@ -44,7 +44,7 @@
 // One B200, bf16, graph replay: 65536 tokens of 16 heads in 9 segments a head:
 // state pass 110 us (4.9 TB/s), outputs 195 us (5.5 TB/s), 303 us together
 // (356 us in calls without a pause, where the power limit takes the clock from
-// 1965 to 1560 MHz); batch 4 of 16 heads x 4096 tokens backward 196 us.
+// 1965 to 1560 MHz); batch 4 of 16 heads x 4096 tokens backward 194 us.
 #include <cstddef>
 #include <cstring>
 
@@ -765,7 +765,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         if (threadIdx.x == 0) raise_status(p.status, kStatusSmemAlign);
         return;
     }
-    const LinSeg g = lin_find(p, blockIdx.x, kAllSegments);
+    LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + (kLtRing + 1) * kLtTile);
+    // (its place is the state's tile, which no copy writes)
+    const LinSeg g = lin_find(p, blockIdx.x, kAllSegments,
+                              *reinterpret_cast<LinFound*>(smem + kLtRing * kLtTile));
     if (!g.ok) return;
     const LinProblem& q = p.pr[g.z];
     if (g.m == 1 && g.n <= kLtShort) {
@@ -773,7 +776,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
         return;
     }
     const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + (kLtRing + 1) * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLtRing; ++i) {
             mbar_init(&c->full[i], 1);
@@ -858,6 +860,7 @@ struct __align__(16) LsCtrl {
     uint64_t parts[2], read[2], mu, taken, drain;
     __align__(16) float w[2][kRows];                   // as in LtCtrl
     float an[2], an_lo[2];
+    LinFound found;
     uint32_t tmem;
     int abort;
 };
@@ -873,14 +876,14 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         if (threadIdx.x == 0) raise_status(p.status, kStatusSmemAlign);
         return;
     }
-    const LinSeg g = lin_find(p, blockIdx.x, kCutSegments);
+    LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + kLsRing * kLtTile);
+    const LinSeg g = lin_find(p, blockIdx.x, kCutSegments, c->found);
     if (!g.ok) return;
     const LinProblem& q = p.pr[g.z];
     if (q.ws_t) return;
     const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* const dst = lin_added(p, q, g);
     if (!dst) return;
-    LsCtrl* c = reinterpret_cast<LsCtrl*>(smem + kLsRing * kLtTile);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kLsRing; ++i) {
             mbar_init(&c->full[i], 1);

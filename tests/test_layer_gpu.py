@@ -309,7 +309,8 @@ def test_linear_some_are_cut(lib, dtype, B, backward):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("lens", [[2] * 40 + [1400, 0, 257], [130] * 3 + [9] * 33 + [900, 450, 260, 1],
-                                  [0] * 35 + [1700]])
+                                  [0] * 35 + [1700],
+                                  [1, 0, 2] * 400 + [300, 5] * 3 + [1200, 0, 130]])
 def test_linear_packed_long_behind_short(lib, dtype, lens):
     c = linear_case(8, dtype, 1, 1, 2, sum(lens), lens, True)
     check_both_ways(c, dtype, sum(lens))
