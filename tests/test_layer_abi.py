@@ -127,6 +127,12 @@ def test_linear_refusals(lib):
     assert backward(lib, ds0=ODD) == gdn.GDN_ERR_ALIGN
 
 
+def test_linear_more_heads_than_a_grid(lib):
+    for s, cu in [(shape(B=1 << 26, T=0), None), (shape(nseq=1 << 26, T=1), FAKE)]:
+        for f in (forward, backward):
+            assert f(lib, s=s, cu=cu) == gdn.GDN_ERR_ARG and "too many" in last(lib)
+
+
 def test_linear_workspace_sizes(lib):
     f, b = lib.gdn_linear_forward_workspace_bytes, lib.gdn_linear_backward_workspace_bytes
     for dtype in (BF16, F32):
