@@ -771,3 +771,35 @@ def test_binding_checks_shapes_and_types(lib):
                            None)
     with pytest.raises(gdn.GdnError):
         gdn.gdn_block_norm(y, None, None, None, None, None, None)
+
+
+# --------------------------------------------------------------------------- #
+# arguments at the alignment that the header asks for, and no more
+# --------------------------------------------------------------------------- #
+def shifted(t, by=16):
+    """The same tensor on memory that starts ``by`` bytes past a 256-byte boundary."""
+    raw = torch.full((t.nbytes + by,), 255, dtype=torch.uint8, device="cuda")
+    assert raw.data_ptr() % 256 == 0
+    return raw[by:].view(t.dtype).view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,Hv,T,lens", [(1, 2, 4, 300, None), (2, 1, 1, 129, None),
+                                            (1, 1, 2, 700, [128, 5, 129, 1, 400]),
+                                            (1, 1, 2, 2600, None)])
+def test_linear_at_16_byte_alignment(lib, dtype, B, Hk, Hv, T, lens):
+    """Every tensor at 16 bytes past a multiple of 32: the bits of the aligned call."""
+    c = linear_case(T + 2, dtype, B, Hk, Hv, T, lens, True)
+    O, S = run_forward(c, 0.7)
+    grads = run_backward(c, 0.7)
+    m = {x: shifted(c[x]) for x in ("Q", "K", "V", "dO", "S0", "dS")}
+    ws = [shifted(torch.full((f(c["K"], c["V"], c["cu"]),), 255, dtype=torch.uint8, device="cuda"))
+          for f in (gdn.gdn_linear_forward_workspace_bytes, gdn.gdn_linear_backward_workspace_bytes)]
+    O1, S1 = shifted(torch.full_like(O, 77.0)), shifted(torch.full_like(S, 77.0))
+    gdn.gdn_linear_forward(m["Q"], m["K"], m["V"], c["lg"], m["S0"], O1, S1, ws[0], scale=0.7,
+                           cu_seqlens=c["cu"])
+    assert torch.equal(O1, O) and torch.equal(S1, S)
+    out = [shifted(torch.full_like(t, 77.0)) for t in grads]
+    gdn.gdn_linear_backward(m["Q"], m["K"], m["V"], c["lg"], m["S0"], m["dO"], m["dS"], *out, ws[1],
+                            scale=0.7, cu_seqlens=c["cu"])
+    assert all(torch.equal(a, b) for a, b in zip(out, grads))
