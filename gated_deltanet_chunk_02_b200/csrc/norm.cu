@@ -91,13 +91,16 @@ __device__ __forceinline__ void weights(const float* w, int at, F2 (&x)[P]) {
 
 // t = e^-z and s = 1 / (1 + t), two at a time, by the base-2 exponential (the
 // product -z log2(e) costs |z| 2^-24).  z stops at -87, where t is still finite:
-// 1 - s = t s then keeps its digits where s is near one.  A NaN stays one.
-__device__ __forceinline__ void logistic2(F2 z, F2& t, F2& s) {
+// 1 - s = t s then keeps its digits where s is near one.  The caller's z stops
+// there too: z s is then at most 1.5e-36 however low the gate, where the type's
+// lowest value times the s of -87 would be -5.6.  A NaN stays one.
+__device__ __forceinline__ void logistic2(F2& z, F2& t, F2& s) {
     float x, y;
     z.get(x, y);
     asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(x));  // -87
     asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(y));
-    mul2(F2(x, y), both(-1.442695041f)).get(x, y);
+    z = F2(x, y);
+    mul2(z, both(-1.442695041f)).get(x, y);
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
     t = F2(x, y);
@@ -106,9 +109,9 @@ __device__ __forceinline__ void logistic2(F2 z, F2& t, F2& s) {
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(y));
     s = F2(x, y);
 }
-// x *= act(z), a vector's channels
+// x *= act(z), a vector's channels (z is used up)
 template <int P>
-__device__ __forceinline__ void apply_gate(const F2 (&z)[P], int act, F2 (&x)[P]) {
+__device__ __forceinline__ void apply_gate(F2 (&z)[P], int act, F2 (&x)[P]) {
     F2 t, s;
     if (act == GDN_ACT_SILU) {
 #pragma unroll

@@ -803,3 +803,36 @@ def test_linear_at_16_byte_alignment(lib, dtype, B, Hk, Hv, T, lens):
     gdn.gdn_linear_backward(m["Q"], m["K"], m["V"], c["lg"], m["S0"], m["dO"], m["dS"], *out, ws[1],
                             scale=0.7, cu_seqlens=c["cu"])
     assert all(torch.equal(a, b) for a, b in zip(out, grads))
+
+
+# --------------------------------------------------------------------------- #
+# gates at the types' lowest values
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_block_norm_gates_that_shut(lib, dtype, act):
+    """Gates from -200 to the lowest value and minus infinity: nothing passes,
+    forward or backward.  e^-200 is 1e-87; the gate is formed at -87, where both
+    activations and their slopes are below 2e-36."""
+    low = torch.finfo(DT[dtype]).min
+    gates = [low, low / 2, -1e35, -1e30, -1e10, -200.0, -87.5, float("-inf")]
+    z = torch.tensor(gates).to(DT[dtype]).cuda()[None, None]
+    y = torch.full((1, 1, 1, 8), 3.0, dtype=DT[dtype], device="cuda")
+    r = torch.tensor([1.0, -2.0, 0.5, 4.0, -1.0, 0.25, 8.0, 3.0]).to(DT[dtype]).cuda()[None, None]
+    w = torch.full((8,), 2.0, device="cuda")
+    X, N = torch.empty_like(z), torch.empty_like(z)
+    gdn.gdn_block_norm(y, z, None, None, None, X, None, act=act)
+    assert (X.float().abs() <= 3 * 2e-36).all(), X
+    gdn.gdn_block_norm(y, z, w, r, w, X, N, act=act)
+    assert torch.equal(X, r)
+    g = torch.ones_like(z)
+    dY, dZ, dR = torch.empty_like(y), torch.empty_like(z), torch.empty_like(z)
+    gdn.gdn_block_norm_backward(y, z, None, None, None, g, None, dY, dZ, None, None, None, None,
+                                act=act)
+    assert (dY.float().abs() <= 2e-36).all() and (dZ.float().abs() <= 3 * 2e-36).all(), (dY, dZ)
+    dw, dv = torch.empty_like(w), torch.empty_like(w)
+    ws = torch.empty(gdn.gdn_block_norm_backward_workspace_bytes(y), dtype=torch.uint8, device="cuda")
+    gdn.gdn_block_norm_backward(y, z, w, r, w, g, g, dY, dZ, dR, dw, dv, ws, act=act)
+    # |dx| <= 1 + 2 / rms + ..: below 16 here, and n = 2
+    for t, n in ((dY, 32), (dZ, 32), (dw, 16)):
+        assert (t.float().abs() <= n * 2e-36).all(), t
