@@ -233,7 +233,8 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int i = ti + 16 * u, j = tj + 16 * w, dist = REV ? j - i : i - j;
-                        s.pm[i][j] = dist >= 0 ? q.s_weight * s.dec[dist] * acc[u][w] : 0.f;
+                        s.pm[i][j] =
+                            dist >= 0 && j < n ? q.s_weight * s.dec[dist] * acc[u][w] : 0.f;
                     }
             }
             __syncthreads();

@@ -267,19 +267,27 @@ __device__ __forceinline__ float* lin_added(const LinArgs& p, const LinProblem& 
 }
 
 // log2 of the decay; -inf (no memory at all) becomes a finite number whose
-// product with a distance of zero is zero
+// product with a distance of zero is zero.  A NaN stays one here and below.
 __device__ __forceinline__ double lin_log2(const float* loggate, int hv) {
-    return fmax((double)loggate[hv] * 1.4426950408889634, -1e30);
+    const double x = (double)loggate[hv] * 1.4426950408889634;
+    return x < -1e30 ? -1e30 : x;
 }
-// lambda^n: the exponent in binary64 and its fraction alone to exp2f, so that
-// the error stays at exp2f's two units however far n reaches
+// an exponent of two, as far as floats and doubles care (the identity for NaN,
+// which fmin and fmax are not)
+__device__ __forceinline__ double lin_clamp(double x) {
+    return x < -1000.0 ? -1000.0 : (x > 1000.0 ? 1000.0 : x);
+}
+// lambda^n, 1 for n = 0 whatever lambda: the exponent in binary64 and its
+// fraction alone to exp2f, so that the error stays at exp2f's two units however
+// far n reaches
 __device__ __forceinline__ float lin_pow(double lg, int64_t n) {
+    if (n == 0) return 1.f;
     const double x = lg * (double)n, i = rint(x);
-    return ldexpf(exp2f((float)(x - i)), (int)fmin(fmax(i, -1000.0), 1000.0));
+    return ldexpf(exp2f((float)(x - i)), (int)lin_clamp(i));
 }
 // the same as a sum of two floats
 __device__ __forceinline__ void lin_pow2(double lg, int64_t n, float& hi, float& lo) {
-    const double x = exp2(fmin(fmax(lg * (double)n, -1000.0), 1000.0));
+    const double x = n == 0 ? 1.0 : exp2(lin_clamp(lg * (double)n));
     hi = (float)x;
     lo = (float)(x - (double)hi);
 }

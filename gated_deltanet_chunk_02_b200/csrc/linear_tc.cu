@@ -590,17 +590,21 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
                             s[i + 1] = mul2(F2(t.z, t.w), f2);
                         }
                         tmem_wait_ld();
-                        if (rev && n < kRows) {        // columns that are not the segment's rows
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = j0 + i < n ? v[i] : 0u;
-                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float x, y;
                             mul2(F2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s[i])
                                 .get(x, y);
-                            w[i] = pack_b2(x, y);
+                            v[2 * i] = __float_as_uint(x);
+                            v[2 * i + 1] = __float_as_uint(y);
                         }
+                        if (rev && n < kRows) {        // columns that are not the segment's rows
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = j0 + i < n ? v[i] : 0u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_b2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                     }
                 }
                 tmem_st16(tSc + 16 * pc, w);           // behind the columns still to be read
@@ -819,8 +823,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
             c->w[t / kRows][i] = i < n ? q.s_state * lin_pow(lg, wk.rev ? i + 1 : n - 1 - i) : 0.f;
         } else if (t < 4 * kRows) {
             const int n = t < 3 * kRows ? kRows : n1;
-            c->d[t / kRows - 2][i] =
-                fmaxf(lin_pow(lg, wk.rev ? (i < n ? n - 1 - i : 0) : i + 1), 0x1p-60f);
+            const float d = lin_pow(lg, wk.rev ? (i < n ? n - 1 - i : 0) : i + 1);
+            c->d[t / kRows - 2][i] = d < 0x1p-60f ? 0x1p-60f : d;  // NaN stays
         } else if (i < 32) {
             c->step[i] = lin_pow(lg, wk.rev ? i : 31 - i);
         } else if (i < 34) {

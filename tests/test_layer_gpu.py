@@ -836,3 +836,31 @@ def test_block_norm_gates_that_shut(lib, dtype, act):
     # |dx| <= 1 + 2 / rms + ..: below 16 here, and n = 2
     for t, n in ((dY, 32), (dZ, 32), (dw, 16)):
         assert (t.float().abs() <= n * 2e-36).all(), t
+
+
+# --------------------------------------------------------------------------- #
+# decays that are not numbers
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,lens", [(1, None), (5, None), (150, None), (2600, None),
+                                    (500, [3, 0, 128, 300])])
+def test_linear_nan_decay_shows_in_its_head_alone(lib, dtype, T, lens):
+    """A NaN log-decay: NaN wherever the recurrence has it (outputs and states;
+    a last row's dK and dV meet no decay), other heads as without it."""
+    c = linear_case(50, dtype, 1, 3, 3, T, lens, True)
+    good = (*run_forward(c, 0.7), *run_backward(c, 0.7))
+    c["lg"] = c["lg"].clone()
+    c["lg"][1] = float("nan")
+    got = (*run_forward(c, 0.7), *run_backward(c, 0.7))
+    want = (*oracle_linear(c, 0.7), *oracle_linear_grad(c, 0.7))
+    used = T if lens is None else sum(lens)
+    for a, b, w in zip(got, good, want):
+        rows = slice(None) if a.shape[2:] == (128, 128) and a.shape[0] == len(c["rows"]) else \
+            slice(0, used)
+        assert torch.equal(a[:, [0, 2]], b[:, [0, 2]])
+        assert np.array_equal(np.isnan(f64(a[:, 1, rows])), np.isnan(w[:, 1, rows]))
+    if T <= 5:
+        O, S = torch.empty_like(c["V"]), c["S0"].clone()
+        gdn.gdn_linear_decode(c["Q"], c["K"], c["V"], c["lg"], S, O, scale=0.7)
+        assert O[:, 1].isnan().all() and S[:, 1].isnan().all()
+        assert not O[:, [0, 2]].isnan().any() and not S[:, [0, 2]].isnan().any()
