@@ -143,6 +143,7 @@ struct SimtSmem {
     float m[kSimtDV][kPitchD];                         // the state slice
     float pm[kSimtC][kPitchC];                         // weights of the chunk
     float dec[kSimtC + 1];                             // lambda^0 .. lambda^64
+    int odd;                                           // a value was infinite or NaN
     LinFound found;
 };
 
@@ -156,6 +157,7 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
     const int tid = threadIdx.x;
     const double lg = lin_log2(p.loggate, hv);
     if (tid <= kSimtC) s.dec[tid] = lin_pow(lg, tid);
+    if (tid == 0) s.odd = 0;
     // incoming state
     for (int e = tid; e < kSimtDV * kLinD; e += kSimtThreads) {
         const int r = e / kLinD, c = e % kLinD;
@@ -198,7 +200,9 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
         }
         for (int e = tid; e < kSimtC * kSimtDV; e += kSimtThreads) {
             const int r = e / kSimtDV, c = e % kSimtDV;
-            s.ct[c][r] = r < n ? gc[(r0 + r) * kLinD + c] : 0.f;
+            const float x = r < n ? gc[(r0 + r) * kLinD + c] : 0.f;
+            if (!STATE_ONLY && !isfinite(x)) s.odd = 1;
+            s.ct[c][r] = x;
         }
         __syncthreads();
         if (!STATE_ONLY) {
@@ -264,23 +268,38 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
                             st[u][w] = fmaf(x[u].w, y[w].w, st[u][w]);
                         }
                 }
+                if (!s.odd) {
 #pragma unroll 2
-                for (int k = 0; k < kSimtC; k += 4) {
-                    float4 x[2], y[4];
+                    for (int k = 0; k < kSimtC; k += 4) {
+                        float4 x[2], y[4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        x[u] = *reinterpret_cast<const float4*>(&s.pm[ri + 32 * u][k]);
+                        for (int u = 0; u < 2; ++u)
+                            x[u] = *reinterpret_cast<const float4*>(&s.pm[ri + 32 * u][k]);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        y[w] = *reinterpret_cast<const float4*>(&s.ct[cj + 8 * w][k]);
+                        for (int w = 0; w < 4; ++w)
+                            y[w] = *reinterpret_cast<const float4*>(&s.ct[cj + 8 * w][k]);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            in[u][w] = fmaf(x[u].x, y[w].x, in[u][w]);
-                            in[u][w] = fmaf(x[u].y, y[w].y, in[u][w]);
-                            in[u][w] = fmaf(x[u].z, y[w].z, in[u][w]);
-                            in[u][w] = fmaf(x[u].w, y[w].w, in[u][w]);
+                            for (int w = 0; w < 4; ++w) {
+                                in[u][w] = fmaf(x[u].x, y[w].x, in[u][w]);
+                                in[u][w] = fmaf(x[u].y, y[w].y, in[u][w]);
+                                in[u][w] = fmaf(x[u].z, y[w].z, in[u][w]);
+                                in[u][w] = fmaf(x[u].w, y[w].w, in[u][w]);
+                            }
+                    }
+                } else {
+                    // a weight of zero would make NaN of an infinite or NaN value,
+                    // and the row is not to see what lies on its other side
+#pragma unroll 1
+                    for (int k = 0; k < kSimtC; ++k)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int i = ri + 32 * u;
+                            if (REV ? k < i : k > i) continue;
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                in[u][w] = fmaf(s.pm[i][k], s.ct[cj + 8 * w][k], in[u][w]);
                         }
                 }
 #pragma unroll

@@ -864,3 +864,33 @@ def test_linear_nan_decay_shows_in_its_head_alone(lib, dtype, T, lens):
         gdn.gdn_linear_decode(c["Q"], c["K"], c["V"], c["lg"], S, O, scale=0.7)
         assert O[:, 1].isnan().all() and S[:, 1].isnan().all()
         assert not O[:, [0, 2]].isnan().any() and not S[:, [0, 2]].isnan().any()
+
+
+# --------------------------------------------------------------------------- #
+# infinities and NaN at one row
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("T,lens,rows", [(6, None, (0, 3)), (200, None, (0, 63, 64, 127, 150, 199)),
+                                         (2600, None, (5, 700, 1290, 2599)),
+                                         (420, [100, 0, 257, 5], (99, 100, 230, 360))])
+def test_linear_odd_values_reach_only_what_the_recurrence_has_them_in(lib, dtype, T, lens, rows):
+    """One NaN or infinity in Q, K, V or dO: results are not finite exactly where
+    the token-by-token formula's are not (a row never sees the rows on its other
+    side), and the bits of the clean call elsewhere."""
+    c = linear_case(60 + T, dtype, 1, 1, 1, T, lens, True)
+    c["lg"] = torch.tensor([-0.01]).cuda()
+    used = slice(0, T if lens is None else sum(lens))
+    good = [t if t.shape[0] == len(c["rows"]) and t.shape[2:] == (128, 128) else t[:, :, used]
+            for t in (*run_forward(c, 0.7), *run_backward(c, 0.7))]
+    for at, name in zip(rows * 4, [x for x in ("V", "K", "Q", "dO") for _ in rows]):
+        odd = dict(c, **{name: c[name].clone()})
+        odd[name][0, 0, at, 37] = float("nan") if at % 2 else float("inf")
+        got = (*run_forward(odd, 0.7), *run_backward(odd, 0.7))
+        with np.errstate(invalid="ignore"):
+            want = (*oracle_linear(odd, 0.7), *oracle_linear_grad(odd, 0.7))
+        for a, b, w in zip(got, good, want):
+            if a.shape != b.shape:
+                a, w = a[:, :, used], w[:, :, used]
+            fine = np.isfinite(w)
+            assert np.array_equal(np.isfinite(f64(a)), fine), (name, at)
+            assert torch.equal(a[torch.from_numpy(fine)], b[torch.from_numpy(fine)]), (name, at)
