@@ -72,15 +72,19 @@ struct __align__(16) LtCtrl {
     __align__(16) float pw[kRows];                     // s lambda^n
     __align__(16) float step[32];                      // lambda^(31 - n), lambda^n if reverse
     // by row, for whole chunks [0] and for the segment's last rows [1]: the
-    // weight of c, d; and lambda^n as a sum of two floats
-    float w[2][kRows], d[2][kRows];
+    // weight of c; and lambda^n as a sum of two floats
+    float w[2][kRows];
+    float d[kRows];                                    // of a whole chunk
     float an[2], an_lo[2], lambda;
     uint32_t tmem;
     int abort;
+    int odd;                                           // a state row ended as NaN
+    __align__(16) int odd_from[kRows];                 // by column of c: lt_scan
 };
 constexpr int kLtSmem = (kLtRing + 1) * kLtTile + (int)sizeof(LtCtrl);
 static_assert(kLtSmem <= 232448, "shared memory budget");
-static_assert(offsetof(LtCtrl, step) % 16 == 0, "step is read 16 bytes at a time");
+static_assert(offsetof(LtCtrl, step) % 16 == 0 && offsetof(LtCtrl, odd_from) % 16 == 0,
+              "read 16 bytes at a time");
 
 // Bounded wait; false once it ran out or another role's did.  The loop is a
 // function of its own: a dozen copies of it would not leave the roles' code in
@@ -304,6 +308,8 @@ struct LtWalk {                                        // chunks of a segment, i
     bool exact;                                        // the state is returned: three parts
     __device__ int first(int ci) const { return (rev ? nch - 1 - ci : ci) * kRows; }
     __device__ int rows(int r0) const { return n - r0 < kRows ? n - r0 : kRows; }
+    // a row's place in walking order (rows that are not there have places too)
+    __device__ int place(int ci, int r) const { return ci * kRows + (rev ? kRows - 1 - r : r); }
 };
 
 __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g, int hv,
@@ -454,9 +460,10 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
 // been read; a's and b's are needed sooner), for the store warp; straight to memory where rows of the
 // chunk are not the segment's, or in float32.  Direct stores of whole rows take
 // the shared-memory pipe for 1000 cycles a chunk.
+template <bool CAREFUL>
 __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, int h, int64_t row,
                                           const LinProblem& q, uint32_t c_tile, LtCtrl* c,
-                                          int chunk) {
+                                          int chunk, int place) {
     const int lane = threadIdx.x & 31;
     uint32_t x[2][32];
     tmem_ld32_async(to, x[0]);
@@ -464,6 +471,16 @@ __device__ __forceinline__ void lt_output(uint32_t to, float d, int n, int r, in
     tmem_wait_ld();
     tc_fence_before();
     warp_arrive(&c->drained, lane);
+    if (CAREFUL) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+            const int4 from = *reinterpret_cast<const int4*>(&c->odd_from[64 * h + i]);
+            const int f[4] = {from.x, from.y, from.z, from.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (place >= f[e]) x[(i + e) >> 5][(i + e) & 31] = 0x7fffffffu;
+        }
+    }
     const bool by_tma = n == kRows && !q.out_f32;
     const int64_t at = (row + r) * kD + 64 * h;
 #pragma unroll
@@ -518,7 +535,38 @@ __device__ void lt_store(const LtWalk& wk, const LinProblem& q, const CUtensorMa
     bulk_wait_all();
 }
 
-__device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
+// An infinite or NaN value of c makes its column not a number from its row on,
+// in walking order; rows before it do not see it.  But their weights for it,
+// which are zero, would make NaN of it in P c.  So such values are zero for the
+// product, and the places from which on their columns are lost are kept for the
+// outputs and the state.  (An infinity is a NaN from here on: the split into
+// parts makes one of it.)  Walks do so on their second turn only: a value that
+// is not finite leaves NaN in its row of the state up to the end of a walk, which
+// then is made again.  That the second turn is there costs ordinary data 2 %
+// (packed 111 -> 113 us, backward 195 -> 199); scans of c in every walk, by the
+// state's warps or by a warp of their own, cost 6 to 10 % (118 and 120, 215 and
+// 213), as did tests for a second turn inside the roles.
+__device__ __noinline__ void lt_scan(uint32_t tile, int r, int h, int place, LtCtrl* c) {
+#pragma unroll 1
+    for (int e = 8 * h; e < 8 * h + 8; ++e) {
+        const uint4 u = lds128(tile + op_off(r, e));
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t half = i & 1 ? 0xffff0000u : 0xffffu, ones = half & 0x7f807f80u;
+            if ((w[i >> 1] & ones) != ones) continue;
+            w[i >> 1] &= ~half;
+            found = true;
+            atomicMin(&c->odd_from[8 * e + i], place);
+        }
+        if (found) sts128(tile + op_off(r, e), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    fence_async_smem();
+}
+
+template <bool CAREFUL>
+__device__ __forceinline__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
                         const LtWalk& wk, uint32_t tiles, LtCtrl* c) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
@@ -539,11 +587,12 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
                 !warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status))
                 break;
             tc_fence_after();
-            lt_output(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, c_tile, c, ci - 1);
+            lt_output<CAREFUL>(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, c_tile, c,
+                               ci - 1, wk.place(ci - 1, r));
         }
         if (ci < wk.nch) {
             const int n = wk.rows(wk.first(ci));
-            d = c->d[n < kRows][r];
+            d = c->d[rev ? min(r + kRows - n, kRows - 1) : r];
             const float inv = 1.f / d;
             if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status)) break;
             tc_fence_after();
@@ -610,15 +659,19 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
                 tmem_st16(tSc + 16 * pc, w);           // behind the columns still to be read
             }
             tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(&c->p, lane);
-            // the parts of w c, once the last chunk's have been read
             const Ring<kLtRing> b = at;
             at.next();
             at.next();
             const Ring<kLtRing> v = at;
             at.next();
             c_tile = v.tile(tiles);
+            if (CAREFUL) {
+                if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status)) break;
+                if (r < n) lt_scan(c_tile, r, h, wk.place(ci, r), c);
+            }
+            tc_fence_before();
+            warp_arrive(&c->p, lane);
+            // the parts of w c, once the last chunk's have been read
             if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status) ||
                 (ci > 0 && !warp_wait(&c->mu, (ci - 1) & 1, &c->abort, p.status)))
                 break;
@@ -643,7 +696,8 @@ __device__ void lt_rows(const LinArgs& p, const LinProblem& q, const LinSeg& g, 
     }
 }
 
-__device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
+template <bool CAREFUL>
+__device__ __forceinline__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g, int hv,
                          const LtWalk& wk, uint32_t tiles, LtCtrl* c) {
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, h = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
@@ -691,7 +745,11 @@ __device__ void lt_state(const LinArgs& p, const LinProblem& q, const LinSeg& g,
         tc_fence_after();
         const int part = wk.rows(wk.first(ci)) < kRows;
         take_update(tMu, c->an[part], c->an_lo[part], m);
+        if (CAREFUL && c->odd_from[r] < (ci + 1) * kRows)
+#pragma unroll
+            for (int i = 0; i < 64; ++i) m[i] = __uint_as_float(0x7fffffffu);
     }
+    if (isnan(m[0])) c->odd = 1;
     if (wk.exact && q.mout)
         store_state(q.mout + (g.seq * p.Hv + hv) * kLinState, r, h, m);
 }
@@ -770,6 +828,84 @@ __device__ void lt_short(const LinArgs& p, const LinProblem& q, const LinSeg& g,
     }
 }
 
+__device__ __forceinline__ void lt_barriers(LtCtrl* c) {
+    for (int i = 0; i < kLtRing; ++i) {
+        mbar_init(&c->full[i], 1);
+        mbar_init(&c->empty[i], 1);
+    }
+    mbar_init(&c->sc, 1);
+    mbar_init(&c->p, 8);
+    mbar_init(&c->parts, 8);
+    mbar_init(&c->o, 1);
+    mbar_init(&c->drained, 8);
+    mbar_init(&c->mu, 1);
+    mbar_init(&c->lo, 1);
+    mbar_init(&c->state, 8);
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&c->staged[i], 8);
+        mbar_init(&c->stored[i], 1);
+    }
+    mbar_init(&c->drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// one walk of the segment by all roles
+template <bool CAREFUL>
+__device__ __forceinline__ void lt_turn(const LinTcArgs& k, const LinProblem& q, const LinSeg& g,
+                                        const LtWalk& wk, uint8_t* smem, LtCtrl* c) {
+    const LinArgs& p = k.a;
+    const uint32_t tiles = su32(smem);
+    const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp < 8) {
+        lt_rows<CAREFUL>(p, q, g, hv, wk, tiles, c);
+    } else if (warp < 16) {
+        lt_state<CAREFUL>(p, q, g, hv, wk, tiles, c);
+    } else if (warp == 16) {
+        if (lane == 0) lt_load(k, q, g, hv, wk, smem, c);
+    } else if (warp == 17) {
+        lt_multiply(wk, tiles, c, p.status);
+    } else if (lane == 0) {
+        lt_store(wk, q, &k.out[g.z], (int)((g.b * p.Hv + hv) * p.T + g.t0), smem, c, p.status);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+}
+
+__device__ __forceinline__ LtWalk lt_walk(const LinSeg& g, const LinProblem& q) {
+    return {(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0,
+            // a sequence of several segments has its outgoing state from steps 1
+            // and 2; whether one is asked for changes no output
+            g.m == 1 && q.has_state};
+}
+
+// The walk's second turn (see lt_scan), behind all copies, products and arrivals
+// of the first.  It finds its segment again: anything that the first turn kept
+// for it would be spilled there (backward 203 us).  TMEM is still held, as a CTA
+// allocates once, and freed here.
+__device__ __noinline__ void lt_again(const LinTcArgs& k) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    LtCtrl* c = reinterpret_cast<LtCtrl*>(smem + (kLtRing + 1) * kLtTile);
+    const LinSeg g = lin_find(k.a, blockIdx.x, kAllSegments,
+                              *reinterpret_cast<LinFound*>(smem + kLtRing * kLtTile));
+    const LinProblem& q = k.a.pr[g.z];
+    const LtWalk wk = lt_walk(g, q);
+    if (threadIdx.x == 0) {
+        land<kLtRing>(c->empty, 3 * wk.nch);
+        if (wk.exact) mbar_wait(&c->lo, (wk.nch - 1) & 1);
+        for (uint64_t* b = c->full; b <= &c->drain; ++b)
+            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(su32(b)) : "memory");
+        lt_barriers(c);
+    }
+    __syncthreads();
+    tc_fence_after();
+    lt_turn<true>(k, q, g, wk, smem, c);
+    if (threadIdx.x >> 5 == 17) {
+        tc_fence_after();
+        tmem_dealloc(c->tmem, 512);
+    }
+}
+
 // one block for each of lin_find's
 __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_constant__ LinTcArgs k) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -790,41 +926,23 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     }
     const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kLtRing; ++i) {
-            mbar_init(&c->full[i], 1);
-            mbar_init(&c->empty[i], 1);
-        }
-        mbar_init(&c->sc, 1);
-        mbar_init(&c->p, 8);
-        mbar_init(&c->parts, 8);
-        mbar_init(&c->o, 1);
-        mbar_init(&c->drained, 8);
-        mbar_init(&c->mu, 1);
-        mbar_init(&c->lo, 1);
-        mbar_init(&c->state, 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c->staged[i], 8);
-            mbar_init(&c->stored[i], 1);
-        }
-        mbar_init(&c->drain, 1);
+        lt_barriers(c);
         c->abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        c->odd = 0;
     }
     if (warp == 17) tmem_alloc(&c->tmem, 512);
-    const LtWalk wk{(int)g.n, (int)((g.n + kRows - 1) / kRows), q.reverse != 0,
-                    // a sequence of several segments has its outgoing state from steps 1
-                    // and 2; whether one is asked for changes no output
-                    g.m == 1 && q.has_state};
+    const LtWalk wk = lt_walk(g, q);
     {
         const double lg = lin_log2(p.loggate, hv);
         const int t = threadIdx.x, i = t % kRows, n1 = wk.n - (wk.nch - 1) * kRows;
         if (t < 2 * kRows) {
             const int n = t < kRows ? kRows : n1;
             c->w[t / kRows][i] = i < n ? q.s_state * lin_pow(lg, wk.rev ? i + 1 : n - 1 - i) : 0.f;
+        } else if (t < 3 * kRows) {
+            const float d = lin_pow(lg, wk.rev ? kRows - 1 - i : i + 1);
+            c->d[i] = d < 0x1p-60f ? 0x1p-60f : d;     // NaN stays
         } else if (t < 4 * kRows) {
-            const int n = t < 3 * kRows ? kRows : n1;
-            const float d = lin_pow(lg, wk.rev ? (i < n ? n - 1 - i : 0) : i + 1);
-            c->d[t / kRows - 2][i] = d < 0x1p-60f ? 0x1p-60f : d;  // NaN stays
+            c->odd_from[i] = 0x7fffffff;               // never
         } else if (i < 32) {
             c->step[i] = lin_pow(lg, wk.rev ? i : 31 - i);
         } else if (i < 34) {
@@ -837,22 +955,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tiles = su32(smem);
-    if (warp < 8) {
-        lt_rows(p, q, g, hv, wk, tiles, c);
-    } else if (warp < 16) {
-        lt_state(p, q, g, hv, wk, tiles, c);
-    } else if (warp == 16) {
-        if (lane == 0) lt_load(k, q, g, hv, wk, smem, c);
-    } else if (warp == 17) {
-        lt_multiply(wk, tiles, c, p.status);
-    } else if (lane == 0) {
-        lt_store(wk, q, &k.out[g.z], (int)((g.b * p.Hv + hv) * p.T + g.t0), smem, c,
-                 p.status);
+    lt_turn<false>(k, q, g, wk, smem, c);
+    if (c->odd && !c->abort) {
+        lt_again(k);
+        return;
     }
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
     if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(c->tmem, 512);

@@ -869,7 +869,7 @@ def test_linear_nan_decay_shows_in_its_head_alone(lib, dtype, T, lens):
 # --------------------------------------------------------------------------- #
 # infinities and NaN at one row
 # --------------------------------------------------------------------------- #
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,lens,rows", [(6, None, (0, 3)), (200, None, (0, 63, 64, 127, 150, 199)),
                                          (2600, None, (5, 700, 1290, 2599)),
                                          (420, [100, 0, 257, 5], (99, 100, 230, 360))])
@@ -894,3 +894,29 @@ def test_linear_odd_values_reach_only_what_the_recurrence_has_them_in(lib, dtype
             fine = np.isfinite(w)
             assert np.array_equal(np.isfinite(f64(a)), fine), (name, at)
             assert torch.equal(a[torch.from_numpy(fine)], b[torch.from_numpy(fine)]), (name, at)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_linear_padded_rows_may_hold_anything(lib, dtype):
+    """A padded batch whose rows behind each prompt are NaN and infinity in V
+    (keys zero there): the prompts' outputs have the clean batch's bits, prompts
+    that are cut into segments and whole ones, and two such calls at once."""
+    for B, H, T, used in ((2, 2, 300, (131, 260)), (1, 2, 2600, (1333,)), (40, 4, 260, None)):
+        c = linear_case(70 + T, dtype, B, H, H, T, None, False)
+        used = used or [(37 * b) % T + 1 for b in range(B)]
+        for b, n in enumerate(used):
+            c["K"][b, :, n:] = 0.0
+        good, _ = run_forward(c, 0.7)
+        for b, n in enumerate(used):
+            c["V"][b, :, n:] = float("nan")
+            c["V"][b, :, n + 3::5, ::3] = float("-inf")
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            also, _ = run_forward(c, 0.7)
+        got, _ = run_forward(c, 0.7)
+        torch.cuda.synchronize()
+        for b, n in enumerate(used):
+            for o in (got, also):
+                assert torch.equal(o[b, :, :n], good[b, :, :n]), (b, n)
+                assert not o[b, :, n:].isfinite().any()
