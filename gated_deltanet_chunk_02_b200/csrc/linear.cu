@@ -105,20 +105,35 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
 }
 
 // ---- gradients of shared heads: the sum over the value heads of a group ----
+// Is row t one of a sequence's?  By the whole warp.  Bisection finds it if all
+// bounds are in order; a row that it does not find is of no sequence, or the
+// bounds of others are bad and left out: all sequences are tried.
+__device__ __forceinline__ bool lin_has_row(const LinArgs& p, int64_t t) {
+    const auto has = [&](int64_t s) {
+        const int64_t lo = p.cu[s], hi = p.cu[s + 1];
+        return lo >= 0 && lo <= t && t < hi && hi <= p.T;
+    };
+    int64_t s = 0;                                     // the last one that starts at t or before
+    for (int64_t n = p.nseq; n > 1;) {
+        const int64_t half = n >> 1;
+        if (p.cu[s + half] <= t) s += half;
+        n -= half;
+    }
+    bool found = has(s);
+    for (int64_t s0 = 0; s0 < p.nseq && !found; s0 += 32) {
+        const int64_t i = s0 + (threadIdx.x & 31);
+        found = __any_sync(0xffffffffu, i < p.nseq && has(i));
+    }
+    return found;
+}
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_lin_group_sum(const LinArgs p, const float* part, T* out, int group) {
     const int64_t Hk = p.Hv / group;
-    int64_t lo = 0, hi = p.T;
-    if (p.cu) {                                        // rows of no sequence stay as they were
-        lo = p.cu[0];
-        hi = p.cu[p.nseq];
-        if (lo < 0 || hi > p.T || hi < lo) return;
-    }
-    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, row = v >> 5;
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x, row = v >> 5;   // a warp to a row
     const int64_t bh = row / p.T, t = row - bh * p.T, b = bh / Hk, h = bh - b * Hk;
     const int c = 4 * (int)(v & 31);
-    if (bh >= p.B * Hk || t < lo || t >= hi) return;
+    if (bh >= p.B * Hk || (p.cu && !lin_has_row(p, t))) return;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int g = 0; g < group; ++g) {
         const float4 f = *reinterpret_cast<const float4*>(

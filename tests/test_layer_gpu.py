@@ -920,3 +920,28 @@ def test_linear_padded_rows_may_hold_anything(lib, dtype):
             for o in (got, also):
                 assert torch.equal(o[b, :, :n], good[b, :, :n]), (b, n)
                 assert not o[b, :, n:].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hv", [2, 6])
+@pytest.mark.parametrize("cu,fine", [([0, 100, 200, 420], (0, 1)), ([-8, 60, 160, 300], (1, 2)),
+                                     ([0, 130, 90, 90], (0, 2)), ([0, 100, 600, 640], (0,))])
+def test_linear_bad_bounds_leave_the_others(lib, dtype, Hv, cu, fine):
+    """A sequence whose bounds break the rule is left out, wherever it stands:
+    the others have their results, and all other rows stay as they were."""
+    c = linear_case(14, dtype, 1, 2, Hv, 400, [1, 1, 1], True)
+    c["cu"] = torch.tensor(cu, dtype=torch.int32).cuda()
+    rows = [slice(cu[i], cu[i + 1]) for i in fine]
+    O, S = run_forward(c, 0.7)
+    got = run_backward(c, 0.7)
+    assert gdn.gdn_get_status() == gdn.GDN_ERR_ARG
+    seen = torch.zeros(400, dtype=torch.bool)
+    for i, r in zip(fine, rows):
+        part = {x: c[x][:, :, r].contiguous() for x in ("Q", "K", "V", "dO")}
+        one = dict(c, **part, cu=torch.tensor([0, r.stop - r.start], dtype=torch.int32).cuda(),
+                   S0=c["S0"][i:i + 1].contiguous(), dS=c["dS"][i:i + 1].contiguous(), rows=[0])
+        for a, b in zip((O, *got[:3]), (run_forward(one, 0.7)[0], *run_backward(one, 0.7)[:3])):
+            assert torch.equal(a[:, :, r], b)
+        seen[r] = True
+    for a in (O, *got[:3]):
+        assert (a[:, :, ~seen] == 77.0).all()
