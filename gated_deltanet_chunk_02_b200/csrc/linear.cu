@@ -56,8 +56,14 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
     }
     if (g.m < 2) return;
     const double lg = lin_log2(p.loggate, hv);
-    const float a_full = lin_pow(lg, p.seg_len);
-    const float a_last = lin_pow(lg, g.seq_n - (g.m - 1) * p.seg_len);
+    float full, full_lo, last, last_lo;                // a decay's own rounding would add up
+    lin_pow2(lg, p.seg_len, full, full_lo);
+    lin_pow2(lg, g.seq_n - (g.m - 1) * p.seg_len, last, last_lo);
+    const auto decayed = [&](const float4& m, bool whole, const float4& u) {
+        const float a = whole ? full : last, l = whole ? full_lo : last_lo;
+        return make_float4(fmaf(a, m.x, fmaf(l, m.x, u.x)), fmaf(a, m.y, fmaf(l, m.y, u.y)),
+                           fmaf(a, m.z, fmaf(l, m.z, u.z)), fmaf(a, m.w, fmaf(l, m.w, u.w)));
+    };
     // a share of the state's elements, four to a thread at a time
     const int share = kLinState / gridDim.y;
     for (int e = blockIdx.y * share + 4 * threadIdx.x; e < (blockIdx.y + 1) * share;
@@ -87,19 +93,14 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
             for (int j = 0; j < kAhead; ++j) {
                 const int i = i0 + j;
                 if (i >= g.m - 1) break;
-                const float a = q.reverse && i == 0 ? a_last : a_full;
-                m = make_float4(fmaf(a, m.x, u[j].x), fmaf(a, m.y, u[j].y), fmaf(a, m.z, u[j].z),
-                                fmaf(a, m.w, u[j].w));
+                m = decayed(m, !(q.reverse && i == 0), u[j]);
                 base[(q.reverse ? g.m - 2 - i : i) * step] = m;
             }
         }
         if (q.mout) {                                  // the walk's last segment left its part here
             float4* const out =
                 reinterpret_cast<float4*>(q.mout + (seq * p.Hv + hv) * kLinState + e);
-            const float a = q.reverse ? a_full : a_last;
-            const float4 u = *out;
-            *out = make_float4(fmaf(a, m.x, u.x), fmaf(a, m.y, u.y), fmaf(a, m.z, u.z),
-                               fmaf(a, m.w, u.w));
+            *out = decayed(m, q.reverse, *out);
         }
     }
 }
@@ -158,6 +159,7 @@ struct SimtSmem {
     float m[kSimtDV][kPitchD];                         // the state slice
     float pm[kSimtC][kPitchC];                         // weights of the chunk
     float dec[kSimtC + 1];                             // lambda^0 .. lambda^64
+    float an[2], an_lo[2];                             // lambda^n, a whole chunk's and the last one's
     int odd;                                           // a value was infinite or NaN
     LinFound found;
 };
@@ -173,6 +175,8 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
     const double lg = lin_log2(p.loggate, hv);
     if (tid <= kSimtC) s.dec[tid] = lin_pow(lg, tid);
     if (tid == 0) s.odd = 0;
+    const int last = (int)((g.n - 1) % kSimtC + 1);    // rows of the last chunk
+    if (tid < 2) lin_pow2(lg, tid ? last : kSimtC, s.an[tid], s.an_lo[tid]);
     // incoming state
     for (int e = tid; e < kSimtDV * kLinD; e += kSimtThreads) {
         const int r = e / kLinD, c = e % kLinD;
@@ -334,7 +338,8 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
         {   // state: rows cr + 8 u (values), columns 4 kc .. 4 kc + 3 (keys)
             const int cr = tid >> 5, kc = 4 * (tid & 31);
             float4 acc[4];
-            const float an = s.dec[n];
+            // as two floats: one's rounding is every chunk's and would add up
+            const float an = s.an[n < kSimtC], al = s.an_lo[n < kSimtC];
 #pragma unroll
             for (int u = 0; u < 4; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
@@ -368,8 +373,10 @@ __device__ void simt_segment(const LinArgs& p, const LinProblem& q, const LinSeg
             for (int u = 0; u < 4; ++u) {
                 float4* m = reinterpret_cast<float4*>(&s.m[cr + 8 * u][kc]);
                 const float4 o = *m;
-                *m = make_float4(fmaf(an, o.x, acc[u].x), fmaf(an, o.y, acc[u].y),
-                                 fmaf(an, o.z, acc[u].z), fmaf(an, o.w, acc[u].w));
+                *m = make_float4(fmaf(an, o.x, fmaf(al, o.x, acc[u].x)),
+                                 fmaf(an, o.y, fmaf(al, o.y, acc[u].y)),
+                                 fmaf(an, o.z, fmaf(al, o.z, acc[u].z)),
+                                 fmaf(an, o.w, fmaf(al, o.w, acc[u].w)));
             }
         }
     }

@@ -945,3 +945,40 @@ def test_linear_bad_bounds_leave_the_others(lib, dtype, Hv, cu, fine):
         seen[r] = True
     for a in (O, *got[:3]):
         assert (a[:, :, ~seen] == 77.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hv", [148, 1])
+def test_linear_slow_decay_over_many_steps(lib, dtype, Hv):
+    """The state's decay over a step (a chunk of 64 or 128 rows, or a segment) is
+    one number, whose rounding to a float would come back at every step: over s
+    steps a mean of s 2^-26 of the state for the decays taken here, which round
+    by 2^-25.4 and more.  What stays is a rounding at each of the state's updates
+    (2^-24, uniform: / sqrt 3, in quadrature over steps) and the sums of 64 or
+    128 products before it, counted as three more such roundings."""
+    T, Hk = 16384, 1
+    gd = torch.Generator(device="cuda")
+    gd.manual_seed(71)
+    rnd = lambda h: torch.randn(1, h, T, 128, generator=gd, device="cuda").to(DT[dtype])
+    K, V = rnd(Hk), rnd(Hv)
+    n = gdn.gdn_linear_forward_workspace_bytes(K, V)
+    step = 64 if dtype == "f32" else 128
+    if n:                                              # the length of a segment
+        m = n // (Hv * 65536) + 1
+        step = -(-(T // 128) // m) * 128
+    assert (n > 0) == (Hv == 1)
+    tries = -np.float32(1e-5) * (1 + np.arange(200, dtype=np.float32) / 128)
+    lam = np.exp(tries.astype(np.float64) * step)
+    off = np.abs(lam.astype(np.float32).astype(np.float64) / lam - 1)
+    lg = torch.full((Hv,), float(tries[off.argmax()]), device="cuda")
+    assert off.max() >= 2.0 ** -25.4
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    O, S = torch.empty_like(V), torch.empty(1, Hv, 128, 128, device="cuda")
+    gdn.gdn_linear_forward(K, K, V, lg, None, O, S, ws, scale=128 ** -0.5)
+    w = torch.exp(lg[0].double() * torch.arange(T - 1, -1, -1, device="cuda"))
+    steps = T // min(step, 64 if dtype == "f32" else 128)
+    tol = 4 * (steps / 3) ** 0.5 * U32
+    for h in {0, Hv // 2, Hv - 1}:
+        want = (V[0, h].double() * w[:, None]).T @ K[0, 0].double()
+        err = float((S[0, h].double() - want).norm() / want.norm())
+        assert err <= tol, (h, err, tol)
