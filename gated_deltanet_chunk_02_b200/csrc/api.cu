@@ -832,6 +832,16 @@ int gdn_debug_arm_wait_expiry(int tile, int load, double timeout_ms) {
     return GDN_OK;
 }
 
+int gdn_debug_arm_linear_expiry(int block, int kernel, double timeout_ms) {
+    if (block < 0) return fail(GDN_ERR_ARG, "block=%d is negative", block);
+    if (kernel != 0 && kernel != 1)
+        return fail(GDN_ERR_ARG, "kernel=%d is neither 0 (outputs) nor 1 (states)", kernel);
+    if (!(timeout_ms > 0.0 && timeout_ms <= 2000.0))
+        return fail(GDN_ERR_ARG, "timeout_ms=%g outside (0, 2000]", timeout_ms);
+    gdn::arm_linear_expiry(block, kernel == 1, (unsigned long long)(timeout_ms * 1e6));
+    return GDN_OK;
+}
+
 const char* gdn_last_error(void) { return t_last_error.c_str(); }
 
 int64_t gdn_launch_count(void) { return t_launches; }

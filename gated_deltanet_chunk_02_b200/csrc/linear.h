@@ -250,6 +250,8 @@ cudaError_t launch_linear(const LinArgs& a, int nprob, const LinPlan& pl, bool b
 // one of the two tensor-core kernels (linear_tc.cu): the boundary states, or the outputs
 cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, bool states,
                              cudaStream_t st);
+// the next launch of one of them: block `block` waits for a tile that never comes
+void arm_linear_expiry(int block, bool states, unsigned long long limit_ns);
 // out[b, h] = sum of part[b, h * group + g] over g, float32 -> the data type
 cudaError_t launch_linear_group_sum(const LinArgs& a, const float* part, void* out, int group,
                                     bool bf16, cudaStream_t st);

@@ -64,6 +64,14 @@ struct LinTcArgs {
     CUtensorMap out[kLinProblems];                     // bf16 outputs
     int8_t ia[kLinProblems], ib[kLinProblems], ic[kLinProblems];
     LinArgs a;
+    unsigned long long limit_ns;                       // of a wait
+    int withhold;                                      // tests: this block's last tile never comes
+};
+
+// A block's end without its work done: who has given up, and when to.
+struct LtStop {
+    unsigned long long limit_ns;
+    int abort;
 };
 
 struct __align__(16) LtCtrl {
@@ -77,7 +85,7 @@ struct __align__(16) LtCtrl {
     float d[kRows];                                    // of a whole chunk
     float an[2], an_lo[2], lambda;
     uint32_t tmem;
-    int abort;
+    LtStop stop;
     int odd;                                           // a state row ended as NaN
     __align__(16) int odd_from[kRows];                 // by column of c: lt_scan
 };
@@ -89,18 +97,18 @@ static_assert(offsetof(LtCtrl, step) % 16 == 0 && offsetof(LtCtrl, odd_from) % 1
 // Bounded wait; false once it ran out or another role's did.  The loop is a
 // function of its own: a dozen copies of it would not leave the roles' code in
 // the instruction cache.
-__device__ __noinline__ bool lt_wait_long(uint64_t* b, uint32_t parity, int* abort, int* status) {
+__device__ __noinline__ bool lt_wait_long(uint64_t* b, uint32_t parity, LtStop* stop, int* status) {
     unsigned long long t0 = 0;
     for (int i = 0;; ++i) {
         if (mbar_try(b, parity)) return true;
         if ((i & 63) == 63) {
-            if (*(volatile int*)abort) return false;
+            if (*(volatile int*)&stop->abort) return false;
             const unsigned long long t = gtime();
             if (!t0) t0 = t;
-            if (t - t0 > kTimeoutNs) break;
+            if (t - t0 > stop->limit_ns) break;
         }
     }
-    atomicExch(abort, 1);
+    atomicExch(&stop->abort, 1);
     raise_status(status, kStatusTimeout);
     return false;
 }
@@ -113,12 +121,12 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
         : "=r"(ok) : "r"(su32(b)), "r"(parity) : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
-    return mbar_try(b, parity) || lt_wait_long(b, parity, abort, status);
+__device__ __forceinline__ bool lt_wait(uint64_t* b, uint32_t parity, LtStop* stop, int* status) {
+    return mbar_try(b, parity) || lt_wait_long(b, parity, stop, status);
 }
 // the same for a whole warp, with one answer
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int* abort, int* status) {
-    return __all_sync(0xffffffffu, lt_wait(b, parity, abort, status));
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, LtStop* stop, int* status) {
+    return __all_sync(0xffffffffu, lt_wait(b, parity, stop, status));
 }
 
 // The upper 16 bits of both (truncated to bf16) as a pair, and what is left.
@@ -318,15 +326,15 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
     const CUtensorMap *mb = &k.map[k.ib[z]], *ma = &k.map[k.ia[z]], *mc = &k.map[k.ic[z]];
     const int yb = lt_row0(k.a, g, hv, q.gb), ya = lt_row0(k.a, g, hv, q.ga),
               yc = lt_row0(k.a, g, hv, q.gc);
-    const int tiles = 3 * wk.nch;
+    const int tiles = 3 * wk.nch - (blockIdx.x == (unsigned)k.withhold);
     Ring<kLtRing> at;
     int t = 0, m = 0, r0 = wk.first(0);
     for (; t < tiles; ++t) {
         const int s = at.slot;
-        if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, &c->abort, k.a.status)) break;
+        if (t >= kLtRing && !lt_wait(&c->empty[s], at.phase ^ 1, &c->stop, k.a.status)) break;
         // c comes where the c of two chunks ago was, and after that chunk's outputs
         if (m == 2 && t >= kLtRing &&
-            !lt_wait(&c->stored[t / 3 & 1], ((t / 3 - 2) >> 1) & 1, &c->abort, k.a.status))
+            !lt_wait(&c->stored[t / 3 & 1], ((t / 3 - 2) >> 1) & 1, &c->stop, k.a.status))
             break;
         const CUtensorMap* mp = m == 0 ? mb : (m == 1 ? ma : mc);
         const int y = r0 + (m == 0 ? yb : (m == 1 ? ya : yc));
@@ -345,7 +353,7 @@ __device__ void lt_load(const LinTcArgs& k, const LinProblem& q, const LinSeg& g
 __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* status) {
     const uint32_t tSc = __shfl_sync(0xffffffffu, c->tmem, 0), tO = tSc + 128, tMu = tSc + 256;
     const uint32_t tPart = tSc + 384, m_tile = tiles + kLtRing * kLtTile;
-    int* const ab = &c->abort;
+    LtStop* const ab = &c->stop;
     const bool lead = elect_one();
     bool ahead = false;
     Ring<kLtRing> at;
@@ -398,12 +406,15 @@ __device__ void lt_multiply(const LtWalk& wk, uint32_t tiles, LtCtrl* c, int* st
         if (!wk.exact && ci + 1 < wk.nch) {
             Ring<kLtRing> a1 = at;
             a1.next();
-            while (!ahead && !__all_sync(0xffffffffu, mbar_test(&c->parts, par))) {
+            // (a look takes 50 cycles or more; after a million of them, 30 ms, the
+            // wait for the parts below decides)
+            for (int look = 0; look < (1 << 20) && !ahead &&
+                               !__all_sync(0xffffffffu, mbar_test(&c->parts, par)); ++look) {
                 ahead = __all_sync(0xffffffffu, mbar_test(&c->full[at.slot], at.phase) &&
                                                     mbar_test(&c->full[a1.slot], a1.phase) &&
                                                     mbar_test(&c->o, par));
-                // the rows' own wait ran out
-                if (__any_sync(0xffffffffu, *(volatile int*)ab)) break;
+                // another role's wait ran out
+                if (__any_sync(0xffffffffu, *(volatile int*)&ab->abort)) break;
             }
             if (ahead) {
                 tc_fence_after();
@@ -523,7 +534,7 @@ __device__ void lt_store(const LtWalk& wk, const LinProblem& q, const CUtensorMa
         const uint8_t* tile = smem + at.slot * kLtTile;
         at.next();
         const int r0 = wk.first(ci);
-        if (!lt_wait(&c->staged[ci & 1], (ci >> 1) & 1, &c->abort, status)) break;
+        if (!lt_wait(&c->staged[ci & 1], (ci >> 1) & 1, &c->stop, status)) break;
         if (wk.rows(r0) == kRows && !q.out_f32) {
             tma_store_2d(map, 0, row + r0, tile);
             tma_store_2d(map, 64, row + r0, tile + kRows * 128);
@@ -583,8 +594,8 @@ __device__ __forceinline__ void lt_rows(const LinArgs& p, const LinProblem& q, c
         if (ci > 0) {                                  // the last chunk's outputs, while Mu is formed
             const int r0 = wk.first(ci - 1);
             // parts: the other warps have read c too
-            if (!warp_wait(&c->parts, (ci - 1) & 1, &c->abort, p.status) ||
-                !warp_wait(&c->o, (ci - 1) & 1, &c->abort, p.status))
+            if (!warp_wait(&c->parts, (ci - 1) & 1, &c->stop, p.status) ||
+                !warp_wait(&c->o, (ci - 1) & 1, &c->stop, p.status))
                 break;
             tc_fence_after();
             lt_output<CAREFUL>(tO, q.s_out * d, wk.rows(r0), r, h, orow + r0, q, c_tile, c,
@@ -594,7 +605,7 @@ __device__ __forceinline__ void lt_rows(const LinArgs& p, const LinProblem& q, c
             const int n = wk.rows(wk.first(ci));
             d = c->d[rev ? min(r + kRows - n, kRows - 1) : r];
             const float inv = 1.f / d;
-            if (!warp_wait(&c->sc, ci & 1, &c->abort, p.status)) break;
+            if (!warp_wait(&c->sc, ci & 1, &c->stop, p.status)) break;
             tc_fence_after();
 #pragma unroll 1
             for (int pc = 0; pc < 2; ++pc) {
@@ -666,14 +677,14 @@ __device__ __forceinline__ void lt_rows(const LinArgs& p, const LinProblem& q, c
             at.next();
             c_tile = v.tile(tiles);
             if (CAREFUL) {
-                if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status)) break;
+                if (!warp_wait(&c->full[v.slot], v.phase, &c->stop, p.status)) break;
                 if (r < n) lt_scan(c_tile, r, h, wk.place(ci, r), c);
             }
             tc_fence_before();
             warp_arrive(&c->p, lane);
             // the parts of w c, once the last chunk's have been read
-            if (!warp_wait(&c->full[v.slot], v.phase, &c->abort, p.status) ||
-                (ci > 0 && !warp_wait(&c->mu, (ci - 1) & 1, &c->abort, p.status)))
+            if (!warp_wait(&c->full[v.slot], v.phase, &c->stop, p.status) ||
+                (ci > 0 && !warp_wait(&c->mu, (ci - 1) & 1, &c->stop, p.status)))
                 break;
             tc_fence_after();
             const float* w = c->w[n < kRows];
@@ -682,7 +693,7 @@ __device__ __forceinline__ void lt_rows(const LinArgs& p, const LinProblem& q, c
             else
                 split_c<2>(v.tile(tiles), quarter, 64 * h, n, w, tPart, tPart + kLtPart, 0);
             if (n < kRows) {                           // rows of others may hold NaN
-                if (!warp_wait(&c->full[b.slot], b.phase, &c->abort, p.status)) break;
+                if (!warp_wait(&c->full[b.slot], b.phase, &c->stop, p.status)) break;
                 if (r >= n) {
                     zero_row(b.tile(tiles), r, h);
                     zero_row(v.tile(tiles), r, h);
@@ -741,7 +752,7 @@ __device__ __forceinline__ void lt_state(const LinArgs& p, const LinProblem& q, 
         fence_async_smem();
         tc_fence_before();
         warp_arrive(&c->state, lane);
-        if (!warp_wait(&c->mu, ci & 1, &c->abort, p.status)) return;
+        if (!warp_wait(&c->mu, ci & 1, &c->stop, p.status)) return;
         tc_fence_after();
         const int part = wk.rows(wk.first(ci)) < kRows;
         take_update(tMu, c->an[part], c->an_lo[part], m);
@@ -927,7 +938,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     const int hv = g.hv, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         lt_barriers(c);
-        c->abort = 0;
+        c->stop = {k.limit_ns, 0};
         c->odd = 0;
     }
     if (warp == 17) tmem_alloc(&c->tmem, 512);
@@ -956,7 +967,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) k_linear_tc(const __grid_consta
     __syncthreads();
     tc_fence_after();
     lt_turn<false>(k, q, g, wk, smem, c);
-    if (c->odd && !c->abort) {
+    if (c->odd && !c->stop.abort) {
         lt_again(k);
         return;
     }
@@ -982,7 +993,7 @@ struct __align__(16) LsCtrl {
     float an[2], an_lo[2];
     LinFound found;
     uint32_t tmem;
-    int abort;
+    LtStop stop;
 };
 constexpr int kLsSmem = kLsRing * kLtTile + (int)sizeof(LsCtrl);
 static_assert(kLsSmem <= 232448, "shared memory budget");
@@ -1016,7 +1027,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
         mbar_init(&c->mu, 1);
         mbar_init(&c->taken, 8);
         mbar_init(&c->drain, 1);
-        c->abort = 0;
+        c->stop = {k.limit_ns, 0};
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 17) tmem_alloc(&c->tmem, 512);
@@ -1036,7 +1047,7 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
     tc_fence_after();
     // TMEM: Mu, then two sets of hi, mid, lo
     const uint32_t tm = c->tmem, tiles = su32(smem), tPart = tm + 128;
-    int* const ab = &c->abort;
+    LtStop* const ab = &c->stop;
     if (warp == 16) {
         if (lane == 0) {
             const int z = g.z;
@@ -1044,7 +1055,8 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
             const int yb = lt_row0(p, g, hv, q.gb), yc = lt_row0(p, g, hv, q.gc);
             Ring<kLsRing> at;
             int t = 0, r0 = wk.first(0);
-            for (; t < 2 * wk.nch; ++t) {              // c first: its parts are made of it
+            const int tiles = 2 * wk.nch - (blockIdx.x == (unsigned)k.withhold);
+            for (; t < tiles; ++t) {              // c first: its parts are made of it
                 const int s = at.slot, y = r0 + (t & 1 ? yb : yc);
                 if (t >= kLsRing && !lt_wait(&c->empty[s], at.phase ^ 1, ab, p.status)) break;
                 mbar_expect_tx(&c->full[s], kLtTile);
@@ -1144,12 +1156,31 @@ k_linear_state_tc(const __grid_constant__ LinTcArgs k) {
 
 }  // namespace tcg
 
+// tests of the bounded waits (gdn_debug_arm_linear_expiry): the next launch of
+// one kernel on this thread withholds a block's last tile
+static thread_local int t_withhold = -1;
+static thread_local bool t_withhold_states = false;
+static thread_local unsigned long long t_withhold_ns = 0;
+
+void arm_linear_expiry(int block, bool states, unsigned long long limit_ns) {
+    t_withhold = block;
+    t_withhold_states = states;
+    t_withhold_ns = limit_ns;
+}
+
 // the distinct tensors of the call's problems, by pointer and heads
 cudaError_t launch_linear_tc(const LinArgs& a, int nprob, const LinPlan& pl, bool states,
                              cudaStream_t st) {
     tcg::LinTcArgs k;
     memset(&k, 0, sizeof k);
     k.a = a;
+    k.limit_ns = tcg::kTimeoutNs;
+    k.withhold = -1;
+    if (t_withhold >= 0 && t_withhold_states == states) {
+        k.withhold = t_withhold;
+        k.limit_ns = t_withhold_ns;
+        t_withhold = -1;
+    }
     const void* seen[4] = {nullptr, nullptr, nullptr, nullptr};
     int group_of[4] = {0, 0, 0, 0}, count = 0;
     auto map_of = [&](const void* t, int group) -> int {

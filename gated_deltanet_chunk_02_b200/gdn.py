@@ -35,6 +35,7 @@ EXPORTS = [
     "gdn_linear_forward_workspace_bytes", "gdn_linear_backward",
     "gdn_linear_backward_workspace_bytes", "gdn_linear_decode", "gdn_block_norm",
     "gdn_block_norm_backward", "gdn_block_norm_backward_workspace_bytes",
+    "gdn_debug_arm_linear_expiry",
 ]
 GDN_ACT = {"sigmoid": 0, "silu": 1}
 GDN_ROTARY = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -117,6 +118,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "gdn_block_norm_backward_workspace_bytes": [_I64, _I64, _I64, _I64],
         "gdn_get_status": [_P],
         "gdn_debug_arm_wait_expiry": [_I, _I, ctypes.c_double],
+        "gdn_debug_arm_linear_expiry": [_I, _I, ctypes.c_double],
         "gdn_last_error": [],
         "gdn_launch_count": [],
     }
@@ -579,6 +581,14 @@ def gdn_debug_arm_wait_expiry(tile: int, which: str, timeout_ms: float) -> None:
     ``timeout_ms`` (the wait runs out, the status word reports
     GDN_ERR_TIMEOUT)."""
     _check(load().gdn_debug_arm_wait_expiry(int(tile), {"K": 0, "V": 1}[which], float(timeout_ms)))
+
+
+def gdn_debug_arm_linear_expiry(block: int, kernel: str, timeout_ms: float) -> None:
+    """Tests only: the same for linear attention on bf16 data; block ``block`` of
+    the next launch of its ``"outputs"`` or ``"states"`` kernel waits for a tile
+    that never comes."""
+    _check(load().gdn_debug_arm_linear_expiry(int(block), {"outputs": 0, "states": 1}[kernel],
+                                              float(timeout_ms)))
 
 
 def gdn_last_error() -> str:

@@ -507,6 +507,16 @@ int gdn_get_status(void* stream);
  */
 int gdn_debug_arm_wait_expiry(int tile, int load, double timeout_ms);
 
+/*
+ * The same for the linear attention calls on bf16 data: in the next launch on
+ * this host thread of their output kernel (`kernel` = 0) or of their state
+ * kernel (1, launched where sequences are cut), block `block` never loads its
+ * last tile, and waits are bounded by `timeout_ms`.  That block gives up as
+ * above; the others finish.  GDN_ERR_ARG for a negative block, another kernel,
+ * or timeout_ms outside (0, 2000].
+ */
+int gdn_debug_arm_linear_expiry(int block, int kernel, double timeout_ms);
+
 /* Message for the most recent nonzero return on this host thread. */
 const char* gdn_last_error(void);
 

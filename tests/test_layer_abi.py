@@ -133,6 +133,13 @@ def test_linear_more_heads_than_a_grid(lib):
             assert f(lib, s=s, cu=cu) == gdn.GDN_ERR_ARG and "too many" in last(lib)
 
 
+def test_linear_expiry_hook_arguments(lib):
+    f = lib.gdn_debug_arm_linear_expiry
+    for block, kernel, ms in [(-1, 0, 5.0), (0, 2, 5.0), (0, 0, 0.0), (0, 1, 2500.0),
+                              (0, 1, float("nan"))]:
+        assert f(block, kernel, ctypes.c_double(ms)) == gdn.GDN_ERR_ARG
+
+
 def test_linear_workspace_sizes(lib):
     f, b = lib.gdn_linear_forward_workspace_bytes, lib.gdn_linear_backward_workspace_bytes
     for dtype in (BF16, F32):

@@ -982,3 +982,28 @@ def test_linear_slow_decay_over_many_steps(lib, dtype, Hv):
         want = (V[0, h].double() * w[:, None]).T @ K[0, 0].double()
         err = float((S[0, h].double() - want).norm() / want.norm())
         assert err <= tol, (h, err, tol)
+
+
+# --------------------------------------------------------------------------- #
+# waits that run out
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("T,lens,kernel,block,backward", [
+    (200, None, "outputs", 1, False), (1100, [900, 150, 50], "outputs", 0, False),
+    (2600, None, "outputs", 3, False), (2600, None, "states", 2, False),
+    (300, None, "outputs", 4, True), (2600, None, "states", 2, True),
+])
+def test_linear_expired_wait_reports_and_the_next_call_is_clean(lib, T, lens, kernel, block,
+                                                                backward):
+    """A tile that never comes: all of the block's roles give up within the
+    bound, the status word says so, and the next call has the bits of one before."""
+    c = linear_case(80, "bf16", 1, 2, 2, T, lens, True)
+    run = (lambda: run_backward(c, 0.7)) if backward else (lambda: run_forward(c, 0.7))
+    want = run()
+    assert gdn.gdn_get_status() == gdn.GDN_OK
+    gdn.gdn_debug_arm_linear_expiry(block, kernel, 5.0)
+    run()
+    assert gdn.gdn_get_status() == gdn.GDN_ERR_TIMEOUT
+    assert "ran out" in gdn.gdn_last_error()
+    got = run()
+    assert gdn.gdn_get_status() == gdn.GDN_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
