@@ -150,6 +150,16 @@ int check_linear(const gdn_linear_shape& s, const int32_t* cu, gdn_dtype dtype) 
     return GDN_OK;
 }
 
+// bytes of a linear attention call's tensors
+struct LinearBytes {
+    int64_t k, v, state, decay, cu;
+    LinearBytes(const gdn_linear_shape& s, gdn_dtype dt)
+        : k(s.B * s.Hk * s.T * s.d * (dt == GDN_BF16 ? 2 : 4)),
+          v(s.B * s.Hv * s.T * s.d * (dt == GDN_BF16 ? 2 : 4)),
+          state((s.nseq > 0 ? s.nseq : s.B) * s.Hv * s.d * s.d * 4), decay(s.Hv * 4),
+          cu((s.nseq + 1) * 4) {}
+};
+
 // Outputs that are an input (or one another) by pointer.
 int check_apart(std::initializer_list<std::pair<const void*, const char*>> outs,
                 std::initializer_list<std::pair<const void*, const char*>> ins) {
@@ -159,6 +169,81 @@ int check_apart(std::initializer_list<std::pair<const void*, const char*>> outs,
             if (o->first == i.first) return fail(GDN_ERR_ARG, "%s is %s", o->second, i.second);
         for (auto p = o + 1; p != outs.end(); ++p)
             if (o->first == p->first) return fail(GDN_ERR_ARG, "%s is %s", p->second, o->second);
+    }
+    return GDN_OK;
+}
+
+// Rows of bytes at up to three strides (of bytes): a tensor as it lies in memory.
+struct Rows {
+    const void* p;
+    int64_t row, st[3], n[3];
+    const char* name;
+};
+Rows flat(const void* p, int64_t bytes, const char* name) {
+    return {p, bytes, {0, 0, 0}, {1, 1, 1}, name};
+}
+Rows strided(const void* p, const gdn_strides& s, int64_t B, int64_t H, int64_t T, int64_t d,
+             int64_t elem, const char* name) {
+    return {p, d * elem, {s.b * elem, s.h * elem, s.t * elem}, {B, H, T}, name};
+}
+
+// Does at + sum st_i x_i fall into [lo, hi] for some lo_i <= x_i <= hi_i?  Terms
+// by stride, the largest first: what the others can still add leaves a nested
+// layout one or two x to try at each.  One that leaves thousands counts as yes.
+struct Term {
+    __int128 st, lo, hi;
+};
+bool falls_in(const Term* t, int n, __int128 at, __int128 lo, __int128 hi, int& tries) {
+    if (n == 0) return lo <= at && at <= hi;
+    __int128 below = 0, above = 0;
+    for (int i = 1; i < n; ++i) {
+        below += t[i].st * t[i].lo;
+        above += t[i].st * t[i].hi;
+    }
+    const auto floor_div = [](__int128 a, __int128 b) { return a >= 0 ? a / b : -((b - 1 - a) / b); };
+    __int128 x0 = -floor_div(at + above - lo, t->st), x1 = floor_div(hi - at - below, t->st);
+    if (x0 < t->lo) x0 = t->lo;
+    if (x1 > t->hi) x1 = t->hi;
+    for (__int128 x = x0; x <= x1; ++x)
+        if (--tries < 0 || falls_in(t + 1, n - 1, at + t->st * x, lo, hi, tries)) return true;
+    return false;
+}
+// Do two tensors have a byte in common?  A row of b starts at a distance of
+// above -b.row and below a.row from one of a.
+bool share_memory(const Rows& a, const Rows& b) {
+    Term t[6];
+    int n = 0;
+    const auto add = [&](int64_t st, int64_t lo, int64_t hi) {
+        if (st == 0 || (lo == 0 && hi == 0)) return;
+        int i = 0;
+        while (i < n && t[i].st > st) ++i;
+        if (i < n && t[i].st == st) {
+            t[i].lo += lo;
+            t[i].hi += hi;
+            return;
+        }
+        for (int j = n++; j > i; --j) t[j] = t[j - 1];
+        t[i] = {st, lo, hi};
+    };
+    for (int i = 0; i < 3; ++i) {
+        if (a.n[i] <= 0 || b.n[i] <= 0) return false;
+        add(b.st[i], 0, b.n[i] - 1);
+        add(a.st[i], 1 - a.n[i], 0);
+    }
+    if (!a.p || !b.p || a.row <= 0 || b.row <= 0) return false;
+    int tries = 4096;
+    return falls_in(t, n, (__int128)(intptr_t)b.p - (intptr_t)a.p, 1 - b.row, a.row - 1, tries);
+}
+// Outputs share no memory with inputs or one another (an input that may be an
+// output in place is left out by the caller).
+int check_memory(std::initializer_list<Rows> outs, std::initializer_list<Rows> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (auto& i : ins)
+            if (share_memory(*o, i))
+                return fail(GDN_ERR_ARG, "%s shares memory with %s", o->name, i.name);
+        for (auto p = o + 1; p != outs.end(); ++p)
+            if (share_memory(*o, *p))
+                return fail(GDN_ERR_ARG, "%s shares memory with %s", p->name, o->name);
     }
     return GDN_OK;
 }
@@ -572,6 +657,15 @@ int gdn_rotary(const void* Q, gdn_strides qs, void* Q_out, gdn_strides qos, cons
         GDN_TRY(check_apart({{Q_out, "Q_out"}}, {{K, "K"}}));
         GDN_TRY(check_apart({{K_out, "K_out"}}, {{Q, "Q"}}));
     }
+    const int64_t el = dtype == GDN_BF16 ? 2 : 4;
+    const auto rows = [&](const void* p, const gdn_strides& s, int64_t H, const char* name) {
+        return strided(H > 0 ? p : nullptr, s, B, H, T, d, el, name);
+    };
+    GDN_TRY(check_memory({rows(Q_out, qos, Hq, "Q_out"), rows(K_out, kos, Hk, "K_out")},
+                         {rows(Q == Q_out ? nullptr : Q, qs, Hq, "Q"),
+                          rows(K == K_out ? nullptr : K, ks, Hk, "K"),
+                          flat(positions, B * T * 8, "positions"),
+                          flat(inv_freq, rot / 2 * 4, "inv_freq")}));
     gdn::RotaryArgs a;
     memset(&a, 0, sizeof a);
     a.Q = Q; a.qs = qs; a.Qo = Q_out; a.qos = qos;
@@ -607,6 +701,12 @@ int gdn_linear_forward(const void* Q, const void* K, const void* V, const float*
         return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
                     (long long)workspace_bytes, (long long)pl.state_bytes);
     if (pl.state_bytes > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
+    const LinearBytes n(s, dtype);
+    GDN_TRY(check_memory({flat(O, n.v, "O"), flat(S_final, n.state, "S_final"),
+                          flat(workspace, pl.state_bytes, "workspace")},
+                         {flat(Q, n.k, "Q"), flat(K, n.k, "K"), flat(V, n.v, "V"),
+                          flat(S0 == S_final ? nullptr : S0, n.state, "S0"),
+                          flat(loggate, n.decay, "loggate"), flat(cu_seqlens, n.cu, "cu_seqlens")}));
     const int group = (int)(s.Hv / s.Hk);
     gdn::LinArgs a = linear_args(s, loggate, cu_seqlens);
     a.pr[0] = {Q, K, V, O, group, group, 1, 0, 0, S0, 0, S_final, 1, scale, 1.f, 1.f, 0, nullptr};
@@ -647,6 +747,13 @@ int gdn_linear_backward(const void* Q, const void* K, const void* V, const float
         return fail(GDN_ERR_ARG, "workspace of %lld bytes is below the %lld needed",
                     (long long)workspace_bytes, (long long)need);
     if (need > 0) GDN_TRY(check_ptrs({{workspace, "workspace"}}));
+    const LinearBytes n(s, dtype);
+    GDN_TRY(check_memory({flat(dQ, n.k, "dQ"), flat(dK, n.k, "dK"), flat(dV, n.v, "dV"),
+                          flat(dS0, n.state, "dS0"), flat(workspace, need, "workspace")},
+                         {flat(Q, n.k, "Q"), flat(K, n.k, "K"), flat(V, n.v, "V"),
+                          flat(S0, n.state, "S0"), flat(dO, n.v, "dO"),
+                          flat(dS_final == dS0 ? nullptr : dS_final, n.state, "dS_final"),
+                          flat(loggate, n.decay, "loggate"), flat(cu_seqlens, n.cu, "cu_seqlens")}));
     const bool bf16 = dtype == GDN_BF16;
     const gdn::LinPlan pl = gdn::linear_plan(s, 3, bf16);
     const int group = (int)(s.Hv / s.Hk);
@@ -693,6 +800,15 @@ int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* 
     GDN_TRY(check_vec(loggate, 4, "loggate"));
     GDN_TRY(check_vec(slots, 4, "slots", true));
     GDN_TRY(check_apart({{O, "O"}, {S, "S"}}, {{Q, "Q"}, {K, "K"}, {V, "V"}}));
+    const int64_t row = n * d * (dtype == GDN_BF16 ? 2 : 4);
+    const auto all = [](int64_t a, int64_t b) {        // sizes have no bound of their own here
+        return b != 0 && a > INT64_MAX / b ? INT64_MAX : a * b;
+    };
+    const int64_t k = all(B * Hk, row), v = all(B * Hv, row);
+    GDN_TRY(check_memory({flat(O, v, "O"), flat(S, all(nslots, Hv * d * d * 4), "S")},
+                         {flat(Q, k, "Q"), flat(K, k, "K"), flat(V, v, "V"),
+                          flat(loggate, Hv * 4, "loggate"),
+                          flat(slots, B * 4, "slots")}));
     return launched(gdn::launch_linear_decode(Q, K, V, loggate, S, slots, nslots, scale, O, B, Hk,
                                               Hv, n, dtype == GDN_BF16, (cudaStream_t)stream),
                     "linear decode");
@@ -735,6 +851,11 @@ int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_
     GDN_TRY(check_apart({{X, "X"}, {N, "N"}},
                         {{Y, "Y"}, {Z, "Z"}, {w_post, "w_post"}, {w_pre, "w_pre"}}));
     GDN_TRY(check_apart({{N, "N"}}, {{R, "R"}}));
+    const int64_t el = dtype == GDN_BF16 ? 2 : 4, all = B * T * H * d * el;
+    GDN_TRY(check_memory({flat(X, all, "X"), flat(N, all, "N")},
+                         {strided(Y, ys, B, H, T, d, el, "Y"), flat(Z, all, "Z"),
+                          flat(R == X ? nullptr : R, all, "R"), flat(w_post, H * d * 4, "w_post"),
+                          flat(w_pre, H * d * 4, "w_pre")}));
     gdn::NormArgs a;
     memset(&a, 0, sizeof a);
     a.Y = Y; a.ys = ys; a.Z = Z; a.w_post = w_post; a.R = R; a.w_pre = w_pre;
@@ -794,6 +915,13 @@ int gdn_block_norm_backward(const void* Y, gdn_strides ys, const void* Z, const 
                         {{Y, "Y"}, {Z, "Z"}, {w_post, "w_post"}, {R, "R"}, {w_pre, "w_pre"},
                          {dN, "dN"}}));
     GDN_TRY(check_apart({{dY, "dY"}, {dZ, "dZ"}}, {{dX, "dX"}}));
+    const int64_t el = dtype == GDN_BF16 ? 2 : 4, all = B * T * H * d * el, w = H * d * 4;
+    GDN_TRY(check_memory({strided(dY, dys, B, H, T, d, el, "dY"), flat(dZ, all, "dZ"),
+                          flat(dR, all, "dR"), flat(dw_post, w, "dw_post"),
+                          flat(dw_pre, w, "dw_pre"), flat(workspace, need, "workspace")},
+                         {strided(Y, ys, B, H, T, d, el, "Y"), flat(Z, all, "Z"),
+                          flat(w_post, w, "w_post"), flat(R, all, "R"), flat(w_pre, w, "w_pre"),
+                          flat(dX == dR ? nullptr : dX, all, "dX"), flat(dN, all, "dN")}));
     gdn::NormArgs a;
     memset(&a, 0, sizeof a);
     a.Y = Y; a.ys = ys; a.Z = Z; a.w_post = w_post; a.R = R; a.w_pre = w_pre;

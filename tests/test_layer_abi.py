@@ -212,6 +212,80 @@ def test_norm_backward_refusals(lib):
     assert f(2, 4, 3, 128) > 0 and f(0, 4, 3, 128) == 0 and f(1, 1, 1, 12) == -1
 
 
+# ---- outputs on a part of an input, or of one another ----
+FAR = [0x1000000 * i for i in range(1, 24)]    # 16 MiB apart; never dereferenced
+
+
+def shares(lib, rc):
+    return rc == gdn.GDN_ERR_ARG and "shares memory" in last(lib)
+
+
+def test_rotary_outputs_on_parts_of_others(lib):
+    """[2, 4, 8, 128] bf16: 128 KiB each; the fused layout [2, 8, 12, 128]."""
+    s, f = st(4096 * 2, 1024, 128), st(8 * 12 * 128, 128, 12 * 128)
+
+    def call(q=FAR[0], qs=s, qo=FAR[1], qos=s, k=FAR[2], ks=s, ko=FAR[3], kos=s, pos=FAR[4],
+             inv=FAR[5]):
+        return lib.gdn_rotary(P(q), qs, P(qo), qos, P(k), ks, P(ko), kos, P(pos), P(inv), 1.0, 64, 0,
+                              0, 2, 4, 4, 8, 128, BF16, None)
+    end = 2 * 8192 + 0                                 # bytes of the first batch row
+    for kw in [dict(qo=FAR[0] + 256), dict(qo=FAR[0] - 256), dict(qo=FAR[2] + end),
+               dict(ko=FAR[1] + 16), dict(ko=FAR[0] + 1024), dict(ko=FAR[4]),
+               dict(qo=FAR[5] - 16 * 1024),
+               # a head further on in the fused layout; K's output on Q's last head in place
+               dict(q=FAR[0], qs=f, qo=FAR[0] + 256, qos=f),
+               dict(q=FAR[0], qs=f, qo=FAR[0], qos=f, k=FAR[2], ko=FAR[0] + 3 * 256, kos=f)]:
+        assert shares(lib, call(**kw)), kw
+
+
+def test_linear_outputs_on_parts_of_others(lib):
+    def fwd(out=FAR[0], sf=FAR[1], s0=FAR[2], lg=FAR[3], q=FAR[4], ws=FAR[12], s=shape(), cu=None):
+        return lib.gdn_linear_forward(P(q), P(FAR[5]), P(FAR[6]), P(lg), P(s0), P(cu), 1.0, P(out),
+                                      P(sf), P(ws), 1 << 40, s, BF16, None)
+
+    def bwd(dq=FAR[0], dk=FAR[1], dv=FAR[2], ds0=FAR[3], do=FAR[4], ds=FAR[5], ws=FAR[12]):
+        return lib.gdn_linear_backward(P(FAR[6]), P(FAR[7]), P(FAR[8]), P(FAR[9]), P(FAR[10]), P(do),
+                                       P(ds), None, 1.0, P(dq), P(dk), P(dv), P(ds0), P(ws), 1 << 40,
+                                       shape(), BF16, None)
+
+    def dec(out=FAR[0], S=FAR[1], q=FAR[2], slots=FAR[4]):
+        return lib.gdn_linear_decode(P(q), P(FAR[5]), P(FAR[6]), P(FAR[7]), P(S), P(slots), 9, 1.0,
+                                     P(out), 2, 2, 4, 1, 128, BF16, None)
+    long = shape(T=65536, Hk=4)                        # its states take more than a megabyte
+    for kw in [dict(out=FAR[4] + 16), dict(out=FAR[6] - 16), dict(sf=FAR[2] + 65536),
+               dict(out=FAR[1] - 256), dict(sf=FAR[3] - 16), dict(s=long, ws=FAR[1] - 65536),
+               dict(s=shape(nseq=3), cu=FAR[0] + 64)]:
+        assert shares(lib, fwd(**kw)), kw
+    for kw in [dict(dq=FAR[6] + 16), dict(dk=FAR[0] + 1024), dict(dv=FAR[4] - 16),
+               dict(ds0=FAR[5] + 65536), dict(ws=FAR[8] - 65536), dict(ws=FAR[1])]:
+        assert shares(lib, bwd(**kw)), kw
+    # a pool of 9 x 4 states is 2.25 MiB
+    for kw in [dict(S=FAR[0] - (9 << 18) + 16), dict(out=FAR[2] + 16), dict(S=FAR[4] - 65536)]:
+        assert shares(lib, dec(**kw)), kw
+
+
+def test_norm_outputs_on_parts_of_others(lib):
+    """[2, 4, 384] bf16 rows: 6 KiB each; Y is [2, 3, 4, 128]."""
+    s = st(1536, 512, 128)
+
+    def fwd(y=FAR[0], z=FAR[1], wo=FAR[2], r=FAR[3], wi=FAR[4], X=FAR[5], N=FAR[6]):
+        return lib.gdn_block_norm(P(y), s, P(z), P(wo), P(r), P(wi), 1.0, 1e-6, 1, P(X), P(N), 2, 4, 3,
+                                  128, BF16, None)
+
+    def bwd(dX=FAR[7], dN=FAR[8], dy=FAR[9], dz=FAR[10], dr=FAR[11], dwo=FAR[12], dwi=FAR[13],
+            ws=FAR[14]):
+        return lib.gdn_block_norm_backward(P(FAR[0]), s, P(FAR[1]), P(FAR[2]), P(FAR[3]), P(FAR[4]),
+                                           P(dX), P(dN), 1.0, 1e-6, 1, P(dy), s, P(dz), P(dr), P(dwo),
+                                           P(dwi), P(ws), 1 << 40, 2, 4, 3, 128, BF16, None)
+    for kw in [dict(X=FAR[0] + 16), dict(X=FAR[3] + 768), dict(r=FAR[5] + 16), dict(N=FAR[5] + 768),
+               dict(N=FAR[1] - 16), dict(X=FAR[2] - 16), dict(N=FAR[4] + 512)]:
+        assert shares(lib, fwd(**kw)), kw
+    for kw in [dict(dy=FAR[0] + 256), dict(dz=FAR[1] + 16), dict(dr=FAR[7] + 768), dict(dy=FAR[7] - 16),
+               dict(dwo=FAR[13] - 512), dict(dr=FAR[9] + 16), dict(ws=FAR[12] - 512),
+               dict(dz=FAR[8] + 6128), dict(dwi=FAR[4] + 16)]:
+        assert shares(lib, bwd(**kw)), kw
+
+
 # ---- the binding ----
 def test_binding_refuses_what_the_library_cannot_see(lib):
     x = torch.zeros(1, 2, 4, 128, dtype=torch.bfloat16)

@@ -1007,3 +1007,44 @@ def test_linear_expired_wait_reports_and_the_next_call_is_clean(lib, T, lens, ke
     got = run()
     assert gdn.gdn_get_status() == gdn.GDN_OK
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# --------------------------------------------------------------------------- #
+# outputs beside inputs in one buffer
+# --------------------------------------------------------------------------- #
+def test_views_of_one_buffer_that_share_no_memory(lib):
+    """Layouts that interleave outputs and inputs in one allocation are taken, and
+    overlapping views of the same buffers are refused with nothing written."""
+    g = gen(90)
+    B, T, H = 2, 37, 3
+    inv = gdn.gdn_rotary_frequencies(64)[0].cuda()
+    pos = torch.arange(T).expand(B, T).contiguous().cuda()
+    x = rand(g, B, T, 4 * H, 128, dtype="bf16")        # q, k and room for both
+    view = lambda i: x[:, :, i * H:(i + 1) * H].transpose(1, 2)
+    want = [torch.empty(B, H, T, 128, dtype=x.dtype, device="cuda") for _ in range(2)]
+    gdn.gdn_rotary(view(0), view(1), pos, inv, *want)
+    gdn.gdn_rotary(view(0), view(1), pos, inv, view(2), view(3))
+    assert torch.equal(view(2), want[0]) and torch.equal(view(3), want[1])
+    y = torch.empty(B, H, 2 * T, 128, dtype=x.dtype, device="cuda")
+    y[:, :, ::2] = view(0)                             # rows between the output's
+    gdn.gdn_rotary(y[:, :, ::2], None, pos, inv, y[:, :, 1::2], None)
+    assert torch.equal(y[:, :, 1::2], want[0])
+    gdn.gdn_rotary(view(0), view(1), pos, inv, view(0), view(1))
+    assert torch.equal(view(0), want[0]) and torch.equal(view(1), want[1])
+    keep = x.clone()
+    for qo, ko in ((x[:, :, 1:1 + H].transpose(1, 2), view(3)), (view(2), x[:, :, 5:8].transpose(1, 2)),
+                   (view(2), view(1)[:, :, 1:])):
+        q, k, p = (t[:, :, :ko.shape[2]] for t in (view(0), view(1), pos[:, None]))
+        with pytest.raises(gdn.GdnError, match="shares memory"):
+            gdn.gdn_rotary(q, k, p[:, 0].contiguous(), inv, qo[:, :, :ko.shape[2]], ko)
+    assert torch.equal(x, keep)
+    # a norm's output in the other half of its input's rows, then half a row too early
+    buf = rand(g, 8, 2, 1, 256)
+    X = torch.empty(8, 1, 256, device="cuda")
+    w = rand(g, 256)
+    gdn.gdn_block_norm(buf[:, :1], None, w, None, None, X, None)
+    r = rand(g, 16, 1, 256)
+    for out in (r[1:9], r[:8].view(-1)[128:-128].view(7, 1, 256)):
+        n = out.shape[0]
+        with pytest.raises(gdn.GdnError, match="shares memory"):
+            gdn.gdn_block_norm(buf[:n, :1], None, w, r[:n], None, out, None)
