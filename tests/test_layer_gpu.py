@@ -1048,3 +1048,38 @@ def test_views_of_one_buffer_that_share_no_memory(lib):
         n = out.shape[0]
         with pytest.raises(gdn.GdnError, match="shares memory"):
             gdn.gdn_block_norm(buf[:n, :1], None, w, r[:n], None, out, None)
+
+
+# --------------------------------------------------------------------------- #
+# errors in the 2-norm, where the bounds by element are wide
+# --------------------------------------------------------------------------- #
+# A bf16 output passes two independent roundings, its own and that of its terms
+# (weights or state).  One spreads evenly over half a step, which is at most 2^-8
+# of a value: 2^-8 / sqrt 3 in the 2-norm, two of them 0.0032.  A quarter more
+# for the sampling.  A float32 output is a sum of at most 128 + 128 + 64 products
+# in order: sqrt(320 / 3), about ten half steps in quadrature; 16 are allowed.
+TOL2 = {"bf16": 1.25 * (2 / 3) ** 0.5 * UBF, "f32": 16 * U32}
+
+
+def near2(got, want, dtype, rows, name):
+    """By head and by 128 rows of a sequence, so that one lost boundary or one
+    wrong tile shows however long the call is."""
+    got = f64(got)
+    for b, a, n in rows:
+        for t in range(a, a + n, 128):
+            x, w = (v[b, :, t:min(t + 128, a + n)] for v in (got, want))
+            err = np.sqrt(((x - w) ** 2).sum((1, 2))) / np.sqrt((w ** 2).sum((1, 2)))
+            assert (err <= TOL2[dtype]).all(), (name, b, t, err)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,Hv,T,lens", SHAPES + [(1, 3, 3, 6400, None), (50, 3, 3, 390, None),
+                                                     (1, 3, 6, 3400, [3000, 260, 140])])
+def test_linear_relative_error(lib, dtype, B, Hk, Hv, T, lens):
+    c = linear_case(95 + T, dtype, B, Hk, Hv, T, lens, True)
+    if Hk == 3:                                        # what a row adds is seen to the end
+        c["lg"] = torch.tensor([-1e-3, -1e-5, 0.0, -1e-4, -1e-2, -2e-3][:Hv]).cuda()
+    O, _ = run_forward(c, 0.7)
+    near2(O, oracle_linear(c, 0.7)[0], dtype, c["rows"], "O")
+    for x, y, name in zip(run_backward(c, 0.7), oracle_linear_grad(c, 0.7)[:3], ("dQ", "dK", "dV")):
+        near2(x, y, dtype, c["rows"], name)
