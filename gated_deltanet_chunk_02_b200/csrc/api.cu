@@ -730,6 +730,8 @@ int gdn_linear_backward(const void* Q, const void* K, const void* V, const float
                         float* dS0, void* workspace, int64_t workspace_bytes, gdn_linear_shape s,
                         gdn_dtype dtype, void* stream) {
     GDN_TRY(check_linear(s, cu_seqlens, dtype));
+    if (s.B > 0 && s.Hk > 0 && s.Hv == 0)              // dQ and dK would be sums over nothing
+        return fail(GDN_ERR_ARG, "Hk=%lld without value heads", (long long)s.Hk);
     if (s.B == 0 || s.Hv == 0) return GDN_OK;
     if (s.T > 0)
         GDN_TRY(check_ptrs({{Q, "Q"}, {K, "K"}, {V, "V"}, {dO, "dO"}, {dQ, "dQ"}, {dK, "dK"},

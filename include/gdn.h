@@ -413,7 +413,7 @@ int64_t gdn_linear_forward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype);
  *   dQ, dK [B,Hk,T,d] (summed over the value heads that share them), dV
  *   [B,Hv,T,d] (dtype), dS0 [n,Hv,d,d] f32 (NULL to skip).
  * Nothing is saved by the forward call: the states are formed again.  Other
- * arguments as there; rows of no sequence stay as they were.
+ * arguments as there (Hv = 0 needs Hk = 0); rows of no sequence stay as they were.
  */
 int gdn_linear_backward(const void* Q, const void* K, const void* V, const float* loggate,
                         const float* S0, const void* dO, const float* dS_final,

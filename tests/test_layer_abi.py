@@ -133,6 +133,12 @@ def test_linear_more_heads_than_a_grid(lib):
             assert f(lib, s=s, cu=cu) == gdn.GDN_ERR_ARG and "too many" in last(lib)
 
 
+def test_linear_gradients_without_value_heads_are_refused(lib):
+    """dQ and dK [B, Hk, T, d] would be left unwritten."""
+    assert backward(lib, s=shape(Hk=2, Hv=0)) == gdn.GDN_ERR_ARG and "value heads" in last(lib)
+    assert forward(lib, s=shape(Hk=2, Hv=0)) == gdn.GDN_OK
+
+
 def test_linear_expiry_hook_arguments(lib):
     f = lib.gdn_debug_arm_linear_expiry
     for block, kernel, ms in [(-1, 0, 5.0), (0, 2, 5.0), (0, 0, 0.0), (0, 1, 2500.0),

@@ -1083,3 +1083,52 @@ def test_linear_relative_error(lib, dtype, B, Hk, Hv, T, lens):
     near2(O, oracle_linear(c, 0.7)[0], dtype, c["rows"], "O")
     for x, y, name in zip(run_backward(c, 0.7), oracle_linear_grad(c, 0.7)[:3], ("dQ", "dK", "dV")):
         near2(x, y, dtype, c["rows"], name)
+
+
+# --------------------------------------------------------------------------- #
+# offsets past 32 bits
+# --------------------------------------------------------------------------- #
+def test_offsets_past_32_bits(lib):
+    """More than 2^31 elements a tensor: the last rows and heads, and the last
+    states of a pool, are those of a small call on them."""
+    gd = torch.Generator(device="cuda")
+    gd.manual_seed(97)
+    rnd = lambda *s, dt=torch.bfloat16: torch.randn(*s, generator=gd, device="cuda", dtype=dt)
+    # rotary and a norm: 17 million rows of 128
+    T = (1 << 24) + 37
+    x = rnd(1, 1, T, 128)
+    pos = torch.arange(T, device="cuda")[None]
+    inv = gdn.gdn_rotary_frequencies(128)[0].cuda()
+    y, z = torch.empty_like(x), torch.empty(1, 1, 100, 128, dtype=x.dtype, device="cuda")
+    gdn.gdn_rotary(x, None, pos, inv, y, None)
+    gdn.gdn_rotary(x[:, :, -100:], None, pos[:, -100:].contiguous(), inv, z, None)
+    assert torch.equal(y[:, :, -100:], z)
+    w = rnd(128, dt=torch.float32)
+    rows = lambda t: t[0, 0][None, :, None]            # [1, T, 1, 128]
+    gdn.gdn_block_norm(rows(x), None, w, None, None, y[0], None)
+    gdn.gdn_block_norm(rows(x[:, :, -100:]), None, w, None, None, z[0], None)
+    assert torch.equal(y[0, :, -100:], z[0])
+    del x, y
+    # linear attention: 40 heads of 430000 rows
+    H, T = 40, 430000
+    K, V = rnd(1, 1, T, 128), rnd(1, H, T, 128)
+    lg = torch.full((H,), -0.01, device="cuda")
+    run = lambda v, o, g: gdn.gdn_linear_forward(
+        K, K, v, g, None, o, None, torch.empty(gdn.gdn_linear_forward_workspace_bytes(K, v),
+                                               dtype=torch.uint8, device="cuda"), scale=128 ** -0.5)
+    O, last = torch.empty_like(V), torch.empty_like(V[:, :1])
+    run(V, O, lg)
+    run(V[:, -1:].contiguous(), last, lg[-1:])
+    a, b = O[0, -1, -4096:].double(), last[0, 0, -4096:].double()
+    assert (a - b).norm() <= 2 ** 0.5 * TOL2["bf16"] * b.norm()
+    del V, O
+    # a pool of 70000 states
+    S = torch.zeros(70000, 1, 128, 128, device="cuda")
+    q = rnd(2, 1, 1, 128, dt=torch.float32)
+    S[[3, 69999]] = rnd(1, 128, 128, dt=torch.float32)
+    o = torch.empty_like(q)
+    at = torch.tensor([69999, 3], dtype=torch.int32, device="cuda")
+    gdn.gdn_linear_decode(q[[0, 0]].contiguous(), q[[1, 1]].contiguous(), q[[0, 0]].contiguous(),
+                          lg[:1], S, o, at)
+    assert torch.equal(o[0], o[1]) and torch.equal(S[3], S[69999])
+    assert int((S != 0).any(-1).any(-1).sum()) == 2
