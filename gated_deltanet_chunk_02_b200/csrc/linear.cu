@@ -106,26 +106,28 @@ __global__ void __launch_bounds__(kCombineThreads) k_lin_combine(const LinArgs p
 }
 
 // ---- gradients of shared heads: the sum over the value heads of a group ----
-// Is row t one of a sequence's?  By the whole warp.  Bisection finds it if all
-// bounds are in order; a row that it does not find is of no sequence, or the
-// bounds of others are bad and left out: all sequences are tried.
+// Is row t one of a sequence's?  By the whole warp, 32 starts at a look: the last
+// that is not behind t has it if all bounds are in order.  A row not found there
+// is of no sequence, or the bounds of others are bad and left out: all are tried.
 __device__ __forceinline__ bool lin_has_row(const LinArgs& p, int64_t t) {
+    const int lane = threadIdx.x & 31;
     const auto has = [&](int64_t s) {
         const int64_t lo = p.cu[s], hi = p.cu[s + 1];
         return lo >= 0 && lo <= t && t < hi && hi <= p.T;
     };
-    int64_t s = 0;                                     // the last one that starts at t or before
+    int64_t s = 0;
     for (int64_t n = p.nseq; n > 1;) {
-        const int64_t half = n >> 1;
-        if (p.cu[s + half] <= t) s += half;
-        n -= half;
+        const int64_t step = (n + 31) / 32, at = lane * step;
+        const uint32_t before = __ballot_sync(0xffffffffu, at < n && p.cu[s + at] <= t);
+        const int64_t skip = before ? (31 - __clz(before)) * step : 0;
+        s += skip;
+        n = n - skip < step ? n - skip : step;
     }
-    bool found = has(s);
-    for (int64_t s0 = 0; s0 < p.nseq && !found; s0 += 32) {
-        const int64_t i = s0 + (threadIdx.x & 31);
-        found = __any_sync(0xffffffffu, i < p.nseq && has(i));
-    }
-    return found;
+    if (has(s)) return true;
+    bool found = false;
+#pragma unroll 4
+    for (int64_t i = lane; i < p.nseq; i += 32) found |= has(i);
+    return __any_sync(0xffffffffu, found);
 }
 template <typename T>
 __global__ void __launch_bounds__(256)
