@@ -7,9 +7,10 @@
 // the gradient (the matrix is m times orthogonal).  Columns from rot on are
 // copied.
 //
-// The angle is reduced in binary64: pos * f_p / 2 pi loses about
-// 2^-53 * (turns), where a float32 product at position 10^6 would be off by
-// 0.06 rad.  Only the fraction of a turn goes on to float32.
+// The angle is reduced in binary64, pos * f_p and 1 / 2 pi as sums of two: one
+// product of one each would lose 2^-53 of the turns, 2e-4 rad at position 10^12
+// (a float32 product 0.06 rad at 10^6).  Only the fraction of a turn goes on to
+// float32.
 //
 // GPU mapping.  Bound by moving the rows: 16 lanes hold one row of 128 columns
 // (8 each), a CTA 16 tokens.  The angles of a token are the same for every
@@ -93,6 +94,14 @@ struct Row8<float> {
     }
 };
 
+// the fraction of a turn, within half of one, that pos * f radians leave
+__device__ __forceinline__ float turn_fraction(double pos, double f) {
+    constexpr double hi = 0.15915494309189535, lo = -9.839338337591243e-18;   // 1 / 2 pi
+    const double a = pos * f, b = fma(pos, f, -a);
+    const double t = a * hi, u = fma(a, hi, -t) + fma(a, lo, b * hi);
+    return (float)((t - rint(t)) + u);
+}
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kRotTokens * 16, sizeof(T) == 2 && MODE != kHalfOdd ? 4 : 1)
 k_rotary(const RotaryArgs p) {
@@ -104,7 +113,7 @@ k_rotary(const RotaryArgs p) {
 
     // x'_c = x_c cs[c] + x_partner(c) sn[c]; columns from rot on: cs = 1, no partner
     float cs[8], sn[8];
-    const double turn = in ? (double)p.positions[n] * 0.15915494309189535 : 0.0;
+    const double pos = in ? (double)p.positions[n] : 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (MODE == kInterleaved && (i & 1)) continue;
@@ -112,9 +121,7 @@ k_rotary(const RotaryArgs p) {
         float co = 1.f, si = 0.f;
         if (c < p.rot) {
             const int pr = MODE == kInterleaved ? c / 2 : (c < half ? c : c - half);
-            double r = turn * (double)p.inv_freq[pr];
-            r -= rint(r);
-            sincospif(2.f * (float)r, &si, &co);
+            sincospif(2.f * turn_fraction(pos, (double)p.inv_freq[pr]), &si, &co);
             co *= p.mscale;
             si *= p.inverse ? -p.mscale : p.mscale;
         }

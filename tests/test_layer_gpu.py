@@ -1132,3 +1132,31 @@ def test_offsets_past_32_bits(lib):
                           lg[:1], S, o, at)
     assert torch.equal(o[0], o[1]) and torch.equal(S[3], S[69999])
     assert int((S != 0).any(-1).any(-1).sum()) == 2
+
+
+# --------------------------------------------------------------------------- #
+# positions as far as binary64 has them
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_far_positions(lib, dtype, inter):
+    """Angles of positions up to 2^53 against their exact remainders (60 digits):
+    the errors of near positions, no more."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    tau = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+    where = [0, 1, 12345, 10 ** 6, 2 ** 31 + 1, 10 ** 12, 2 ** 40 + 12345, 2 ** 52 + 1, 2 ** 53 - 1,
+             -(10 ** 12), -7]
+    T, half = len(where), 8
+    g = gen(98)
+    x = rand(g, 1, 1, T, 128, dtype=dtype)
+    inv = torch.tensor([1.0, 0.75, 0.1, 3e-2, 1e-3, 1e-4, 3.3e-6, 1e-7])
+    y = torch.empty_like(x)
+    gdn.gdn_rotary(x, None, torch.tensor([where]).cuda(), inv.cuda(), y, None, interleaved=inter)
+    left = np.array([[float(Decimal(p) * Decimal(float(f)) % tau) for f in inv] for p in where])
+    want = f64(x)[0, 0].copy()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+        c, s, xa, xb = np.cos(left[:, i]), np.sin(left[:, i]), f64(x)[0, 0, :, a], f64(x)[0, 0, :, b]
+        want[:, a], want[:, b] = xa * c - xb * s, xa * s + xb * c
+    near(y[0, 0], want, rotary_tol(f64(x)[0, 0], f64(inv), 1.0, inter, dtype), "far")
