@@ -21,6 +21,7 @@
 // Token t + 1's vectors load while token t computes.
 #include "common.cuh"
 #include "kernels.h"
+#include "linear.h"
 
 namespace gdn {
 namespace {
@@ -205,13 +206,15 @@ k_linear_decode(const T* __restrict__ Q, const T* __restrict__ K, const T* __res
     const T* kp = K + bk * n * kDh + 4 * sub;
     const T* vp = V + bh * n * kDh + row0;
     T* op = O + bh * n * kDh + row0;
-    const float a = expf(loggate[hv]);
+    const float lg = loggate[hv];
 
     float kn[kSeg], qn[kSeg], vn[R];
     ld16(kp, kn);
     ld16(qp, qn);
 #pragma unroll
     for (int r = 0; r < R; ++r) vn[r] = ld_elem(vp, r);
+    float a, al;                                       // behind the loads: it branches
+    lin_decay(lg, a, al);
     for (int t = 0; t < n; ++t) {
         float k[kSeg], q[kSeg], v[R];
 #pragma unroll
@@ -234,7 +237,7 @@ k_linear_decode(const T* __restrict__ Q, const T* __restrict__ K, const T* __res
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 p[r] += s[r][c] * q[c];
-                s[r][c] = a * s[r][c] + v[r] * k[c];
+                s[r][c] = fmaf(a, s[r][c], fmaf(al, s[r][c], v[r] * k[c]));
             }
         }
         kq = row_sum(kq);

@@ -782,6 +782,7 @@ __device__ void lt_short(const LinArgs& p, const LinProblem& q, const LinSeg& g,
     if (threadIdx.x >= 512) return;                    // 16 whole warps
     const int v = threadIdx.x >> 2, sub = threadIdx.x & 3, n = (int)g.n;
     const bool rev = q.reverse != 0;
+    const float lg = p.loggate[hv];
     float m[8][4];
     {
         const float* src = q.m0 ? q.m0 + (g.seq * p.Hv + hv) * kLinState : nullptr;
@@ -806,7 +807,9 @@ __device__ void lt_short(const LinArgs& p, const LinProblem& q, const LinSeg& g,
         (const __nv_bfloat16*)q.b + (int64_t)lt_row0(p, g, hv, q.gb) * kD + 4 * sub;
     const __nv_bfloat16* c = (const __nv_bfloat16*)q.c + (int64_t)lt_row0(p, g, hv, q.gc) * kD + v;
     const int64_t out = ((g.b * p.Hv + hv) * p.T + g.t0) * kD + v;
-    const float lam = lin_pow(lin_log2(p.loggate, hv), 1), before = rev ? 1.f : lam;
+    float lam, lam_lo;
+    lin_decay(lg, lam, lam_lo);
+    const float before = rev ? 1.f : lam, before_lo = rev ? 0.f : lam_lo;
     for (int t = 0; t < n; ++t) {
         const int64_t at = (int64_t)(rev ? n - 1 - t : t) * kD;
         const float w = q.s_state * __bfloat162float(c[at]);
@@ -818,9 +821,9 @@ __device__ void lt_short(const LinArgs& p, const LinProblem& q, const LinSeg& g,
             ld4(b + at + 16 * e, y);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                m[e][i] = fmaf(before, m[e][i], w * y[i]);
+                m[e][i] = fmaf(before, m[e][i], fmaf(before_lo, m[e][i], w * y[i]));
                 o = fmaf(m[e][i], x[i], o);
-                if (rev) m[e][i] *= lam;
+                if (rev) m[e][i] = fmaf(lam, m[e][i], lam_lo * m[e][i]);
             }
         }
         o += __shfl_xor_sync(0xffffffffu, o, 1);

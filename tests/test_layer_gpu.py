@@ -1160,3 +1160,32 @@ def test_rotary_far_positions(lib, dtype, inter):
         c, s, xa, xb = np.cos(left[:, i]), np.sin(left[:, i]), f64(x)[0, 0, :, a], f64(x)[0, 0, :, b]
         want[:, a], want[:, b] = xa * c - xb * s, xa * s + xb * c
     near(y[0, 0], want, rotary_tol(f64(x)[0, 0], f64(inv), 1.0, inter, dtype), "far")
+
+
+@pytest.mark.parametrize("how", ["one call", "calls of 8", "prompts of 8"])
+def test_linear_slow_decay_over_many_tokens(lib, how):
+    """16384 tokens one after the other: as over steps, one rounding per token to
+    the state in quadrature, where a decay rounded to a float is off by the same
+    2^-25.4 at each (1e-4 of the state in all)."""
+    T, n = 16384, 16384 if how == "one call" else 8
+    tries = -np.float32(1e-5) * (1 + np.arange(200, dtype=np.float32) / 128)
+    lam = np.exp(tries.astype(np.float64))
+    off = np.abs(lam.astype(np.float32).astype(np.float64) / lam - 1)
+    assert off.max() >= 2.0 ** -25.4
+    lg = torch.tensor([float(tries[off.argmax()])]).cuda()
+    g = gen(99)
+    dtype = "bf16" if how == "prompts of 8" else "f32"
+    K, V = rand(g, 1, 1, T, 128, dtype=dtype), rand(g, 1, 1, T, 128, dtype=dtype)
+    S, S2 = torch.zeros(1, 1, 128, 128, device="cuda"), torch.empty(1, 1, 128, 128, device="cuda")
+    O = torch.empty_like(V[:, :, :n])
+    for t in range(0, T, n):
+        k, v = K[:, :, t:t + n], V[:, :, t:t + n]
+        if how == "prompts of 8":
+            gdn.gdn_linear_forward(k, k, v, lg, S, O, S2, None)
+            S, S2 = S2, S
+        else:
+            gdn.gdn_linear_decode(k, k, v, lg, S, O)
+    w = torch.exp(lg[0].double() * torch.arange(T - 1, -1, -1, device="cuda"))
+    want = (V[0, 0].double() * w[:, None]).T @ K[0, 0].double()
+    err = float((S[0, 0].double() - want).norm() / want.norm())
+    assert err <= 2 * (T / 3) ** 0.5 * U32, err
