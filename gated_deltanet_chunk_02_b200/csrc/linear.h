@@ -298,7 +298,6 @@ __device__ __forceinline__ void lin_pow2(double lg, int64_t n, float& hi, float&
 // of one comes back at every token, 3e-4 of the state over 16384 of them.  Near
 // one the distance from one has float32's relative accuracy, which 1 / loggate
 // tokens turn into 2^-23 in all; a decay of e^-0.5 or faster forgets its rounding.
-// (In binary64, exp costs 2 us a call of four tokens.)
 __device__ __forceinline__ void lin_decay(float loggate, float& hi, float& lo) {
     if (fabsf(loggate) < 0.5f) {
         const float d = expm1f(loggate);

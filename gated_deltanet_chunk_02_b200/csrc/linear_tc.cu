@@ -42,9 +42,9 @@
 // k_linear_state_tc is step 1: the state part alone, always with three parts.
 //
 // One B200, bf16, graph replay: 65536 tokens of 16 heads in 9 segments a head:
-// state pass 110 us (4.9 TB/s), outputs 195 us (5.5 TB/s), 303 us together
-// (356 us in calls without a pause, where the power limit takes the clock from
-// 1965 to 1560 MHz); batch 4 of 16 heads x 4096 tokens backward 194 us.
+// state pass 110 us (4.9 TB/s), outputs 197 us (5.4 TB/s), 315 us together
+// (371 us in calls without a pause, where the power limit takes the clock from
+// 1965 to 1560 MHz); batch 4 of 16 heads x 4096 tokens backward 199 us (223).
 #include <cstddef>
 #include <cstring>
 

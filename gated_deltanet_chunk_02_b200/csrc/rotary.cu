@@ -16,7 +16,7 @@
 // (8 each), a CTA 16 tokens.  The angles of a token are the same for every
 // head, so a lane forms its 8 (4 if interleaved) sines and cosines once and
 // walks the heads with them, four rows in flight (64 registers, so that four
-// CTAs share an SM: 1 GB of bf16 in 192 us, 202 at three); heads are split over CTAs
+// CTAs share an SM: 1 GB of bf16 in 194 us, 202 at three); heads are split over CTAs
 // only when the tokens alone do not fill the GPU (one token per request).
 // The partner columns of the half layout come by shuffle from the lane that
 // holds them when rot is a multiple of 16, else by loads of the elements.

@@ -343,7 +343,8 @@ int gdn_decode(const void* Q, const void* K, const void* V, const float* beta,
  * (prompts, gradients, single tokens), and the norms around a block.  They
  * take the layouts of the calls above; small vectors (positions, frequencies,
  * log-decays, sequence bounds, slots) need the alignment of their elements
- * only.  Outputs may not share memory with inputs except where stated.
+ * only.  Outputs may not share memory with inputs or one another except where
+ * stated (GDN_ERR_ARG); views that interleave in one buffer share none.
  */
 
 /*
@@ -356,7 +357,9 @@ int gdn_decode(const void* Q, const void* K, const void* V, const float* beta,
  *   GDN_ROTARY_YARN    pairs that turn more than 32 times over
  *                      `original_length` tokens kept, those below 1 turn divided
  *                      by `factor`, linear in the turns between;
- *                      *mscale = 0.1 ln(factor) + 1.
+ *                      *mscale = 0.1 ln(factor) + 1.  (A model trained with a
+ *                      ramp over the pairs' indices between two borders, or with
+ *                      other borders, brings its own inv_freq.)
  * Both outputs are host pointers.  rot is even, 2 <= rot <= 128; factor >= 1.
  */
 int gdn_rotary_frequencies(float* inv_freq, float* mscale, int rot, double base, int scaling,
@@ -368,8 +371,8 @@ int gdn_rotary_frequencies(float* inv_freq, float* mscale, int rot, double base,
  *   a' = mscale (a cos - b sin),  b' = mscale (a sin + b cos),
  * pair i being columns (i, i + rot/2), or (2i, 2i + 1) if interleaved; columns
  * from rot on are copied.  inverse = 1 turns back by the same angle (times
- * mscale again): the gradient of the forward call.  Angles are formed in
- * binary64, so positions may be any that it holds.  In: Q [B,Hq,T,d], K
+ * mscale again): the gradient of the forward call.  Angles keep float32's
+ * accuracy at every position that binary64 holds (2^53).  In: Q [B,Hq,T,d], K
  * [B,Hk,T,d] (dtype, strided: a projection's [B,T,H,d] output serves as it is),
  * positions [B,T] int64, inv_freq [rot/2] f32.  Out: Q_out, K_out (dtype,
  * strided); each may be its input (same pointer and strides), else they share
@@ -395,11 +398,19 @@ int gdn_rotary(const void* Q, gdn_strides qs, void* Q_out, gdn_strides qos, cons
  * anything.  `workspace` holds gdn_linear_forward_workspace_bytes(s, dtype)
  * bytes (it may be 0; of the current device, fixed by shape and dtype); calls
  * that may overlap need one each.  A bound outside the rule sets the status
- * word (gdn_get_status returns GDN_ERR_ARG) and that sequence is left out.
+ * word (gdn_get_status returns GDN_ERR_ARG) and that sequence is left out: its
+ * rows stay as they were, its S_final is its S0.
  * bf16 data: products of bf16 on the tensor cores with fp32 accumulation; the
- * state is fp32 and returned to fp32 accuracy (its updates split into bf16
- * parts); weights and the state as an operand of o are rounded to bf16.
+ * state is fp32 and returned to fp32 accuracy (its updates split into three bf16
+ * parts; two, 2^-16, where it is not returned); weights and the state as an
+ * operand of o are rounded to bf16 (an error of o of 0.0024 in all, where its
+ * own rounding is 0.0017), and a state reaches a row with no less than 2^-60.
  * Sequences of up to 8 rows run in fp32.  f32 data: fp32 on CUDA cores.
+ * A NaN log-decay makes its head NaN.  An infinite or NaN value of V reaches o in
+ * its column from its row on, and the state, and nothing else (with bf16 data as
+ * a NaN beyond 8 rows); calls with such values take longer.
+ * Packed: every block reads all bounds, so that their cost grows with nseq^2;
+ * thousands of sequences of a few rows are better packed in several calls.
  */
 int gdn_linear_forward(const void* Q, const void* K, const void* V, const float* loggate,
                        const float* S0, const int32_t* cu_seqlens, float scale, void* O,
@@ -430,7 +441,8 @@ int64_t gdn_linear_backward_workspace_bytes(gdn_linear_shape s, gdn_dtype dtype)
  * int32 on the device; NULL: S[b]).  Out: O [B,Hv,n,d] (dtype).  A row with a
  * negative slot is left out (its O stays as it was).  So is one whose slot is
  * nslots or more, or the slot of an earlier row, and the status word is set
- * (gdn_get_status returns GDN_ERR_ARG).  d = 128, B <= 65535.
+ * (gdn_get_status returns GDN_ERR_ARG).  The decay's rounding costs 2^-23 of
+ * the state however many tokens it remembers.  d = 128, B <= 65535.
  */
 int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* loggate, float* S,
                       const int32_t* slots, int64_t nslots, float scale, void* O, int64_t B,
@@ -447,8 +459,9 @@ int gdn_linear_decode(const void* Q, const void* K, const void* V, const float* 
  * act(z) n), w_pre with N.  In: Y [B,H,T,d] (dtype, strided: the head-major
  * output of the attention calls, or H = 1 and [B,T,d]), Z, R [B,T,W] (dtype),
  * w_post, w_pre [W] f32.  Out: X [B,T,W] (dtype; NULL to skip if N is given; may
- * be R, no other argument), N [B,T,W] (dtype).  N is the norm of x before X's rounding.  d = 128,
- * or H = 1 and d a multiple of 8; W <= 16384; eps > 0.
+ * be R, no other argument), N [B,T,W] (dtype).  N is the norm of x before X's rounding.  Squares
+ * are summed in float32; gates are formed to |z| 2^-24 relative and stop at z = -87, where act(z)
+ * is below 1.5e-36.  d = 128, or H = 1 and d a multiple of 8; W <= 16384; eps > 0.
  */
 int gdn_block_norm(const void* Y, gdn_strides ys, const void* Z, const float* w_post,
                    const void* R, const float* w_pre, float scale, float eps, int act, void* X,
