@@ -1189,3 +1189,53 @@ def test_linear_slow_decay_over_many_tokens(lib, how):
     want = (V[0, 0].double() * w[:, None]).T @ K[0, 0].double()
     err = float((S[0, 0].double() - want).norm() / want.norm())
     assert err <= 2 * (T / 3) ** 0.5 * U32, err
+
+
+# --------------------------------------------------------------------------- #
+# gradients and tokens in a graph
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_and_tokens_captured_and_replayed(lib, dtype):
+    """Linear backward of shared heads, packed and cut, a norm's gradients and a
+    token step in one graph: on other inputs, and on inputs that hold NaN and
+    infinities, the bits of the calls themselves."""
+    def case(seed, odd=False):
+        c = linear_case(seed, dtype, 1, 2, 4, 2900, [2600, 0, 5, 250], True)
+        n = norm_case(seed, dtype, 2, 33, 4, 128, "zprnx")
+        n["pool"], n["token"] = rand(gen(seed), 4, 4, 128, 128), rand(gen(seed), 2, 4, 1, 128, dtype=dtype)
+        if odd:
+            c["V"][0, 0, 700, 3], c["Q"][0, 1, 1900, 5] = float("nan"), float("inf")
+            n["Z"][0, 3, 9] = torch.finfo(DT[dtype]).min
+        return c, n
+
+    def run(c, n):
+        Y = n["Y"]
+        new = lambda t: torch.full_like(t, 77.0)
+        dY, dZ, dR, dwo, dwi = new(Y), new(n["Z"]), new(n["R"]), new(n["wo"]), new(n["wi"])
+        ws = torch.empty(gdn.gdn_block_norm_backward_workspace_bytes(Y), dtype=torch.uint8,
+                         device="cuda")
+        gdn.gdn_block_norm_backward(Y, n["Z"], n["wo"], n["R"], n["wi"], n["dX"], n["dN"], dY, dZ, dR,
+                                    dwo, dwi, ws)
+        S, O = n["pool"].clone(), new(n["token"])
+        gdn.gdn_linear_decode(n["token"], n["token"], n["token"], c["lg"], S, O, slots)
+        return (*run_backward(c, 0.7), dY, dZ, dR, dwo, dwi, S, O)
+
+    slots = torch.tensor([3, 1], dtype=torch.int32).cuda()
+    sets = [case(110), case(111), case(112, odd=True)]
+    want = [run(*s) for s in sets]
+    c, n = case(110)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(c, n)
+    for (c2, n2), w in zip(sets, want):
+        for mine, other in ((c, c2), (n, n2)):
+            for x in mine:
+                if isinstance(mine[x], torch.Tensor):
+                    mine[x].copy_(other[x])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            a, b = a.contiguous(), b.contiguous()
+            assert torch.equal(a.isnan(), b.isnan())
+            assert torch.equal(a.nan_to_num(0.0), b.nan_to_num(0.0))
