@@ -1239,3 +1239,43 @@ def test_gradients_and_tokens_captured_and_replayed(lib, dtype):
             a, b = a.contiguous(), b.contiguous()
             assert torch.equal(a.isnan(), b.isnan())
             assert torch.equal(a.nan_to_num(0.0), b.nan_to_num(0.0))
+
+
+# --------------------------------------------------------------------------- #
+# behind the gated delta rule
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_block_norm_behind_the_gated_delta_rule(lib, dtype):
+    """The head norm, gate and residual on what gdn_forward and gdn_decode leave,
+    head-major as it lies: the oracle's values on the same outputs, the bits of a
+    token-major copy."""
+    from gated_deltanet_chunk_02_b200.inputs import Workload, make_decode_inputs, make_inputs
+    H, T = 3, 128
+    d = {k: v.cuda() for k, v in make_inputs(Workload(B=2, H=H, T=T, k=64, dtype=dtype), seed=5,
+                                             with_q=True).items()}
+    O = torch.empty_like(d["V"])
+    Sf = torch.empty(2, H, 128, 128, device="cuda")
+    ws = torch.empty(gdn.gdn_forward_workspace_bytes(d["K"], 64), dtype=torch.uint8, device="cuda")
+    gdn.gdn_forward(d["Q"], d["K"], d["V"], d["beta"], d["g"], None, 3, 1, 8, 0, O, Sf, ws)
+    t = {k: v.cuda() for k, v in make_decode_inputs(2, H, H, 1, dtype=dtype, seed=6).items()}
+    o = torch.empty_like(t["V"])
+    gdn.gdn_decode(t["Q"], t["K"], t["V"], t["beta"], t["loggate"], Sf, o)
+    g = gen(120)
+    wo, wi = rand(g, H * 128), rand(g, H * 128)
+    for Y in (O.transpose(1, 2), o.transpose(1, 2)):
+        B, n = Y.shape[:2]
+        z, r = (rand(g, B, n, H * 128, dtype=dtype) for _ in range(2))
+        out = []
+        for y in (Y, Y.contiguous()):
+            X, N = torch.empty_like(z), torch.empty_like(z)
+            gdn.gdn_block_norm(y, z, wo, r, wi, X, N, scale=0.5, eps=1e-5)
+            out.append((X, N))
+        assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+        row = lambda a: f64(a).reshape(B * n, H * 128)
+        x, want = L.block_norm(f64(Y).reshape(B * n, H, 128), row(z), f64(wo), row(r), f64(wi), 0.5,
+                               1e-5)
+        u, mag = half_step(dtype), np.abs(row(r)) + np.abs(x - row(r))
+        rms = np.sqrt((x * x).mean(-1, keepdims=True) + 1e-5)
+        near(X.view(B * n, -1), x, u * np.abs(x) + 64 * U32 * mag, "X")
+        near(N.view(B * n, -1), want,
+             u * np.abs(want) + 128 * U32 * np.abs(f64(wi)) * (mag / rms + np.abs(x) / rms), "N")
